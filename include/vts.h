@@ -335,6 +335,172 @@ int topk_page_table_transform(const void* scores, int32_t dtype, int64_t num_row
                               int32_t top_k, int32_t* out, int32_t* out_raw_indices,
                               void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Decode-step operators over a paged KV cache.
+ *
+ * The four calls below are what a decode step with drafted tokens does after
+ * the selection: attention of the drafted tokens, verification of them,
+ * attention weight accumulated per cached entry, and eviction by it.  They
+ * share one description of the cache.  A length counts the drafted tokens, as
+ * in vts_topk_varlen (next_n): of a request with length n and `draft` drafted
+ * tokens, positions [0, n - draft) are the prefix and position n - draft + i is
+ * drafted token i.  Lengths are clamped to [0, page_table_width * page_size].
+ *
+ * A page-table entry outside [0, num_pages) means that its positions are not
+ * there: they are skipped, whatever the length says.
+ *
+ * k, v       device, dtype (VTS_BF16 or VTS_F16), 16-byte aligned: num_pages
+ *            pages of page_size positions of kv_heads rows of head_dim (64 or
+ *            128) consecutive elements.
+ * k_strides, v_strides  elements between pages, positions of a page, and
+ *            heads, multiples of 8: any order of the three dimensions is
+ *            possible.  A cache spans at most 2^32 16-byte vectors.
+ * page_table device int32[batch, page_table_width], rows page_table_stride
+ *            entries apart.
+ * seq_lens   device int32[batch].
+ */
+typedef struct {
+    const void* k;
+    const void* v;
+    int64_t k_strides[3];
+    int64_t v_strides[3];
+    const int32_t* page_table;
+    int64_t page_table_stride;
+    int64_t page_table_width;
+    const int32_t* seq_lens;
+    int64_t num_pages;
+    int32_t page_size;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t batch;
+    int32_t dtype;
+} vts_paged_cache;
+
+/*
+ * vts_tree_attention -- attention of drafted tokens over the cache.
+ *
+ *   out[b, t, h] = sum_j p_j v_j,   p = softmax_j(scale * q[b, t, h] . k_j)
+ *   lse[b, t, h] = log sum_j exp(scale * q . k_j)
+ *
+ * over the places j that row (b, t) sees; query head h uses KV head
+ * h / (heads / kv_heads).  Without `slots` these are the prefix and the drafted
+ * tokens i with bit i of tree_mask[b, t] set (tree_mask NULL: i <= t, a chain).
+ * With `slots` they are the row's listed slots (page * page_size + position in
+ * the page, as vts_topk_page_table_transform writes them; slots outside the
+ * cache, such as the -1 of unused entries, are skipped) and, if tree_mask is
+ * given, the drafted tokens it names.  A row that sees nothing, or nothing of
+ * weight, gets zeros and an lse of -inf.  Values in places that a row does not
+ * see never reach it, infinities and NaN among them.
+ *
+ * q          device, the cache's dtype, 16-byte aligned; q_strides: elements
+ *            between requests, drafted tokens and heads, multiples of 8.
+ * draft      1..64 drafted tokens per request (1 for plain decoding).
+ * heads      a multiple of kv_heads, at most 8192.
+ * tree_mask  device int64[batch, draft] or NULL.
+ * slots      device int32[batch, draft, top_k] or NULL (then top_k is 0).
+ * out        device, dtype[batch, draft, heads, head_dim], 16-byte aligned.
+ * lse        device float[batch, draft, heads] or NULL.
+ * workspace  device, 16-byte aligned, at least
+ *            vts_tree_attention_workspace_bytes(...) bytes, zeroed once.  The
+ *            calls of this section leave their workspaces fit for each
+ *            other, of any shape, but not for the selections.
+ *
+ * Sums are 32-bit; the probabilities are rounded to dtype for the product with
+ * V.  The result depends on the shape and the lengths but not on timing.
+ * Work is shared in units of 128 places over the batch's real lengths, so
+ * ragged batches cost what their lengths say.
+ */
+size_t vts_tree_attention_workspace_bytes(int32_t draft, int32_t heads, int32_t kv_heads,
+                                          int32_t head_dim, int32_t top_k);
+int vts_tree_attention(const vts_paged_cache* cache, const void* q, const int64_t* q_strides,
+                       int32_t draft, int32_t heads, const int64_t* tree_mask,
+                       const int32_t* slots, int32_t top_k, float scale, void* out, float* lse,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * vts_attention_weight_add -- attention weight accumulated per cached entry:
+ *
+ *   weights[b, hk, j] += sum over t with row_keep[b, t] != 0 and the query
+ *       heads h of KV head hk of exp(scale * q[b, t, h] . k_j - lse[b, t, h])
+ *
+ * for every position j < width that row (b, t) sees (as vts_tree_attention
+ * without slots).  Rows whose lse is -inf add nothing.  cache->v is not read
+ * and may be NULL.  The sum over rows is in a fixed order.
+ *
+ * lse        device float[batch, draft, heads], of vts_tree_attention.
+ * row_keep   device uint8[batch, draft] or NULL (all rows): for instance the
+ *            drafted tokens that were accepted.
+ * weights    device float, `width` consecutive per request and KV head, at
+ *            the strides given (elements).
+ */
+int vts_attention_weight_add(const vts_paged_cache* cache, const void* q,
+                             const int64_t* q_strides, int32_t draft, int32_t heads,
+                             const int64_t* tree_mask, const float* lse, const uint8_t* row_keep,
+                             float scale, float* weights, int64_t weights_batch_stride,
+                             int64_t weights_head_stride, int64_t width, void* stream);
+
+/*
+ * vts_evict_cache -- shrinks every request to at most `keep` entries.
+ *
+ * Of a request's n entries (its length, at most `width`) and each KV head by
+ * itself: if n <= keep all stay; else the first `sinks`, the last `recent`, and
+ * the entries of largest weight among the others stay, keep in all; of
+ * equal weights the lower positions stay, and weights order as in
+ * vts_topk_varlen_ordered (-0 equals +0, a NaN ranks by its sign beyond the
+ * infinities).  The kept entries' K and V rows go, in the order of their
+ * positions, to the pages of out_page_table, which must not be pages that are
+ * read (k_out may be the cache itself, with fresh pages); their positions to
+ * kept[b, hk, 0..] (-1 in unused entries) and their weights to
+ * out_weights[b, hk, 0..] (0 in unused entries); min(n, keep) to out_lens[b].
+ * An entry whose page is not there is moved as zeros; a row whose out_page_table
+ * entry is outside [0, out_pages) is not written.
+ *
+ * sinks + recent <= keep; out_page_table_width >= ceil(keep / page_size).
+ */
+int vts_evict_cache(const vts_paged_cache* cache, const float* weights,
+                    int64_t weights_batch_stride, int64_t weights_head_stride, int64_t width,
+                    int32_t keep, int32_t sinks, int32_t recent, void* k_out,
+                    const int64_t* k_out_strides, void* v_out, const int64_t* v_out_strides,
+                    int64_t out_pages, const int32_t* out_page_table,
+                    int64_t out_page_table_stride, int64_t out_page_table_width, int32_t* kept,
+                    int32_t* out_lens, float* out_weights, void* stream);
+
+/*
+ * vts_verify_draft -- verification of drafted tokens against the target's
+ * probabilities from given random numbers; the accepted tokens and the next one
+ * are distributed as the target's own.
+ *
+ * Node t of a request is drafted token draft_tokens[b, t], hung from node
+ * parents[b, t] < t (-1: the context; parents NULL: a chain).  Row n + 1 of
+ * target_probs[b] is the target's distribution after node n (row 0: after the
+ * context), row n + 1 of draft_probs[b] the distribution that the children of
+ * node n were drawn from (never read for the last node, so `draft` rows).
+ * From the context on, a node's children are tried in index order: the child
+ * of token x is accepted if u q(x) < r(x), u = uniforms[b, t], where r begins
+ * as the target's row p and turns into max(r - q, 0), normalised, at each
+ * rejection.  draft_probs NULL: the tokens were chosen, not drawn, and q is 1
+ * at x and 0 elsewhere.  Where no child is accepted, the next token is the
+ * first v whose running sum of r passes uniforms[b, draft] times r's whole sum
+ * (if r has no mass, p's; if p has none, -1).
+ *
+ * Probabilities are used as they are given; NaN and negative values count as
+ * 0.  A token outside [0, vocab) or a parent outside [-1, t) makes a node that
+ * is never accepted.  Sums and comparisons are in 64 bits.
+ *
+ * path       device int32[batch, draft]: the accepted nodes in order, then -1.
+ * count      device int32[batch]: how many.
+ * next_token device int32[batch].
+ * workspace  as for vts_tree_attention, sized by
+ *            vts_verify_draft_workspace_bytes.
+ */
+size_t vts_verify_draft_workspace_bytes(int64_t batch, int64_t vocab);
+int vts_verify_draft(const void* target_probs, int32_t dtype, int64_t target_batch_stride,
+                     int64_t target_row_stride, const void* draft_probs,
+                     int64_t draft_batch_stride, int64_t draft_row_stride,
+                     const int32_t* draft_tokens, const int32_t* parents, const float* uniforms,
+                     int64_t batch, int32_t draft, int64_t vocab, int32_t* path, int32_t* count,
+                     int32_t* next_token, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Human-readable text of a vts_status. */
 const char* vts_status_string(int status);
 

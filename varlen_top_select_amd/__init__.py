@@ -14,6 +14,10 @@ Each has a deterministic mode (``tie_break="small"`` or ``"large"``; the
 ``topk_varlen_ordered`` entry point, or the ``tie_break`` argument of the
 transforms): a unique selection, in canonical order unless ``sort=False``.
 
+The operators of the rest of the decode step (attention of drafted tokens over a
+paged cache, accumulated attention weight, eviction, draft verification) are in
+``varlen_top_select_amd.decode`` and exported here too.
+
 The C entry points, their argument contracts and the page citations are in
 ``include/vts.h``.
 """
@@ -28,7 +32,9 @@ import torch
 __all__ = ["topk_varlen", "topk_varlen_noalloc", "topk_varlen_ordered", "topk_page_table_transform", "topk_transform_ragged",
            "topk_transform_page1",
            "workspace_bytes", "make_workspace",
-           "set_tuning", "workspace_stats", "VtsError", "library", "LIB_PATH"]
+           "set_tuning", "workspace_stats", "VtsError", "library", "LIB_PATH",
+           "tree_attention", "attention_weight_add", "evict_cache", "verify_draft",
+           "tree_mask_from_parents"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libvts.so")
@@ -95,6 +101,7 @@ def library():
     lib.vts_workspace_stats.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), i32, vp]
     lib.vts_set_tuning.restype = ctypes.c_int
     lib.vts_set_tuning.argtypes = [i32, i64]
+    decode.declare(lib)
     _lib = lib
     return lib
 
@@ -132,12 +139,13 @@ def make_workspace(num_rows: int, width: int, top_k: int, dtype: torch.dtype, de
     return ws
 
 
-# one zeroed workspace per (device, stream), grown on demand (the caller may pass its own)
+# one zeroed workspace per (device, stream) and kind of call, grown on demand
+# (the caller may pass its own)
 _WS_CACHE: dict = {}
 
 
-def _default_workspace(need: int, device, stream_ptr: int) -> torch.Tensor:
-    key = (device.index, stream_ptr)
+def _default_workspace(need: int, device, stream_ptr: int, kind: str = "select") -> torch.Tensor:
+    key = (device.index, stream_ptr, kind)
     ws = _WS_CACHE.get(key)
     if ws is None or ws.numel() < need:
         if torch.cuda.is_current_stream_capturing():
@@ -400,3 +408,8 @@ def workspace_stats(workspace: torch.Tensor, stream=None) -> list[int]:
     _check("vts_workspace_stats", library().vts_workspace_stats(
         workspace.data_ptr(), out, 4, _stream_ptr(stream, workspace.device)))
     return list(out)
+
+
+from . import decode  # noqa: E402  (uses the helpers above)
+from .decode import (attention_weight_add, evict_cache, tree_attention,  # noqa: E402
+                     tree_mask_from_parents, verify_draft)

@@ -7,11 +7,12 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libvts.so")
-# compiled separately and in parallel, linked in this order (the first two are
-# the kernels' code objects: any-order kernels, the deterministic mode, top_k
-# above 2048)
+# compiled separately and in parallel, linked in this order (first the
+# kernels' code objects: any-order selection, the deterministic mode, top_k
+# above 2048, the hint rung, the decode-step operators)
 SOURCES = ["vts_kernels.hip", "vts_kernels_ordered.hip", "vts_kernels_wide.hip",
-           "vts_kernels_hint.hip", "vts_api.hip"]
+           "vts_kernels_hint.hip", "vts_attend.hip", "vts_weigh.hip", "vts_evict.hip",
+           "vts_verify.hip", "vts_api.hip", "vts_decode_api.hip"]
 PROBE_LIB = os.path.join(HERE, "libvts_probe.so")
 PROBE_SOURCES = ["vts_probe.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -113,9 +113,11 @@ int check_workspace(void* ws, size_t bytes, int64_t num_rows, int64_t width, int
     return VTS_OK;
 }
 
+}  // namespace
+
 // The device that work on `stream` runs on (the current device for the null
 // stream), checked to be a gfx950, and its compute units; cached per device.
-int check_device(void* stream, int* dev_out = nullptr, int* cus_out = nullptr) {
+int vts::check_device(void* stream, int* dev_out, int* cus_out) {
     static std::mutex mu;
     static int known[64];  // 0 unknown, 1 gfx950, 2 other
     static int cus[64];
@@ -140,6 +142,8 @@ int check_device(void* stream, int* dev_out = nullptr, int* cus_out = nullptr) {
     if (cus_out) *cus_out = cus[dev];
     return known[dev] == 1 ? VTS_OK : VTS_ERR_UNSUPPORTED;
 }
+
+namespace {
 
 // Device scratch of vts_topk_varlen_noalloc, for callers that cannot
 // allocate: one array per device, held by the loaded library until the

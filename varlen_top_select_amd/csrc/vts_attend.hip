@@ -1,0 +1,546 @@
+// vts_attend.hip -- attention of drafted tokens over a paged KV cache.
+//
+//   o = sum_j p_j v_j,  p = softmax_j(scale * q . k_j)
+//
+// over the places a query row sees: the cached prefix (or a list of slots per
+// row) and the drafted tokens its mask names.  All query rows that share a KV
+// head and a list of places are taken together (drafted tokens x grouped
+// heads), so each K and V row is read once per 16 * MT of them.
+//
+// One pass: each wave walks its 32-place tiles with a running maximum m, sum l
+// and output O per query row (32-bit), and the waves, then the workgroups that
+// share a list, join theirs: O = sum_w 2^(m_w - m) O_w and the same for l.  The
+// maximum is only raised when a score passes it by more than 2^8, so that most
+// tiles need no exchange between lanes; p stays below 2^8 in either 16-bit
+// type and its relative rounding does not change.  p is rounded to the cache's
+// type for the second product (half a step, 2^-9 of bf16's p on average out
+// over the places); l sums the unrounded p.
+#include "vts_paged.hpp"
+
+namespace vts {
+
+template <int D, int MT>
+struct AttendShared {
+    float o[2][16 * MT][D];
+    float ml[WAVES][16 * MT][2];
+    int64_t scan[WAVES + 1];
+    int32_t found;
+    uint32_t last;
+};
+
+template <int DT, int D, int MT, bool SLOTS>
+struct Attend {
+    static constexpr int KS = D / 32;       // steps of the first product
+    static constexpr int VB = D / 16 * 2;   // bytes of a V row per lane
+    static constexpr int VW = VB / 4;       // words of a V row per lane
+    static constexpr int NTILE = D / 16;    // 16-row tiles of the second product
+    using VRow = typename std::conditional<D == 128, u32x4, u32x2>::type;
+
+    const AttendParams& p;
+    AttendShared<D, MT>& sm;
+    const int lane, wave, col, grp;
+    const uint32_t page_stride, pos_stride;  // of K in lanes 0..31, of V above
+    int32_t req, head_kv, mb, t0;  // t0: the row of a slot list
+    Places pl;
+    u32x4 q[MT][KS];
+    uint64_t bits[MT];
+    f32x4 o[MT][NTILE];
+    float m[MT], l[MT];
+    u32x4 k[2][KS];
+    VRow v[8];
+    const void* kbase;
+    const void* vbase;
+
+    __device__ Attend(const AttendParams& p_, AttendShared<D, MT>& s_, int32_t mb_)
+        : p(p_), sm(s_), lane(lane_id()), wave(threadIdx.x >> 6), col(lane & 15), grp(lane >> 4),
+          page_stride(lane < 32 ? p_.c.k.page_stride : p_.c.v.page_stride),
+          pos_stride(lane < 32 ? p_.c.k.pos_stride : p_.c.v.pos_stride), mb(mb_) {}
+
+    // row m of the block: the drafted token and the query head
+    __device__ __forceinline__ bool row_of(int r, int32_t& t, int32_t& head) const {
+        const int32_t row = mb * 16 * MT + r;
+        if (SLOTS) {
+            t = t0;
+            head = head_kv * p.c.group + row;
+        } else {
+            t = row / p.c.group;
+            head = head_kv * p.c.group + (row - t * p.c.group);
+        }
+        return row < p.rows;
+    }
+
+    __device__ __forceinline__ void begin(int32_t b, int32_t h) {
+        head_kv = h;
+        const PagedParams& c = p.c;
+        if (SLOTS) {
+            req = b / c.draft;
+            t0 = b - req * c.draft;
+            pl.slots = p.slots + (int64_t)b * p.top_k;
+        } else {
+            req = b;
+            t0 = 0;
+            pl.slots = nullptr;
+        }
+        const int32_t n = clamped_len(c, req);
+        pl.table = c.table + (int64_t)req * c.table_stride;
+        pl.top_k = p.top_k;
+        pl.draft_pos = n - c.draft;
+        pl.first = SLOTS ? p.top_k : n - c.draft;
+        pl.count = place_count<SLOTS>(p, n);
+        kbase = (const char*)c.k.base + (((uint64_t)h * c.k.head_stride) << 4);
+        vbase = (const char*)c.v.base + (((uint64_t)h * c.v.head_stride) << 4);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            int32_t t, head;
+            const bool ok = row_of(mt * 16 + col, t, head);
+            const char* at = (const char*)p.q +
+                             2 * (req * p.q_batch + (ok ? t * p.q_row + head * p.q_head : 0));
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                const u32x4 z = {0, 0, 0, 0};
+                q[mt][s] = ok ? gload((const u32x4*)(at + s * 64 + grp * 16)) : z;
+            }
+            uint64_t w = 0;
+            if (ok) {
+                if (p.tree_mask)
+                    w = (uint64_t)gload(p.tree_mask + (int64_t)req * c.draft + t);
+                else
+                    w = t >= 63 ? ~0ull : (2ull << t) - 1;
+            }
+            bits[mt] = w;
+            m[mt] = NEG_INF;
+            l[mt] = 0;
+#pragma unroll
+            for (int n2 = 0; n2 < NTILE; ++n2) o[mt][n2] = f32x4{0, 0, 0, 0};
+        }
+    }
+
+    __device__ __forceinline__ Entry issue(int32_t u) const {
+        return issue_entry<SLOTS>(p.c, pl, u * UNIT + wave * 32 + (lane & 31));
+    }
+    // K offsets in lanes 0..31, V offsets in lanes 32..63
+    __device__ __forceinline__ uint32_t resolve(const Entry& e) const {
+        return resolve_entry<SLOTS>(p.c, page_stride, pos_stride, e);
+    }
+    __device__ __forceinline__ void load_k(uint32_t off) {
+        const uint32_t safe = off == NO_PLACE ? 0 : off;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t r = from_lane(safe, h * 16 + col);
+#pragma unroll
+            for (int s = 0; s < KS; ++s) k[h][s] = row_load<u32x4>(kbase, r, s * 64 + grp * 16);
+        }
+    }
+    // register j: place 4 * grp + j of the first half, or of the second for j >= 4
+    __device__ __forceinline__ int v_place(int j) const {
+        return (j >> 2) * 16 + grp * 4 + (j & 3);
+    }
+    __device__ __forceinline__ void load_v(uint32_t off) {
+        const uint32_t safe = off == NO_PLACE ? 0 : off;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = row_load<VRow>(vbase, from_lane(safe, 32 + v_place(j)), col * VB);
+    }
+
+    // The tile's share of O: V rows turned so that each lane holds eight places
+    // of one V column, two of them to a word.
+    __device__ __forceinline__ void second_product(const u32x4 (&pv)[MT]) {
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+            u32x4 lo, hi;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                lo[j] = __builtin_amdgcn_perm(v[2 * j + 1][w], v[2 * j][w], 0x05040100u);
+                hi[j] = __builtin_amdgcn_perm(v[2 * j + 1][w], v[2 * j][w], 0x07060302u);
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                o[mt][2 * w] = mfma<DT>(lo, pv[mt], o[mt][2 * w]);
+                o[mt][2 * w + 1] = mfma<DT>(hi, pv[mt], o[mt][2 * w + 1]);
+            }
+        }
+    }
+
+    // Places whose V row holds an infinity or NaN, where not every row sees
+    // every place: 0 * inf would reach rows that do not see them.  Their V
+    // registers are cleared here and their share is added by add_rows.
+    __device__ __forceinline__ uint32_t clear_not_finite() {
+        uint32_t bad = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            bool f = false;
+#pragma unroll
+            for (int w = 0; w < VW; ++w) f = f || not_finite<DT>(v[j][w]);
+            const uint64_t any = ballot(f);
+            if (any == 0) continue;
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                if ((any >> (16 * g)) & 0xFFFFu) bad |= 1u << ((j >> 2) * 16 + g * 4 + (j & 3));
+            if ((any >> (16 * grp)) & 0xFFFFu)
+#pragma unroll
+                for (int w = 0; w < VW; ++w) v[j][w] = 0;
+        }
+        return bad;
+    }
+    __device__ __forceinline__ void add_rows(uint32_t bad, uint32_t off, int32_t j0,
+                                             const float (&pr)[MT][8]) {
+#pragma unroll 1
+        while (bad) {
+            const int kk = __builtin_ctz(bad);
+            bad &= bad - 1;
+            const uint32_t r = from_lane(off, 32 + kk);
+            VRow x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = row_load<VRow>(vbase, r, (grp * 4 + e) * VB);
+            const int src = ((kk & 15) >> 2) * 16 + col;
+            const int idx = (kk >> 4) * 4 + (kk & 3);
+            const int32_t i = j0 + kk - pl.first;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                float w = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w = e == idx ? pr[mt][e] : w;
+                w = __builtin_bit_cast(float, from_lane(__builtin_bit_cast(uint32_t, w), src));
+                const bool see = i < 0 || ((bits[mt] >> (i & 63)) & 1);
+#pragma unroll
+                for (int n = 0; n < NTILE; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t raw = (x[e][n >> 1] >> (16 * (n & 1))) & 0xFFFFu;
+                        const float y = o[mt][n][e] + w * to_float<DT>(raw);
+                        o[mt][n][e] = see ? y : o[mt][n][e];
+                    }
+            }
+        }
+    }
+
+    // One tile: its scores' softmax against the running state, and its share of
+    // O.  MASKED: some place is missing, or some row does not see some place.
+    template <bool MASKED>
+    __device__ __forceinline__ void tile(f32x4 (&s)[MT][2], uint32_t have, bool drafted,
+                                         uint32_t off, int32_t j0) {
+        const float c = p.scale_log2e;
+        float pr[MT][8];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            float top = NEG_INF;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float x = s[mt][e >> 2][e & 3] * c;
+                if constexpr (MASKED) {
+                    const int kk = v_place(e);
+                    const int32_t i = j0 + kk - pl.first;
+                    const bool see = ((have >> kk) & 1u) &&
+                                     (i < 0 || (i < MAX_DRAFT && ((bits[mt] >> (i & 63)) & 1)));
+                    x = see ? x : NEG_INF;
+                }
+                pr[mt][e] = x;
+                top = fmaxf(top, x);
+            }
+            if (ballot(top > m[mt] + 8.0f)) {
+                top = fmaxf(top, __shfl_xor(top, 16));
+                top = fmaxf(top, __shfl_xor(top, 32));
+                const float up = fmaxf(top, m[mt]);
+                const float f = up == NEG_INF ? 1.0f : exp2f(m[mt] - up);
+                m[mt] = up;
+                l[mt] *= f;
+#pragma unroll
+                for (int n = 0; n < NTILE; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[mt][n][e] *= f;
+            }
+            const float base = m[mt] == NEG_INF ? 0.0f : m[mt];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                pr[mt][e] = __builtin_amdgcn_exp2f(pr[mt][e] - base);
+                l[mt] += pr[mt][e];
+            }
+        }
+        uint32_t bad = 0;
+        if constexpr (MASKED) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const bool there = (have >> v_place(j)) & 1u;
+#pragma unroll
+                for (int w = 0; w < VW; ++w) v[j][w] = there ? v[j][w] : 0;
+            }
+            if (drafted) bad = clear_not_finite();
+        }
+        u32x4 pv[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) pv[mt][e] = pack2<DT>(pr[mt][2 * e], pr[mt][2 * e + 1]);
+        second_product(pv);
+        if constexpr (MASKED)
+            if (bad) add_rows(bad, off, j0, pr);
+    }
+
+    // Units [u0, u1) of the places, this wave's 32 of each 128.  The next
+    // tile's K rows are asked for as soon as this tile's are used up, and its V
+    // rows after the second product, so one of the two is always on its way.
+    __device__ __forceinline__ void walk(int32_t u0, int32_t u1) {
+        uint32_t off = resolve(issue(u0));
+        Entry next = issue(u0 + 1);
+        load_k(off);
+        load_v(off);
+#pragma unroll 1
+        for (int32_t u = u0; u < u1; ++u) {
+            const int32_t j0 = u * UNIT + wave * 32;
+            const bool more = u + 1 < u1;
+            const uint32_t off_next = resolve(next);
+            next = issue(u + 2);
+            f32x4 s[MT][2];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) acc = mfma<DT>(k[h][ks], q[mt][ks], acc);
+                    s[mt][h] = acc;
+                }
+            if (more) load_k(off_next);
+            const uint32_t have = (uint32_t)ballot(off != NO_PLACE);
+            const bool drafted = j0 + 31 >= pl.first;
+            if (have == ~0u && !drafted)
+                tile<false>(s, have, false, off, j0);
+            else
+                tile<true>(s, have, drafted, off, j0);
+            if (more) load_v(off_next);
+            off = off_next;
+        }
+    }
+
+    // o[.] += the rows that another wave left in LDS
+    __device__ __forceinline__ void put(int slot) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int n = 0; n < NTILE; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    sm.o[slot][mt * 16 + col][(grp * 4 + e) * NTILE + n] = o[mt][n][e];
+    }
+    __device__ __forceinline__ void take(int slot) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int n = 0; n < NTILE; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[mt][n][e] += sm.o[slot][mt * 16 + col][(grp * 4 + e) * NTILE + n];
+    }
+
+    // Joins the four waves; the block's rows are then in sm.o[0], sm.ml[0].
+    __device__ __forceinline__ void join_waves() {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            l[mt] += __shfl_xor(l[mt], 16);
+            l[mt] += __shfl_xor(l[mt], 32);
+            if (grp == 0) {
+                sm.ml[wave][mt * 16 + col][0] = m[mt];
+                sm.ml[wave][mt * 16 + col][1] = l[mt];
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            float top = NEG_INF, sum = 0;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) top = fmaxf(top, sm.ml[w][mt * 16 + col][0]);
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w)
+                sum += sm.ml[w][mt * 16 + col][1] * scale_to(sm.ml[w][mt * 16 + col][0], top);
+            const float f = scale_to(m[mt], top);
+            m[mt] = top;
+            l[mt] = sum;
+#pragma unroll
+            for (int n = 0; n < NTILE; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[mt][n][e] *= f;
+        }
+        if (wave >= 2) put(wave - 2);
+        __syncthreads();
+        if (wave < 2) take(wave);
+        __syncthreads();
+        if (wave == 1) put(1);
+        __syncthreads();
+        if (wave == 0) {
+            take(1);
+            put(0);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                if (grp == 0) {
+                    sm.ml[0][mt * 16 + col][0] = m[mt];
+                    sm.ml[0][mt * 16 + col][1] = l[mt];
+                }
+        }
+        __syncthreads();
+    }
+    // 2^(m - top), 1 where nothing has been seen
+    static __device__ __forceinline__ float scale_to(float from, float top) {
+        return top == NEG_INF ? 1.0f : exp2f(from - top);
+    }
+
+    // Normalises four outputs of row r and writes them, and its lse.
+    __device__ __forceinline__ void write_row(int r, int d, f32x4 x, float top, float sum) const {
+        int32_t t, head;
+        if (!row_of(r, t, head)) return;
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const int64_t at = ((int64_t)req * p.c.draft + t) * p.c.heads + head;
+        u32x2 w;
+        w[0] = pack2<DT>(x[0] * inv, x[1] * inv);
+        w[1] = pack2<DT>(x[2] * inv, x[3] * inv);
+        gstore((u32x2*)((char*)p.out + 2 * (at * D + d)), w);
+        if (d == 0 && p.lse)
+            gstore(p.lse + at, sum == 0.0f ? NEG_INF : (top + log2f(sum)) * 0.6931471805599453f);
+    }
+
+    __device__ __forceinline__ void finish_whole() {
+        join_waves();
+        for (int x = threadIdx.x * 4; x < 16 * MT * D; x += NT * 4) {
+            const int r = x / D, d = x % D;
+            write_row(r, d, *(const f32x4*)&sm.o[0][r][d], sm.ml[0][r][0], sm.ml[0][r][1]);
+        }
+        __syncthreads();
+    }
+
+    // A share of the places: leaves the block's rows in slot `mine`; the
+    // last of the workers [w0, w1] to arrive joins all, in their order.
+    __device__ __forceinline__ void finish_part(int64_t mine, int32_t w0, int32_t w1,
+                                                bool w0_whole_start) {
+        join_waves();
+        float* po = p.part_o + mine * (16 * MT * D);
+        float* pm = p.part_ml + mine * (16 * MT * 2);
+        for (int x = threadIdx.x * 4; x < 16 * MT * D; x += NT * 4)
+            gstore((f32x4*)(po + x), *(const f32x4*)(&sm.o[0][0][0] + x));
+        if (threadIdx.x < 16 * MT * 2) gstore(pm + threadIdx.x, (&sm.ml[0][0][0])[threadIdx.x]);
+        // every wave's stores are complete before the barrier; thread 0's
+        // release fence then covers the workgroup's
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+            uint32_t* ticket = p.tickets + (int64_t)mb * p.workers + w0;
+            const uint32_t old = __hip_atomic_fetch_add((VTS_GLOBAL uint32_t*)ticket, 1u,
+                                                        __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            const bool last = old == (uint32_t)(w1 - w0);
+            if (last) {
+                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+                gstore(ticket, 0u);  // self-restoring
+            }
+            sm.last = last;
+        }
+        __syncthreads();
+        if (sm.last) {
+            for (int x = threadIdx.x * 4; x < 16 * MT * D; x += NT * 4) {
+                const int r = x / D;
+                float top = NEG_INF, sum = 0;
+                for (int32_t w = w0; w <= w1; ++w)
+                    top = fmaxf(top, gload(p.part_ml + part(w, w0, w0_whole_start) * (16 * MT * 2) +
+                                           r * 2));
+                f32x4 acc = {0, 0, 0, 0};
+                for (int32_t w = w0; w <= w1; ++w) {
+                    const int64_t at = part(w, w0, w0_whole_start);
+                    const float f =
+                        scale_to(gload(p.part_ml + at * (16 * MT * 2) + r * 2), top);
+                    sum += f * gload(p.part_ml + at * (16 * MT * 2) + r * 2 + 1);
+                    const f32x4 x4 = gload((const f32x4*)(p.part_o + at * (16 * MT * D) + x));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[e] += f * x4[e];
+                }
+                write_row(r, x % D, acc, top, sum);
+            }
+        }
+        __syncthreads();
+    }
+    // A worker's slot: its first segment's, or the one of a list that begins
+    // inside its share.
+    __device__ __forceinline__ int64_t part(int32_t w, int32_t w0, bool w0_whole_start) const {
+        return 2 * ((int64_t)mb * p.workers + w) + (w == w0 && !w0_whole_start ? 1 : 0);
+    }
+};
+
+template <int DT, int D, int MT, bool SLOTS>
+__global__ __launch_bounds__(NT, MT == 4 ? 1 : 2) void attend_kernel(AttendParams p) {
+    __shared__ AttendShared<D, MT> sm;
+    // the row blocks of one share run next to each other on one XCD
+    const int32_t per = 8 * p.row_blocks;
+    const int32_t w = (int32_t)(blockIdx.x / per) * 8 + (int32_t)(blockIdx.x & 7);
+    const int32_t mb = (int32_t)(blockIdx.x % per) >> 3;
+    if (w >= p.workers) return;
+    Share sh;
+    if constexpr (SLOTS) {
+        const int32_t each = units_of(place_count<true>(p, 0)) * p.c.kv_heads;
+        sh.total = (int64_t)p.c.batch * p.c.draft * each;
+        sh.workers = sh.total < p.workers ? (int32_t)sh.total : p.workers;
+        if (w >= sh.workers) return;
+        sh.begin = share_start(sh.total, sh.workers, w);
+        sh.end = share_start(sh.total, sh.workers, w + 1);
+        sh.b = (int32_t)(sh.begin / each);
+        sh.b_unit = (int64_t)sh.b * each;
+    } else {
+        sh = dense_share(p.c, p.workers, w, sm.scan, &sm.found);
+        if (w >= sh.workers) return;
+    }
+    Attend<DT, D, MT, SLOTS> a(p, sm, mb);
+    int64_t x = sh.begin;
+    int32_t b = sh.b;
+    int64_t b_unit = sh.b_unit;
+    while (x < sh.end) {
+        const int32_t units =
+            SLOTS ? units_of(place_count<true>(p, 0)) : units_of(clamped_len(p.c, b));
+        const int32_t h = (int32_t)((x - b_unit) / units);
+        const int64_t g0 = b_unit + (int64_t)h * units, g1 = g0 + units;
+        const int64_t x1 = g1 < sh.end ? g1 : sh.end;
+        a.begin(b, h);
+        a.walk((int32_t)(x - g0), (int32_t)(x1 - g0));
+        if (x == g0 && x1 == g1) {
+            a.finish_whole();
+        } else {
+            const int32_t w0 = share_of(sh.total, sh.workers, g0);
+            const int32_t w1 = share_of(sh.total, sh.workers, g1 - 1);
+            const bool whole_start = share_start(sh.total, sh.workers, w0) == g0;
+            a.finish_part(a.part(w, w0, whole_start), w0, w1, whole_start);
+        }
+        x = x1;
+        if (h + 1 == p.c.kv_heads && x1 == g1) {
+            b_unit = g1;
+            ++b;
+        }
+    }
+}
+
+template <int DT, int D, bool SLOTS>
+static hipError_t launch_mt(int mt, const AttendParams& p, hipStream_t stream) {
+    const uint32_t grid = (uint32_t)((p.workers + 7) / 8 * 8 * p.row_blocks);
+    switch (mt) {
+        case 1:
+            hipLaunchKernelGGL((attend_kernel<DT, D, 1, SLOTS>), dim3(grid), dim3(NT), 0, stream, p);
+            break;
+        case 2:
+            hipLaunchKernelGGL((attend_kernel<DT, D, 2, SLOTS>), dim3(grid), dim3(NT), 0, stream, p);
+            break;
+        default:
+            hipLaunchKernelGGL((attend_kernel<DT, D, 4, SLOTS>), dim3(grid), dim3(NT), 0, stream, p);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_attend(int dtype, int head_dim, int mt, const AttendParams& p,
+                         hipStream_t stream) {
+    if (dtype == BF16) {
+        if (head_dim == 64)
+            return p.slots ? launch_mt<BF16, 64, true>(mt, p, stream)
+                           : launch_mt<BF16, 64, false>(mt, p, stream);
+        return p.slots ? launch_mt<BF16, 128, true>(mt, p, stream)
+                       : launch_mt<BF16, 128, false>(mt, p, stream);
+    }
+    if (head_dim == 64)
+        return p.slots ? launch_mt<F16, 64, true>(mt, p, stream)
+                       : launch_mt<F16, 64, false>(mt, p, stream);
+    return p.slots ? launch_mt<F16, 128, true>(mt, p, stream)
+                   : launch_mt<F16, 128, false>(mt, p, stream);
+}
+
+}  // namespace vts

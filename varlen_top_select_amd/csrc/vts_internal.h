@@ -128,6 +128,8 @@ hipError_t launch_varlen_ordered(int dtype, const Params& p, hipStream_t stream)
 hipError_t launch_varlen_wide(int dtype, const Params& p, hipStream_t stream);
 hipError_t launch_varlen_hint(int dtype, const Params& p, hipStream_t stream);
 hipError_t launch_transform_wide(int dtype, const Params& p, hipStream_t stream);
+// The device of `stream`, checked to be a gfx950 (vts_api.hip).
+int check_device(void* stream, int* dev_out = nullptr, int* cus_out = nullptr);
 // Zeroes `words` 32-bit words at `p` (a kernel, so it can sit in a captured graph).
 hipError_t launch_zero(uint32_t* p, size_t words, hipStream_t stream);
 hipError_t launch_transform_ordered(int dtype, const Params& p, hipStream_t stream);
