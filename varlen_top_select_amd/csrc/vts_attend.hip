@@ -161,9 +161,10 @@ struct Attend {
         }
     }
 
-    // Places whose V row holds an infinity or NaN, where not every row sees
-    // every place: 0 * inf would reach rows that do not see them.  Their V
-    // registers are cleared here and their share is added by add_rows.
+    // Where not every row sees every place, an infinity or NaN in a V row would
+    // reach rows that do not see it (0 * inf).  Such elements' registers are
+    // cleared here, and add_rows adds them to the rows that do.  Returns the
+    // places that hold any.
     __device__ __forceinline__ uint32_t clear_not_finite() {
         uint32_t bad = 0;
 #pragma unroll
@@ -176,9 +177,11 @@ struct Attend {
 #pragma unroll
             for (int g = 0; g < 4; ++g)
                 if ((any >> (16 * g)) & 0xFFFFu) bad |= 1u << ((j >> 2) * 16 + g * 4 + (j & 3));
-            if ((any >> (16 * grp)) & 0xFFFFu)
 #pragma unroll
-                for (int w = 0; w < VW; ++w) v[j][w] = 0;
+            for (int w = 0; w < VW; ++w) {
+                if (not_finite<DT>(v[j][w] & 0xFFFFu)) v[j][w] &= 0xFFFF0000u;
+                if (not_finite<DT>(v[j][w] >> 16)) v[j][w] &= 0xFFFFu;
+            }
         }
         return bad;
     }
@@ -208,7 +211,7 @@ struct Attend {
                     for (int e = 0; e < 4; ++e) {
                         const uint32_t raw = (x[e][n >> 1] >> (16 * (n & 1))) & 0xFFFFu;
                         const float y = o[mt][n][e] + w * to_float<DT>(raw);
-                        o[mt][n][e] = see ? y : o[mt][n][e];
+                        o[mt][n][e] = see && not_finite<DT>(raw) ? y : o[mt][n][e];
                     }
             }
         }
