@@ -101,7 +101,7 @@ struct VerifyParams {
     int32_t* count;  // [batch]
     int32_t* token;  // [batch]
     uint32_t* tickets;
-    double* sums;    // [batch][slices][2]
+    double* sums;    // [batch][16 * slices]
 };
 
 hipError_t launch_attend(int dtype, int head_dim, int mt, const AttendParams& p, hipStream_t stream);

@@ -129,14 +129,14 @@ int attend_plan(int32_t draft, int32_t heads, int32_t kv_heads, int32_t head_dim
     return VTS_OK;
 }
 
-// Slices of a request's vocabulary: about three workgroups per compute unit,
-// of at least 2048 values each.
+// Workgroups per request: as many as the device holds at once (two of 16 waves
+// on each compute unit), of at least 4096 values each.
 int32_t verify_slices(int64_t batch, int64_t vocab) {
     if (batch < 1 || batch > MAX_TICKETS) return 1;
-    int64_t s = 3 * CUS / batch;
-    const int64_t most = (vocab + 2047) / 2048;
+    int64_t s = 2 * CUS / batch;
+    const int64_t most = (vocab + 4095) / 4096;
     if (s > most) s = most;
-    if (s > 64) s = 64;
+    if (s > 64) s = 64;  // 1024 segments, one to a thread of the joining workgroup
     return s < 1 ? 1 : (int32_t)s;
 }
 
@@ -297,7 +297,7 @@ int vts_evict_cache(const vts_paged_cache* cache, const float* weights,
 
 size_t vts_verify_draft_workspace_bytes(int64_t batch, int64_t vocab) {
     const int64_t n = batch < 1 ? 1 : batch;
-    return TICKET_BYTES + align256((size_t)n * verify_slices(batch, vocab) * 8);
+    return TICKET_BYTES + align256((size_t)n * verify_slices(batch, vocab) * 16 * 8);
 }
 
 int vts_verify_draft(const void* target_probs, int32_t dtype, int64_t target_batch_stride,

@@ -11,20 +11,29 @@
 // first v whose running sum passes u S.  Sums are held in 64 bits: the token is
 // a whole number that must not depend on how the sum is split.
 //
-// Each request has `slices` workgroups.  All of them walk the tree as far as it
-// goes without a sum, which is a few dozen scalars and gives all the same
-// state, and sum one slice each; the last to arrive joins the sums in order,
-// finishes the walk, and scans the one slice that the token lies in.
+// Each request has `slices` workgroups of 16 waves.  All of them walk the tree
+// as far as it goes without a sum, which is a few dozen scalars and gives all
+// the same state, and every wave sums one segment of the vocabulary; the last
+// workgroup to arrive joins the sums in order, finishes the walk, and scans the
+// one segment that the token lies in.  A sum that the rest of the walk needs
+// (a second rejection) it takes alone, a sixteenth of the row to a wave.
 #include "vts_paged.hpp"
 
 namespace vts {
 
+constexpr int VT = 1024;  // threads
+constexpr int VW = VT / 64;
+
+// a 16-byte load from any element's address
+typedef u32x4 Unaligned __attribute__((aligned(2)));
+
 struct VerifyShared {
     float p[MAX_DRAFT], q[MAX_DRAFT], u[MAX_DRAFT];
     int32_t token[MAX_DRAFT], parent[MAX_DRAFT], path[MAX_DRAFT];
-    double sum[WAVES];
+    double sums[VT];  // of the segments
+    double scan[VW];
     uint32_t last;
-    int32_t found;
+    int32_t found, tail;
 };
 
 __device__ __forceinline__ float prob(float x) { return x > 0.0f ? x : 0.0f; }  // NaN: 0
@@ -48,6 +57,7 @@ struct Walk {
 
 template <int DT>
 struct Verify {
+    static constexpr int VE = DT == F32 ? 4 : 8;  // elements of a 16-byte vector
     const VerifyParams& p;
     VerifyShared& sm;
     const int32_t b;
@@ -128,32 +138,117 @@ struct Verify {
         return false;
     }
 
-    __device__ __forceinline__ double residual(const Walk& k, const void* pr, const void* qr,
-                                               int32_t v) const {
-        const double x = load_prob<DT>(pr, v);
-        if (k.a > 0) return fmax(x - k.a * (double)load_prob<DT>(qr, v), 0.0);
-        return k.gone && is_gone(k.gone, v) ? 0.0 : x;
+    // A vector of values from element v of a row on, past the vocabulary 0.
+    // Rows need no alignment beyond their element's.
+    __device__ __forceinline__ void load(const void* row, int32_t v, float (&x)[VE]) const {
+        constexpr int E = DT == F32 ? 4 : 2;
+        if (v + VE <= p.vocab) {
+            const Unaligned w = *(const VTS_GLOBAL Unaligned*)((const VTS_GLOBAL char*)row + (int64_t)v * E);
+#pragma unroll
+            for (int i = 0; i < VE; ++i) {
+                if constexpr (DT == F32) {
+                    const uint32_t bits = w[i];  // (a bit cast of w[i] itself takes element 0)
+                    x[i] = __builtin_bit_cast(float, bits);
+                } else
+                    x[i] = to_float<DT>((w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VE; ++i) x[i] = v + i < p.vocab ? load_prob<DT>(row, v + i) : 0.0f;
+        }
+    }
+    // The residual at elements v .. v + VE - 1.
+    struct Pair {
+        float x[VE], y[VE];
+    };
+    __device__ __forceinline__ Pair fetch(const Walk& k, const void* pr, const void* qr,
+                                          int32_t v) const {
+        Pair f;
+        load(pr, v, f.x);
+        if (k.a > 0) load(qr, v, f.y);
+        return f;
+    }
+    __device__ __forceinline__ void residual(const Walk& k, const Pair& f, int32_t v,
+                                             double (&r)[VE]) const {
+        if (k.a > 0) {
+#pragma unroll
+            for (int i = 0; i < VE; ++i)
+                r[i] = fmax((double)prob(f.x[i]) - k.a * (double)prob(f.y[i]), 0.0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VE; ++i) r[i] = prob(f.x[i]);
+            if (k.gone)
+                for (uint64_t g = k.gone; g; g &= g - 1) {
+                    const int32_t x = sm.token[__builtin_ctzll(g)] - v;
+#pragma unroll
+                    for (int i = 0; i < VE; ++i) r[i] = x == i ? 0.0 : r[i];
+                }
+        }
     }
 
-    __device__ __forceinline__ int32_t slice_begin(int32_t s) const {
-        return (int32_t)((int64_t)p.vocab * s / p.slices);
-    }
-
-    // The residual's sum over [v0, v1), the same in every thread.
-    __device__ __forceinline__ double sum(const Walk& k, int32_t v0, int32_t v1) {
+    // This wave's lanes' sum over [v0, v1) (v0 a multiple of VE), in every lane.
+    __device__ __forceinline__ double wave_sum(const Walk& k, int32_t v0, int32_t v1) const {
+        constexpr int U = DT == F32 ? 4 : 2;  // vectors in flight per lane and row
         const void* pr = target_row(k.cur);
         const void* qr = k.a > 0 ? draft_row(k.cur) : nullptr;
         double s = 0;
-        for (int32_t v = v0 + (int32_t)threadIdx.x; v < v1; v += NT) s += residual(k, pr, qr, v);
+        for (int32_t v = v0 + (int32_t)lane_id() * VE; v < v1; v += 64 * VE * U) {
+            Pair f[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (v + u * 64 * VE < v1) f[u] = fetch(k, pr, qr, v + u * 64 * VE);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (v + u * 64 * VE < v1) {
+                    double r[VE];
+                    residual(k, f[u], v + u * 64 * VE, r);
+#pragma unroll
+                    for (int i = 0; i < VE; ++i) s += r[i];
+                }
+        }
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
-        __syncthreads();
-        if (lane_id() == 0) sm.sum[threadIdx.x >> 6] = s;
-        __syncthreads();
-        s = 0;
-#pragma unroll
-        for (int w = 0; w < WAVES; ++w) s += sm.sum[w];
         return s;
+    }
+
+    // Elements per segment when the row is cut in `n`.
+    __device__ __forceinline__ int32_t segment(int32_t n) const {
+        return ((p.vocab + n - 1) / n + VE - 1) / VE * VE;
+    }
+    __device__ __forceinline__ double sum_segment(const Walk& k, int32_t n, int32_t g) const {
+        const int64_t len = segment(n), v0 = g * len;
+        const int64_t v1 = v0 + len < p.vocab ? v0 + len : p.vocab;
+        return v0 < v1 ? wave_sum(k, (int32_t)v0, (int32_t)v1) : 0.0;
+    }
+    // The whole row by this workgroup alone, VW segments.
+    __device__ __forceinline__ void sum_alone(const Walk& k) {
+        const int wave = threadIdx.x >> 6;
+        const double s = sum_segment(k, VW, wave);
+        __syncthreads();
+        if (lane_id() == 0) sm.sums[wave] = s;
+        __syncthreads();
+    }
+
+    // Inclusive sums over the workgroup's threads, and the whole.
+    __device__ __forceinline__ double block_scan(double v, double& total) {
+        double inc = v;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const double o = __shfl_up(inc, d);
+            if ((int)lane_id() >= d) inc += o;
+        }
+        const int wave = threadIdx.x >> 6;
+        __syncthreads();
+        if (lane_id() == 63) sm.scan[wave] = inc;
+        __syncthreads();
+        double before = 0;
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+            if (w < wave) before += sm.scan[w];
+            total += sm.scan[w];
+        }
+        return before + inc;
     }
 
     // First v of [v0, v1) with start + (running sum) > bar; if none, the last v
@@ -162,30 +257,47 @@ struct Verify {
                                               double bar) {
         const void* pr = target_row(k.cur);
         const void* qr = k.a > 0 ? draft_row(k.cur) : nullptr;
-        int32_t fallback = -1;
-        for (int32_t x0 = v0; x0 < v1; x0 += NT) {
-            const int32_t v = x0 + (int32_t)threadIdx.x;
-            const double r = v < v1 ? residual(k, pr, qr, v) : 0.0;
-            double inc = r;
+        int32_t tail = -1;
+        for (int32_t x0 = v0; x0 < v1; x0 += VT * VE) {
+            const int32_t v = x0 + (int32_t)threadIdx.x * VE;
+            double r[VE], s = 0, total;
 #pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const double o = __shfl_up(inc, d);
-                if ((int)lane_id() >= d) inc += o;
+            for (int i = 0; i < VE; ++i) r[i] = 0;
+            if (v < v1) residual(k, fetch(k, pr, qr, v), v, r);
+#pragma unroll
+            for (int i = 0; i < VE; ++i) s += r[i];
+            if (threadIdx.x == 0) sm.found = INT32_MAX, sm.tail = -1;
+            const double inc = start + block_scan(s, total);
+            if (s > 0) {
+                if (inc > bar) atomicMin(&sm.found, (int32_t)threadIdx.x);
+                int32_t mine = 0;
+#pragma unroll
+                for (int i = 0; i < VE; ++i) mine = r[i] > 0 ? i : mine;
+                atomicMax(&sm.tail, v + mine);
             }
             __syncthreads();
-            if (lane_id() == 63) sm.sum[threadIdx.x >> 6] = inc;
-            if (threadIdx.x == 0) sm.found = INT32_MAX, sm.last = 0;
+            if (sm.found != INT32_MAX) {
+                const bool me = sm.found == (int32_t)threadIdx.x;
+                __syncthreads();
+                if (me) {
+                    double run = inc - s;
+                    int32_t at = 0;
+                    bool hit = false;
+#pragma unroll
+                    for (int i = 0; i < VE; ++i) {
+                        run += r[i];
+                        if (!hit && r[i] > 0) at = i, hit = run > bar;
+                    }
+                    sm.found = v + at;
+                }
+                __syncthreads();
+                return sm.found;
+            }
+            if (sm.tail >= 0) tail = sm.tail;
+            start += total;
             __syncthreads();
-            double before = start;
-            for (int w = 0; w < (int)(threadIdx.x >> 6); ++w) before += sm.sum[w];
-            if (r > 0 && before + inc > bar) atomicMin(&sm.found, v);
-            if (r > 0) atomicMax(&sm.last, (uint32_t)v + 1);
-            for (int w = 0; w < WAVES; ++w) start += sm.sum[w];
-            __syncthreads();
-            if (sm.found != INT32_MAX) return sm.found;
-            if (sm.last) fallback = (int32_t)sm.last - 1;
         }
-        return fallback;
+        return tail;
     }
 
     __device__ __forceinline__ void run(int32_t slice) {
@@ -198,10 +310,16 @@ struct Verify {
         k.mass = 1;
         k.gone = 0;
         bool more = advance(k);
+        const int wave = threadIdx.x >> 6;
+        int32_t segments = p.slices * VW;  // whose sums are in sm.sums
         if (p.slices > 1) {
-            const double mine = sum(k, slice_begin(slice), slice_begin(slice + 1));
+            double* sums = p.sums + (int64_t)b * segments;
+            const double mine = sum_segment(k, segments, slice * VW + wave);
+            if (lane_id() == 0) gstore(sums + slice * VW + wave, mine);
+            // every wave's store is complete before the barrier; thread 0's
+            // release fence then covers the workgroup's
+            __syncthreads();
             if (threadIdx.x == 0) {
-                gstore(p.sums + (int64_t)b * p.slices + slice, mine);
                 __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
                 const uint32_t old =
                     __hip_atomic_fetch_add((VTS_GLOBAL uint32_t*)(p.tickets + b), 1u,
@@ -215,59 +333,55 @@ struct Verify {
             }
             __syncthreads();
             if (!sm.last) return;
+            if ((int32_t)threadIdx.x < segments)
+                sm.sums[threadIdx.x] = gload(sums + threadIdx.x);
+        } else {
+            sum_alone(k);
         }
-        // Slice sums of the state at hand, in sums[]; whether they are current.
-        double* sums = p.sums + (int64_t)b * p.slices;
-        bool current = p.slices > 1;
-        double total = 0;
+        double total, inc;
         for (;;) {
-            if (!current) {
-                for (int32_t s = 0; s < p.slices; ++s) {
-                    const double x = sum(k, slice_begin(s), slice_begin(s + 1));
-                    if (threadIdx.x == 0) gstore(sums + s, x);
-                }
-                __syncthreads();
-            }
-            total = 0;
-            for (int32_t s = 0; s < p.slices; ++s) total += gload(sums + s);
-            if (!more) break;
-            k.mass = total;
-            const Walk was = k;
-            more = advance(k);
-            current = !more && k.cur == was.cur && k.a == was.a;
-        }
-        if (total == 0 && (k.a > 0 || k.gone)) {  // nothing left of p: draw from p itself
-            k.a = 0;
-            k.gone = 0;
             __syncthreads();
-            for (int32_t s = 0; s < p.slices; ++s) {
-                const double x = sum(k, slice_begin(s), slice_begin(s + 1));
-                if (threadIdx.x == 0) gstore(sums + s, x);
-                total += x;
+            inc = block_scan((int32_t)threadIdx.x < segments ? sm.sums[threadIdx.x] : 0.0, total);
+            if (more) {
+                const int32_t cur = k.cur;
+                const double a = k.a;
+                k.mass = total;
+                more = advance(k);
+                if (!more && k.cur == cur && k.a == a) continue;  // the same residual
+            } else if (total == 0 && (k.a > 0 || k.gone)) {
+                k.a = 0;  // nothing is left of p: draw from p itself
+                k.gone = 0;
+            } else {
+                break;
             }
-            __syncthreads();
+            sum_alone(k);
+            segments = VW;
         }
         const double bar =
             (double)gload(p.uniforms + (int64_t)b * (p.draft + 1) + p.draft) * total;
-        int32_t token = -1;
-        double start = 0;
-        int32_t at = -1;
-        double at_start = 0;
-        for (int32_t s = 0; s < p.slices; ++s) {  // the slice the running sum passes the bar in
-            const double x = gload(sums + s);
-            if (x > 0) {
-                at = s;
-                at_start = start;
-                if (start + x > bar) break;
-            }
-            start += x;
+        // the first segment whose running sum passes the bar, or the last of any mass
+        const double x = (int32_t)threadIdx.x < segments ? sm.sums[threadIdx.x] : 0.0;
+        if (threadIdx.x == 0) sm.found = INT32_MAX, sm.tail = -1;
+        __syncthreads();
+        if (x > 0) {
+            if (inc > bar) atomicMin(&sm.found, (int32_t)threadIdx.x);
+            atomicMax(&sm.tail, (int32_t)threadIdx.x);
         }
-        if (at >= 0) token = search(k, slice_begin(at), slice_begin(at + 1), at_start, bar);
+        __syncthreads();
+        const int32_t at = sm.found != INT32_MAX ? sm.found : sm.tail;
+        if ((int32_t)threadIdx.x == at) sm.scan[0] = inc - x;
+        __syncthreads();
+        int32_t token = -1;
+        if (at >= 0) {
+            const double start = sm.scan[0];
+            const int64_t len = segment(segments), v0 = at * len;
+            const int64_t v1 = v0 + len < p.vocab ? v0 + len : p.vocab;
+            token = search(k, (int32_t)v0, (int32_t)v1, start, bar);
+        }
         if (threadIdx.x == 0) {
             gstore(p.token + b, token);
             gstore(p.count + b, k.steps);
         }
-        __syncthreads();
         if ((int32_t)threadIdx.x < p.draft)
             gstore(p.path + (int64_t)b * p.draft + threadIdx.x,
                    (int32_t)threadIdx.x < k.steps ? sm.path[threadIdx.x] : -1);
@@ -275,16 +389,15 @@ struct Verify {
 };
 
 template <int DT>
-__global__ __launch_bounds__(NT) void verify_kernel(VerifyParams p) {
+__global__ __launch_bounds__(VT) void verify_kernel(VerifyParams p) {
     __shared__ VerifyShared sm;
-    // a request's slices run on the XCDs in turn
     const int32_t b = (int32_t)(blockIdx.x / p.slices), slice = (int32_t)(blockIdx.x % p.slices);
     Verify<DT> v(p, sm, b);
     v.run(slice);
 }
 
 hipError_t launch_verify(int dtype, const VerifyParams& p, hipStream_t stream) {
-    const dim3 grid((uint32_t)p.batch * (uint32_t)p.slices), block(NT);
+    const dim3 grid((uint32_t)p.batch * (uint32_t)p.slices), block(VT);
     switch (dtype) {
         case F32: hipLaunchKernelGGL((verify_kernel<F32>), grid, block, 0, stream, p); break;
         case BF16: hipLaunchKernelGGL((verify_kernel<BF16>), grid, block, 0, stream, p); break;
