@@ -21,7 +21,8 @@ namespace vts {
 
 template <int D, int MT>
 struct AttendShared {
-    float o[2][16 * MT][D];
+    u32x4 q[MT > 1 ? MT * (D / 32) : 1][64];  // query rows as operands, from 32 rows on
+    float o[2][16 * MT][D + 4];  // padded: the 16 rows of a store fall on all banks
     float ml[WAVES][16 * MT][2];
     int64_t scan[WAVES + 1];
     int32_t found;
@@ -38,11 +39,12 @@ struct Attend {
 
     const AttendParams& p;
     AttendShared<D, MT>& sm;
-    const int lane, wave, col, grp;
-    const uint32_t page_stride, pos_stride;  // of K in lanes 0..31, of V above
+    int tid, lane, wave, col, grp;
+    uint32_t page_stride, pos_stride;  // of K in lanes 0..31, of V above
     int32_t req, head_kv, mb, t0;  // t0: the row of a slot list
     Places pl;
-    u32x4 q[MT][KS];
+    static constexpr bool QL = MT > 1;  // query rows in LDS
+    u32x4 q[QL ? 1 : KS];
     uint64_t bits[MT];
     f32x4 o[MT][NTILE];
     float m[MT], l[MT];
@@ -52,9 +54,20 @@ struct Attend {
     const void* vbase;
 
     __device__ Attend(const AttendParams& p_, AttendShared<D, MT>& s_, int32_t mb_)
-        : p(p_), sm(s_), lane(lane_id()), wave(threadIdx.x >> 6), col(lane & 15), grp(lane >> 4),
-          page_stride(lane < 32 ? p_.c.k.page_stride : p_.c.v.page_stride),
-          pos_stride(lane < 32 ? p_.c.k.pos_stride : p_.c.v.pos_stride), mb(mb_) {}
+        : p(p_), sm(s_), mb(mb_) {
+        fresh();
+    }
+    // The thread's place, opaque to the compiler: called where a stage begins, so
+    // that what one stage computes from it is not kept in registers through the
+    // others (70 of them, otherwise, through the walk).
+    __device__ __forceinline__ void fresh() {
+        tid = threadIdx.x;
+        asm volatile("" : "+v"(tid));
+        lane = tid & 63;
+        wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        col = lane & 15;
+        grp = lane >> 4;
+    }
 
     // row m of the block: the drafted token and the query head
     __device__ __forceinline__ bool row_of(int r, int32_t& t, int32_t& head) const {
@@ -70,6 +83,7 @@ struct Attend {
     }
 
     __device__ __forceinline__ void begin(int32_t b, int32_t h) {
+        fresh();
         head_kv = h;
         const PagedParams& c = p.c;
         if (SLOTS) {
@@ -97,8 +111,13 @@ struct Attend {
                              2 * (req * p.q_batch + (ok ? t * p.q_row + head * p.q_head : 0));
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                const u32x4 z = {0, 0, 0, 0};
-                q[mt][s] = ok ? gload((const u32x4*)(at + s * 64 + grp * 16)) : z;
+                u32x4 x = {0, 0, 0, 0};
+                if (QL && (mt * KS + s) % WAVES != wave) continue;
+                if (ok) x = gload((const u32x4*)(at + s * 64 + grp * 16));
+                if constexpr (QL)
+                    sm.q[mt * KS + s][lane] = x;
+                else
+                    q[s] = x;
             }
             uint64_t w = 0;
             if (ok) {
@@ -113,6 +132,7 @@ struct Attend {
 #pragma unroll
             for (int n2 = 0; n2 < NTILE; ++n2) o[mt][n2] = f32x4{0, 0, 0, 0};
         }
+        if constexpr (QL) __syncthreads();
     }
 
     __device__ __forceinline__ Entry issue(int32_t u) const {
@@ -186,7 +206,7 @@ struct Attend {
         return bad;
     }
     __device__ __forceinline__ void add_rows(uint32_t bad, uint32_t off, int32_t j0,
-                                             const float (&pr)[MT][8]) {
+                                             const u32x4 (&pv)[MT]) {
 #pragma unroll 1
         while (bad) {
             const int kk = __builtin_ctz(bad);
@@ -200,10 +220,11 @@ struct Attend {
             const int32_t i = j0 + kk - pl.first;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                float w = 0;
+                uint32_t pair = 0;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) w = e == idx ? pr[mt][e] : w;
-                w = __builtin_bit_cast(float, from_lane(__builtin_bit_cast(uint32_t, w), src));
+                for (int e = 0; e < 4; ++e) pair = e == idx >> 1 ? pv[mt][e] : pair;
+                pair = from_lane(pair, src);
+                const float w = to_float<DT>((pair >> (16 * (idx & 1))) & 0xFFFFu);
                 const bool see = i < 0 || ((bits[mt] >> (i & 63)) & 1);
 #pragma unroll
                 for (int n = 0; n < NTILE; ++n)
@@ -217,34 +238,48 @@ struct Attend {
         }
     }
 
-    // One tile: its scores' softmax against the running state, and its share of
-    // O.  MASKED: some place is missing, or some row does not see some place.
-    template <bool MASKED>
-    __device__ __forceinline__ void tile(f32x4 (&s)[MT][2], uint32_t have, bool drafted,
-                                         uint32_t off, int32_t j0) {
+    // One tile: scores, the running softmax, O.  `masked`: some place is missing,
+    // or some row does not see some place.  The next tile's K rows are asked for
+    // as soon as this tile's are used up, and its V rows after the second
+    // product, so one of the two is always on its way.
+    __device__ __forceinline__ void tile(uint32_t have, bool drafted, uint32_t off, int32_t j0,
+                                         bool more, uint32_t off_next) {
         const float c = p.scale_log2e;
-        float pr[MT][8];
+        const bool masked = have != ~0u || drafted;
+        u32x4 pv[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
+            f32x4 s[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                s[h] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+                    s[h] = mfma<DT>(k[h][ks], QL ? sm.q[mt * KS + ks][lane] : q[QL ? 0 : ks], s[h]);
+            }
+            if (mt == MT - 1 && more) load_k(off_next);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e >> 2][e & 3] *= c;
+            if (masked) {
+                int g = grp;  // opaque: nothing of this is kept in registers between tiles
+                asm volatile("" : "+v"(g));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int kk = (e >> 2) * 16 + g * 4 + (e & 3);
+                    const int32_t i = j0 + kk - pl.first;
+                    const uint32_t see = (have >> kk) & (((uint32_t)i >> 31) |
+                                                         (uint32_t)(bits[mt] >> (i & 63)));
+                    s[e >> 2][e & 3] = (see & 1u) ? s[e >> 2][e & 3] : NEG_INF;
+                }
+            }
             float top = NEG_INF;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float x = s[mt][e >> 2][e & 3] * c;
-                if constexpr (MASKED) {
-                    const int kk = v_place(e);
-                    const int32_t i = j0 + kk - pl.first;
-                    const bool see = ((have >> kk) & 1u) &&
-                                     (i < 0 || (i < MAX_DRAFT && ((bits[mt] >> (i & 63)) & 1)));
-                    x = see ? x : NEG_INF;
-                }
-                pr[mt][e] = x;
-                top = fmaxf(top, x);
-            }
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, s[e >> 2][e & 3]);
             if (ballot(top > m[mt] + 8.0f)) {
                 top = fmaxf(top, __shfl_xor(top, 16));
                 top = fmaxf(top, __shfl_xor(top, 32));
                 const float up = fmaxf(top, m[mt]);
-                const float f = up == NEG_INF ? 1.0f : exp2f(m[mt] - up);
+                const float f = up == NEG_INF ? 1.0f : __builtin_amdgcn_exp2f(m[mt] - up);
                 m[mt] = up;
                 l[mt] *= f;
 #pragma unroll
@@ -254,35 +289,35 @@ struct Attend {
             }
             const float base = m[mt] == NEG_INF ? 0.0f : m[mt];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                pr[mt][e] = __builtin_amdgcn_exp2f(pr[mt][e] - base);
-                l[mt] += pr[mt][e];
+            for (int e = 0; e < 4; ++e) {
+                const float a = __builtin_amdgcn_exp2f(s[e >> 1][2 * (e & 1)] - base);
+                const float b = __builtin_amdgcn_exp2f(s[e >> 1][2 * (e & 1) + 1] - base);
+                l[mt] += a + b;
+                pv[mt][e] = pack2<DT>(a, b);
             }
         }
         uint32_t bad = 0;
-        if constexpr (MASKED) {
+        if (masked) {
+            int g = grp;
+            asm volatile("" : "+v"(g));
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const bool there = (have >> v_place(j)) & 1u;
+                const uint32_t there = (have >> ((j >> 2) * 16 + g * 4 + (j & 3))) & 1u;
 #pragma unroll
                 for (int w = 0; w < VW; ++w) v[j][w] = there ? v[j][w] : 0;
             }
             if (drafted) bad = clear_not_finite();
         }
-        u32x4 pv[MT];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) pv[mt][e] = pack2<DT>(pr[mt][2 * e], pr[mt][2 * e + 1]);
         second_product(pv);
-        if constexpr (MASKED)
-            if (bad) add_rows(bad, off, j0, pr);
+        if (bad) add_rows(bad, off, j0, pv);
+        if (more) load_v(off_next);
     }
 
-    // Units [u0, u1) of the places, this wave's 32 of each 128.  The next
-    // tile's K rows are asked for as soon as this tile's are used up, and its V
-    // rows after the second product, so one of the two is always on its way.
+    // Units [u0, u1) of the places, this wave's 32 of each 128.
     __device__ __forceinline__ void walk(int32_t u0, int32_t u1) {
+        fresh();
+        page_stride = lane < 32 ? p.c.k.page_stride : p.c.v.page_stride;
+        pos_stride = lane < 32 ? p.c.k.pos_stride : p.c.v.pos_stride;
         uint32_t off = resolve(issue(u0));
         Entry next = issue(u0 + 1);
         load_k(off);
@@ -290,27 +325,11 @@ struct Attend {
 #pragma unroll 1
         for (int32_t u = u0; u < u1; ++u) {
             const int32_t j0 = u * UNIT + wave * 32;
-            const bool more = u + 1 < u1;
             const uint32_t off_next = resolve(next);
             next = issue(u + 2);
-            f32x4 s[MT][2];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    f32x4 acc = {0, 0, 0, 0};
-#pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) acc = mfma<DT>(k[h][ks], q[mt][ks], acc);
-                    s[mt][h] = acc;
-                }
-            if (more) load_k(off_next);
             const uint32_t have = (uint32_t)ballot(off != NO_PLACE);
             const bool drafted = j0 + 31 >= pl.first;
-            if (have == ~0u && !drafted)
-                tile<false>(s, have, false, off, j0);
-            else
-                tile<true>(s, have, drafted, off, j0);
-            if (more) load_v(off_next);
+            tile(have, drafted, off, j0, u + 1 < u1, off_next);
             off = off_next;
         }
     }
@@ -337,6 +356,7 @@ struct Attend {
 
     // Joins the four waves; the block's rows are then in sm.o[0], sm.ml[0].
     __device__ __forceinline__ void join_waves() {
+        fresh();
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             l[mt] += __shfl_xor(l[mt], 16);
@@ -399,10 +419,16 @@ struct Attend {
         if (d == 0 && p.lse)
             gstore(p.lse + at, sum == 0.0f ? NEG_INF : (top + log2f(sum)) * 0.6931471805599453f);
     }
+    // rows of this block that are there
+    __device__ __forceinline__ int rows_here() const {
+        const int32_t n = p.rows - mb * 16 * MT;
+        return n < 16 * MT ? n : 16 * MT;
+    }
 
     __device__ __forceinline__ void finish_whole() {
         join_waves();
-        for (int x = threadIdx.x * 4; x < 16 * MT * D; x += NT * 4) {
+        const int n = rows_here() * D;
+        for (int x = tid * 4; x < n; x += NT * 4) {
             const int r = x / D, d = x % D;
             write_row(r, d, *(const f32x4*)&sm.o[0][r][d], sm.ml[0][r][0], sm.ml[0][r][1]);
         }
@@ -414,15 +440,16 @@ struct Attend {
     __device__ __forceinline__ void finish_part(int64_t mine, int32_t w0, int32_t w1,
                                                 bool w0_whole_start) {
         join_waves();
+        const int rows = rows_here();
         float* po = p.part_o + mine * (16 * MT * D);
         float* pm = p.part_ml + mine * (16 * MT * 2);
-        for (int x = threadIdx.x * 4; x < 16 * MT * D; x += NT * 4)
-            gstore((f32x4*)(po + x), *(const f32x4*)(&sm.o[0][0][0] + x));
-        if (threadIdx.x < 16 * MT * 2) gstore(pm + threadIdx.x, (&sm.ml[0][0][0])[threadIdx.x]);
+        for (int x = tid * 4; x < rows * D; x += NT * 4)
+            gstore((f32x4*)(po + x), *(const f32x4*)&sm.o[0][x / D][x % D]);
+        if (tid < rows * 2) gstore(pm + tid, (&sm.ml[0][0][0])[tid]);
         // every wave's stores are complete before the barrier; thread 0's
         // release fence then covers the workgroup's
         __syncthreads();
-        if (threadIdx.x == 0) {
+        if (tid == 0) {
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
             uint32_t* ticket = p.tickets + (int64_t)mb * p.workers + w0;
             const uint32_t old = __hip_atomic_fetch_add((VTS_GLOBAL uint32_t*)ticket, 1u,
@@ -435,27 +462,56 @@ struct Attend {
             sm.last = last;
         }
         __syncthreads();
-        if (sm.last) {
-            for (int x = threadIdx.x * 4; x < 16 * MT * D; x += NT * 4) {
-                const int r = x / D;
-                float top = NEG_INF, sum = 0;
-                for (int32_t w = w0; w <= w1; ++w)
-                    top = fmaxf(top, gload(p.part_ml + part(w, w0, w0_whole_start) * (16 * MT * 2) +
-                                           r * 2));
-                f32x4 acc = {0, 0, 0, 0};
-                for (int32_t w = w0; w <= w1; ++w) {
-                    const int64_t at = part(w, w0, w0_whole_start);
-                    const float f =
-                        scale_to(gload(p.part_ml + at * (16 * MT * 2) + r * 2), top);
-                    sum += f * gload(p.part_ml + at * (16 * MT * 2) + r * 2 + 1);
-                    const f32x4 x4 = gload((const f32x4*)(p.part_o + at * (16 * MT * D) + x));
+        if (sm.last) join_parts(rows, w0, w1, w0_whole_start);
+        __syncthreads();
+    }
+
+    // Other workgroups' parts come from beyond this XCD, so their loads are
+    // issued eight at a time: one after the other, 32 parts took 40 us.
+    __device__ __forceinline__ void join_parts(int rows, int32_t w0, int32_t w1, bool w0_whole_start) {
+        constexpr int LANES = NT / (16 * MT);  // threads to a row for the maxima
+        const int row = tid % (16 * MT), sub = tid / (16 * MT);
+        float top = NEG_INF;
+        if (row < rows)
+            for (int32_t w = w0 + sub; w <= w1; w += LANES)
+                top = fmaxf(top, gload(p.part_ml + part(w, w0, w0_whole_start) * (16 * MT * 2) +
+                                       row * 2));
+        float* tops = &sm.o[0][0][0];
+        tops[sub * 16 * MT + row] = top;
+        __syncthreads();
+        if (sub == 0) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[e] += f * x4[e];
-                }
-                write_row(r, x % D, acc, top, sum);
-            }
+            for (int i = 1; i < LANES; ++i) top = fmaxf(top, tops[i * 16 * MT + row]);
+            sm.ml[0][row][0] = top;
         }
         __syncthreads();
+        for (int x = tid * 4; x < rows * D; x += NT * 4) {
+            const int r = x / D;
+            const float to = sm.ml[0][r][0];
+            float sum = 0;
+            f32x4 acc = {0, 0, 0, 0};
+            constexpr int U = 8;
+            for (int32_t w = w0; w <= w1; w += U) {
+                f32x4 o4[U];
+                float mm[U], ll[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int64_t at = part(w + u <= w1 ? w + u : w1, w0, w0_whole_start);
+                    o4[u] = gload((const f32x4*)(p.part_o + at * (16 * MT * D) + x));
+                    mm[u] = gload(p.part_ml + at * (16 * MT * 2) + r * 2);
+                    ll[u] = gload(p.part_ml + at * (16 * MT * 2) + r * 2 + 1);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (w + u <= w1) {
+                        const float f = scale_to(mm[u], to);
+                        sum += f * ll[u];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[e] += f * o4[u][e];
+                    }
+            }
+            write_row(r, x % D, acc, to, sum);
+        }
     }
     // A worker's slot: its first segment's, or the one of a list that begins
     // inside its share.
