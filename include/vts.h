@@ -410,8 +410,8 @@ typedef struct {
  * Work is shared in units of 128 places over the batch's real lengths, so
  * ragged batches cost what their lengths say.
  */
-size_t vts_tree_attention_workspace_bytes(int32_t draft, int32_t heads, int32_t kv_heads,
-                                          int32_t head_dim, int32_t top_k);
+size_t vts_tree_attention_workspace_bytes(int32_t batch, int32_t draft, int32_t heads,
+                                          int32_t kv_heads, int32_t head_dim, int32_t top_k);
 int vts_tree_attention(const vts_paged_cache* cache, const void* q, const int64_t* q_strides,
                        int32_t draft, int32_t heads, const int64_t* tree_mask,
                        const int32_t* slots, int32_t top_k, float scale, void* out, float* lse,

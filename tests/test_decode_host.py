@@ -81,10 +81,11 @@ def test_attention_empty_batch_and_null_cache(lib):
 
 def test_attention_workspace_is_a_function_of_the_shape(lib):
     f = lib.vts_tree_attention_workspace_bytes
-    assert f(2, 64, 8, 128, 0) == f(2, 64, 8, 128, 0) > 32768
-    assert f(0, 64, 8, 128, 0) == 0 and f(65, 64, 8, 128, 0) == 0 and f(1, 63, 8, 128, 0) == 0
+    assert f(4, 2, 64, 8, 128, 0) == f(4, 2, 64, 8, 128, 0) > 65536
+    assert f(4, 0, 64, 8, 128, 0) == 0 and f(4, 65, 64, 8, 128, 0) == 0
+    assert f(4, 1, 63, 8, 128, 0) == 0 and f(-1, 1, 64, 8, 128, 0) == 0
     for draft, heads, kv in ((64, 512, 1), (1, 1, 1), (64, 8192, 1), (16, 64, 8)):
-        assert 0 < f(draft, heads, kv, 128, 0) < 1 << 32
+        assert 0 < f(4, draft, heads, kv, 128, 0) < 1 << 32
 
 
 def weigh(lib, c=None, **kw):

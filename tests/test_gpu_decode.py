@@ -81,6 +81,15 @@ CASES = [
     ([150, 64, 40], 64, 4, 2, 64, 16, True, torch.bfloat16),  # 64 drafted tokens, a length below
     ([2500], 2, 16, 1, 128, 128, False, torch.float16),       # one list over many workgroups
     ([777, 1, 300], 1, 40, 1, 128, 32, False, torch.bfloat16),  # 40 rows of one token
+    # four heads or a multiple: a head to a wave
+    ([2600, 33, 0, 1], 3, 32, 4, 64, 16, True, torch.bfloat16),
+    ([1100, 2, 31, 65], 2, 48, 4, 128, 24, True, torch.float16),
+    ([4000], 1, 8, 8, 128, 64, False, torch.bfloat16),
+    ([130, 0, 5000], 2, 12, 12, 64, 1, False, torch.float16),
+    ([500, 90], 9, 32, 8, 128, 16, True, torch.bfloat16),  # 36 rows: not a head to a wave
+    ([(x * 61) % 300 for x in range(16)] + [4000] * 16, 1, 16, 4, 64, 16, False, torch.bfloat16),
+    ([100] * 31 + [9000], 2, 16, 4, 128, 32, True, torch.float16),  # one list over most workgroups
+    ([20000], 1, 2, 1, 64, 64, False, torch.bfloat16),  # blocks of parts
 ]
 
 

@@ -19,29 +19,35 @@
 
 namespace vts {
 
-template <int D, int MT>
+template <int D, int MT, bool HEADS>
 struct AttendShared {
-    u32x4 q[MT > 1 ? MT * (D / 32) : 1][64];  // query rows as operands, from 32 rows on
-    float o[2][16 * MT][D + 4];  // padded: the 16 rows of a store fall on all banks
-    float ml[WAVES][16 * MT][2];
+    static constexpr int ROWS = (HEADS ? WAVES : 1) * 16 * MT;
+    // query rows as operands, from 32 rows on
+    u32x4 q[MT > 1 ? (HEADS ? WAVES : 1) * MT * (D / 32) : 1][64];
+    // padded: the 16 rows of a store fall on all banks
+    float o[HEADS ? 1 : 2][HEADS ? 1 : 16 * MT][D + 4];
+    float ml[HEADS ? 1 : WAVES][ROWS][2];
+    float tops[NT];
     int64_t scan[WAVES + 1];
     int32_t found;
     uint32_t last;
 };
 
-template <int DT, int D, int MT, bool SLOTS>
+template <int DT, int D, int MT, bool SLOTS, bool HEADS>
 struct Attend {
     static constexpr int KS = D / 32;       // steps of the first product
     static constexpr int VB = D / 16 * 2;   // bytes of a V row per lane
     static constexpr int VW = VB / 4;       // words of a V row per lane
     static constexpr int NTILE = D / 16;    // 16-row tiles of the second product
+    static constexpr int JOIN = 16;         // parts joined by one workgroup
+    static constexpr int ROWS = AttendShared<D, MT, HEADS>::ROWS;
     using VRow = typename std::conditional<D == 128, u32x4, u32x2>::type;
 
     const AttendParams& p;
-    AttendShared<D, MT>& sm;
+    AttendShared<D, MT, HEADS>& sm;
     int tid, lane, wave, col, grp;
     uint32_t page_stride, pos_stride;  // of K in lanes 0..31, of V above
-    int32_t req, head_kv, mb, t0;  // t0: the row of a slot list
+    int32_t req, head_unit, mb, t0;  // t0: the row of a slot list
     Places pl;
     static constexpr bool QL = MT > 1;  // query rows in LDS
     u32x4 q[QL ? 1 : KS];
@@ -53,7 +59,7 @@ struct Attend {
     const void* kbase;
     const void* vbase;
 
-    __device__ Attend(const AttendParams& p_, AttendShared<D, MT>& s_, int32_t mb_)
+    __device__ Attend(const AttendParams& p_, AttendShared<D, MT, HEADS>& s_, int32_t mb_)
         : p(p_), sm(s_), mb(mb_) {
         fresh();
     }
@@ -69,22 +75,24 @@ struct Attend {
         grp = lane >> 4;
     }
 
-    // row m of the block: the drafted token and the query head
-    __device__ __forceinline__ bool row_of(int r, int32_t& t, int32_t& head) const {
+    // row r of the block (of its head `sub`): the drafted token and the query head
+    __device__ __forceinline__ bool row_of(int sub, int r, int32_t& t, int32_t& head) const {
         const int32_t row = mb * 16 * MT + r;
+        const int32_t h = HEADS ? head_unit * WAVES + sub : head_unit;
         if (SLOTS) {
             t = t0;
-            head = head_kv * p.c.group + row;
+            head = h * p.c.group + row;
         } else {
             t = row / p.c.group;
-            head = head_kv * p.c.group + (row - t * p.c.group);
+            head = h * p.c.group + (row - t * p.c.group);
         }
         return row < p.rows;
     }
 
     __device__ __forceinline__ void begin(int32_t b, int32_t h) {
         fresh();
-        head_kv = h;
+        head_unit = h;
+        if (HEADS) h = h * WAVES + wave;
         const PagedParams& c = p.c;
         if (SLOTS) {
             req = b / c.draft;
@@ -106,16 +114,16 @@ struct Attend {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             int32_t t, head;
-            const bool ok = row_of(mt * 16 + col, t, head);
+            const bool ok = row_of(wave, mt * 16 + col, t, head);
             const char* at = (const char*)p.q +
                              2 * (req * p.q_batch + (ok ? t * p.q_row + head * p.q_head : 0));
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 u32x4 x = {0, 0, 0, 0};
-                if (QL && (mt * KS + s) % WAVES != wave) continue;
+                if (QL && !HEADS && (mt * KS + s) % WAVES != wave) continue;
                 if (ok) x = gload((const u32x4*)(at + s * 64 + grp * 16));
                 if constexpr (QL)
-                    sm.q[mt * KS + s][lane] = x;
+                    sm.q[q_at(mt, s)][lane] = x;
                 else
                     q[s] = x;
             }
@@ -132,11 +140,17 @@ struct Attend {
 #pragma unroll
             for (int n2 = 0; n2 < NTILE; ++n2) o[mt][n2] = f32x4{0, 0, 0, 0};
         }
-        if constexpr (QL) __syncthreads();
+        if constexpr (QL && !HEADS) __syncthreads();
+    }
+    __device__ __forceinline__ int q_at(int mt, int s) const {
+        return ((HEADS ? wave * MT : 0) + mt) * KS + s;
     }
 
+    __device__ __forceinline__ int32_t first_place(int32_t u) const {
+        return HEADS ? u * 32 : u * UNIT + wave * 32;
+    }
     __device__ __forceinline__ Entry issue(int32_t u) const {
-        return issue_entry<SLOTS>(p.c, pl, u * UNIT + wave * 32 + (lane & 31));
+        return issue_entry<SLOTS>(p.c, pl, first_place(u) + (lane & 31));
     }
     // K offsets in lanes 0..31, V offsets in lanes 32..63
     __device__ __forceinline__ uint32_t resolve(const Entry& e) const {
@@ -148,7 +162,7 @@ struct Attend {
         for (int h = 0; h < 2; ++h) {
             const uint32_t r = from_lane(safe, h * 16 + col);
 #pragma unroll
-            for (int s = 0; s < KS; ++s) k[h][s] = row_load<u32x4>(kbase, r, s * 64 + grp * 16);
+            for (int s = 0; s < KS; ++s) k[h][s] = row_load<u32x4, HEADS>(kbase, r, s * 64 + grp * 16);
         }
     }
     // register j: place 4 * grp + j of the first half, or of the second for j >= 4
@@ -159,7 +173,7 @@ struct Attend {
         const uint32_t safe = off == NO_PLACE ? 0 : off;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            v[j] = row_load<VRow>(vbase, from_lane(safe, 32 + v_place(j)), col * VB);
+            v[j] = row_load<VRow, HEADS>(vbase, from_lane(safe, 32 + v_place(j)), col * VB);
     }
 
     // The tile's share of O: V rows turned so that each lane holds eight places
@@ -255,7 +269,7 @@ struct Attend {
                 s[h] = f32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
-                    s[h] = mfma<DT>(k[h][ks], QL ? sm.q[mt * KS + ks][lane] : q[QL ? 0 : ks], s[h]);
+                    s[h] = mfma<DT>(k[h][ks], QL ? sm.q[q_at(mt, ks)][lane] : q[QL ? 0 : ks], s[h]);
             }
             if (mt == MT - 1 && more) load_k(off_next);
 #pragma unroll
@@ -313,7 +327,7 @@ struct Attend {
         if (more) load_v(off_next);
     }
 
-    // Units [u0, u1) of the places, this wave's 32 of each 128.
+    // Units [u0, u1) of the places, this wave's 32 of each.
     __device__ __forceinline__ void walk(int32_t u0, int32_t u1) {
         fresh();
         page_stride = lane < 32 ? p.c.k.page_stride : p.c.v.page_stride;
@@ -324,7 +338,7 @@ struct Attend {
         load_v(off);
 #pragma unroll 1
         for (int32_t u = u0; u < u1; ++u) {
-            const int32_t j0 = u * UNIT + wave * 32;
+            const int32_t j0 = first_place(u);
             const uint32_t off_next = resolve(next);
             next = issue(u + 2);
             const uint32_t have = (uint32_t)ballot(off != NO_PLACE);
@@ -403,13 +417,19 @@ struct Attend {
     }
     // 2^(m - top), 1 where nothing has been seen
     static __device__ __forceinline__ float scale_to(float from, float top) {
-        return top == NEG_INF ? 1.0f : exp2f(from - top);
+        return top == NEG_INF ? 1.0f : __builtin_amdgcn_exp2f(from - top);
+    }
+    // rows of this block that are there
+    __device__ __forceinline__ int rows_here() const {
+        const int32_t n = p.rows - mb * 16 * MT;
+        return n < 16 * MT ? n : 16 * MT;
     }
 
     // Normalises four outputs of row r and writes them, and its lse.
-    __device__ __forceinline__ void write_row(int r, int d, f32x4 x, float top, float sum) const {
+    __device__ __forceinline__ void write_row(int sub, int r, int d, f32x4 x, float top,
+                                              float sum) const {
         int32_t t, head;
-        if (!row_of(r, t, head)) return;
+        if (!row_of(sub, r, t, head)) return;
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         const int64_t at = ((int64_t)req * p.c.draft + t) * p.c.heads + head;
         u32x2 w;
@@ -419,42 +439,97 @@ struct Attend {
         if (d == 0 && p.lse)
             gstore(p.lse + at, sum == 0.0f ? NEG_INF : (top + log2f(sum)) * 0.6931471805599453f);
     }
-    // rows of this block that are there
-    __device__ __forceinline__ int rows_here() const {
-        const int32_t n = p.rows - mb * 16 * MT;
-        return n < 16 * MT ? n : 16 * MT;
+    // this lane's outputs 4 * i .. of row mt * 16 + col, and where they begin
+    __device__ __forceinline__ f32x4 four(int mt, int i) const {
+        f32x4 x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = o[mt][(4 * i + j) % NTILE][(4 * i + j) / NTILE];
+        return x;
+    }
+    __device__ __forceinline__ int four_at(int i) const { return grp * 4 * NTILE + 4 * i; }
+
+    // A wave with a head of its own: joins the lanes' sums.
+    __device__ __forceinline__ void close() {
+        fresh();
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            l[mt] += __shfl_xor(l[mt], 16);
+            l[mt] += __shfl_xor(l[mt], 32);
+        }
     }
 
     __device__ __forceinline__ void finish_whole() {
-        join_waves();
-        const int n = rows_here() * D;
-        for (int x = tid * 4; x < n; x += NT * 4) {
-            const int r = x / D, d = x % D;
-            write_row(r, d, *(const f32x4*)&sm.o[0][r][d], sm.ml[0][r][0], sm.ml[0][r][1]);
+        if constexpr (HEADS) {
+            close();
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < NTILE; ++i)
+                    write_row(wave, mt * 16 + col, four_at(i), four(mt, i), m[mt], l[mt]);
+        } else {
+            join_waves();
+            const int n = rows_here() * D;
+            for (int x = tid * 4; x < n; x += NT * 4) {
+                const int r = x / D, d = x % D;
+                write_row(0, r, d, *(const f32x4*)&sm.o[0][r][d], sm.ml[0][r][0], sm.ml[0][r][1]);
+            }
+            __syncthreads();
         }
-        __syncthreads();
     }
 
     // A share of the places: leaves the block's rows in slot `mine`; the
     // last of the workers [w0, w1] to arrive joins all, in their order.
     __device__ __forceinline__ void finish_part(int64_t mine, int32_t w0, int32_t w1,
                                                 bool w0_whole_start) {
-        join_waves();
+        float* po = p.part_o + mine * (ROWS * D);
+        float* pm = p.part_ml + mine * (ROWS * 2);
         const int rows = rows_here();
-        float* po = p.part_o + mine * (16 * MT * D);
-        float* pm = p.part_ml + mine * (16 * MT * 2);
-        for (int x = tid * 4; x < rows * D; x += NT * 4)
-            gstore((f32x4*)(po + x), *(const f32x4*)&sm.o[0][x / D][x % D]);
-        if (tid < rows * 2) gstore(pm + tid, (&sm.ml[0][0][0])[tid]);
+        if constexpr (HEADS) {
+            close();
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const int r = mt * 16 + col, at = wave * 16 * MT + r;
+                if (r >= rows) continue;
+#pragma unroll
+                for (int i = 0; i < NTILE; ++i)
+                    gstore((f32x4*)(po + at * D + four_at(i)), four(mt, i));
+                if (grp == 0) {
+                    gstore(pm + at * 2, m[mt]);
+                    gstore(pm + at * 2 + 1, l[mt]);
+                }
+            }
+        } else {
+            join_waves();
+            for (int x = tid * 4; x < rows * D; x += NT * 4)
+                gstore((f32x4*)(po + x), *(const f32x4*)&sm.o[0][x / D][x % D]);
+            if (tid < rows * 2) gstore(pm + tid, (&sm.ml[0][0][0])[tid]);
+        }
+        // The parts are joined in blocks of JOIN workers, each by the block's last
+        // to arrive, and the blocks by the last of those: with one joiner for
+        // all, a list shared by hundreds of workgroups would wait for it.
+        const int32_t blocks = (w1 - w0) / JOIN + 1, w = (int32_t)((mine >> 1) - (int64_t)mb * p.workers);
+        const int32_t block = (w - w0) / JOIN, wb = w0 + block * JOIN;
+        const int32_t members = w1 - wb + 1 < JOIN ? w1 - wb + 1 : JOIN;
+        if (members == 1 || last_of(p.tickets + MAX_TICKETS + (int64_t)mb * p.workers + wb, members)) {
+            if (blocks == 1 || members > 1)
+                join_parts(rows, wb, 1, members, w0, w0_whole_start, blocks == 1);
+            if (blocks > 1 && last_of(p.tickets + (int64_t)mb * p.workers + w0, blocks))
+                join_parts(rows, w0, JOIN, blocks, w0, w0_whole_start, true);
+        }
+        __syncthreads();
+    }
+
+    // Whether this workgroup is the last of `n` to come here; what the others
+    // stored before is then visible.
+    __device__ __forceinline__ bool last_of(uint32_t* ticket, int32_t n) {
         // every wave's stores are complete before the barrier; thread 0's
         // release fence then covers the workgroup's
         __syncthreads();
         if (tid == 0) {
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-            uint32_t* ticket = p.tickets + (int64_t)mb * p.workers + w0;
             const uint32_t old = __hip_atomic_fetch_add((VTS_GLOBAL uint32_t*)ticket, 1u,
                                                         __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            const bool last = old == (uint32_t)(w1 - w0);
+            const bool last = old + 1 == (uint32_t)n;
             if (last) {
                 __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
                 gstore(ticket, 0u);  // self-restoring
@@ -462,55 +537,70 @@ struct Attend {
             sm.last = last;
         }
         __syncthreads();
-        if (sm.last) join_parts(rows, w0, w1, w0_whole_start);
-        __syncthreads();
+        return sm.last;
     }
 
-    // Other workgroups' parts come from beyond this XCD, so their loads are
-    // issued eight at a time: one after the other, 32 parts took 40 us.
-    __device__ __forceinline__ void join_parts(int rows, int32_t w0, int32_t w1, bool w0_whole_start) {
-        constexpr int LANES = NT / (16 * MT);  // threads to a row for the maxima
-        const int row = tid % (16 * MT), sub = tid / (16 * MT);
+    // Joins the parts of workers first, first + stride, ..: to the outputs, or
+    // to the first one's slot.  Other workgroups' parts come from beyond this
+    // XCD, so their loads are issued eight at a time: one after the other,
+    // 32 parts took 40 us.
+    __device__ __forceinline__ void join_parts(int rows, int32_t first, int32_t stride, int32_t count,
+                                               int32_t w0, bool w0_whole_start, bool to_outputs) {
+        constexpr int LANES = NT / ROWS;  // threads to a row for the maxima
+        const int row = tid % ROWS, sub = tid / ROWS;
         float top = NEG_INF;
-        if (row < rows)
-            for (int32_t w = w0 + sub; w <= w1; w += LANES)
-                top = fmaxf(top, gload(p.part_ml + part(w, w0, w0_whole_start) * (16 * MT * 2) +
-                                       row * 2));
-        float* tops = &sm.o[0][0][0];
-        tops[sub * 16 * MT + row] = top;
+        if (row % (16 * MT) < rows)
+            for (int32_t i = sub; i < count; i += LANES)
+                top = fmaxf(top, gload(p.part_ml + part(first + i * stride, w0, w0_whole_start) *
+                                                       (ROWS * 2) + row * 2));
+        sm.tops[sub * ROWS + row] = top;
         __syncthreads();
         if (sub == 0) {
 #pragma unroll
-            for (int i = 1; i < LANES; ++i) top = fmaxf(top, tops[i * 16 * MT + row]);
+            for (int i = 1; i < LANES; ++i) top = fmaxf(top, sm.tops[i * ROWS + row]);
             sm.ml[0][row][0] = top;
         }
         __syncthreads();
-        for (int x = tid * 4; x < rows * D; x += NT * 4) {
+        const int64_t to = part(first, w0, w0_whole_start);
+        for (int x = tid * 4; x < ROWS * D; x += NT * 4) {
             const int r = x / D;
-            const float to = sm.ml[0][r][0];
+            if (r % (16 * MT) >= rows) continue;
+            const float base = sm.ml[0][r][0];
             float sum = 0;
             f32x4 acc = {0, 0, 0, 0};
             constexpr int U = 8;
-            for (int32_t w = w0; w <= w1; w += U) {
+            for (int32_t i = 0; i < count; i += U) {
                 f32x4 o4[U];
                 float mm[U], ll[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int64_t at = part(w + u <= w1 ? w + u : w1, w0, w0_whole_start);
-                    o4[u] = gload((const f32x4*)(p.part_o + at * (16 * MT * D) + x));
-                    mm[u] = gload(p.part_ml + at * (16 * MT * 2) + r * 2);
-                    ll[u] = gload(p.part_ml + at * (16 * MT * 2) + r * 2 + 1);
+                    const int32_t w = first + (i + u < count ? i + u : count - 1) * stride;
+                    const int64_t at = part(w, w0, w0_whole_start);
+                    o4[u] = gload((const f32x4*)(p.part_o + at * (ROWS * D) + x));
+                    mm[u] = gload(p.part_ml + at * (ROWS * 2) + r * 2);
+                    ll[u] = gload(p.part_ml + at * (ROWS * 2) + r * 2 + 1);
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (w + u <= w1) {
-                        const float f = scale_to(mm[u], to);
+                    if (i + u < count) {
+                        const float f = scale_to(mm[u], base);
                         sum += f * ll[u];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) acc[e] += f * o4[u][e];
                     }
             }
-            write_row(r, x % D, acc, to, sum);
+            if (to_outputs) {
+                write_row(r / (16 * MT), r % (16 * MT), x % D, acc, base, sum);
+            } else {
+                gstore((f32x4*)(p.part_o + to * (ROWS * D) + x), acc);
+                if (x % D == 0) sm.ml[0][r][1] = sum;
+            }
+        }
+        if (to_outputs) return;
+        __syncthreads();  // everyone has read the slot's maxima and sums
+        if (sub == 0 && row % (16 * MT) < rows) {
+            gstore(p.part_ml + to * (ROWS * 2) + row * 2, sm.ml[0][row][0]);
+            gstore(p.part_ml + to * (ROWS * 2) + row * 2 + 1, sm.ml[0][row][1]);
         }
     }
     // A worker's slot: its first segment's, or the one of a list that begins
@@ -520,9 +610,9 @@ struct Attend {
     }
 };
 
-template <int DT, int D, int MT, bool SLOTS>
+template <int DT, int D, int MT, bool SLOTS, bool HEADS>
 __global__ __launch_bounds__(NT, MT == 4 ? 1 : 2) void attend_kernel(AttendParams p) {
-    __shared__ AttendShared<D, MT> sm;
+    __shared__ AttendShared<D, MT, HEADS> sm;
     // the row blocks of one share run next to each other on one XCD
     const int32_t per = 8 * p.row_blocks;
     const int32_t w = (int32_t)(blockIdx.x / per) * 8 + (int32_t)(blockIdx.x & 7);
@@ -530,7 +620,7 @@ __global__ __launch_bounds__(NT, MT == 4 ? 1 : 2) void attend_kernel(AttendParam
     if (w >= p.workers) return;
     Share sh;
     if constexpr (SLOTS) {
-        const int32_t each = units_of(place_count<true>(p, 0)) * p.c.kv_heads;
+        const int32_t each = units_of<HEADS>(place_count<true>(p, 0)) * head_units<HEADS>(p.c);
         sh.total = (int64_t)p.c.batch * p.c.draft * each;
         sh.workers = sh.total < p.workers ? (int32_t)sh.total : p.workers;
         if (w >= sh.workers) return;
@@ -539,16 +629,16 @@ __global__ __launch_bounds__(NT, MT == 4 ? 1 : 2) void attend_kernel(AttendParam
         sh.b = (int32_t)(sh.begin / each);
         sh.b_unit = (int64_t)sh.b * each;
     } else {
-        sh = dense_share(p.c, p.workers, w, sm.scan, &sm.found);
+        sh = dense_share<HEADS>(p.c, p.workers, w, sm.scan, &sm.found);
         if (w >= sh.workers) return;
     }
-    Attend<DT, D, MT, SLOTS> a(p, sm, mb);
+    Attend<DT, D, MT, SLOTS, HEADS> a(p, sm, mb);
     int64_t x = sh.begin;
     int32_t b = sh.b;
     int64_t b_unit = sh.b_unit;
     while (x < sh.end) {
         const int32_t units =
-            SLOTS ? units_of(place_count<true>(p, 0)) : units_of(clamped_len(p.c, b));
+            units_of<HEADS>(SLOTS ? place_count<true>(p, 0) : clamped_len(p.c, b));
         const int32_t h = (int32_t)((x - b_unit) / units);
         const int64_t g0 = b_unit + (int64_t)h * units, g1 = g0 + units;
         const int64_t x1 = g1 < sh.end ? g1 : sh.end;
@@ -563,27 +653,32 @@ __global__ __launch_bounds__(NT, MT == 4 ? 1 : 2) void attend_kernel(AttendParam
             a.finish_part(a.part(w, w0, whole_start), w0, w1, whole_start);
         }
         x = x1;
-        if (h + 1 == p.c.kv_heads && x1 == g1) {
+        if (h + 1 == head_units<HEADS>(p.c) && x1 == g1) {
             b_unit = g1;
             ++b;
         }
     }
 }
 
+template <int DT, int D, int MT, bool SLOTS, bool HEADS>
+static hipError_t launch_one(const AttendParams& p, hipStream_t stream) {
+    const uint32_t grid = (uint32_t)((p.workers + 7) / 8 * 8 * p.row_blocks);
+    hipLaunchKernelGGL((attend_kernel<DT, D, MT, SLOTS, HEADS>), dim3(grid), dim3(NT), 0, stream, p);
+    return hipGetLastError();
+}
+
 template <int DT, int D, bool SLOTS>
 static hipError_t launch_mt(int mt, const AttendParams& p, hipStream_t stream) {
-    const uint32_t grid = (uint32_t)((p.workers + 7) / 8 * 8 * p.row_blocks);
-    switch (mt) {
-        case 1:
-            hipLaunchKernelGGL((attend_kernel<DT, D, 1, SLOTS>), dim3(grid), dim3(NT), 0, stream, p);
-            break;
-        case 2:
-            hipLaunchKernelGGL((attend_kernel<DT, D, 2, SLOTS>), dim3(grid), dim3(NT), 0, stream, p);
-            break;
-        default:
-            hipLaunchKernelGGL((attend_kernel<DT, D, 4, SLOTS>), dim3(grid), dim3(NT), 0, stream, p);
+    if constexpr (!SLOTS) {
+        if (p.heads_on_waves)
+            return mt == 1 ? launch_one<DT, D, 1, SLOTS, true>(p, stream)
+                           : launch_one<DT, D, 2, SLOTS, true>(p, stream);
     }
-    return hipGetLastError();
+    switch (mt) {
+        case 1: return launch_one<DT, D, 1, SLOTS, false>(p, stream);
+        case 2: return launch_one<DT, D, 2, SLOTS, false>(p, stream);
+    }
+    return launch_one<DT, D, 4, SLOTS, false>(p, stream);
 }
 
 hipError_t launch_attend(int dtype, int head_dim, int mt, const AttendParams& p,

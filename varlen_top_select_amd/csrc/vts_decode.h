@@ -12,12 +12,13 @@ namespace vts {
 // Drafted tokens of a request, at most: the bits of one tree_mask word.
 constexpr int MAX_DRAFT = 64;
 constexpr int MAX_HEADS = 8192;
-// Positions of one unit of work: four waves of 32.
+// Positions of one unit of work: four waves of 32 (32 where each wave has a KV
+// head of its own).
 constexpr int UNIT = 128;
-// Workgroups that may hold a ticket: the fixed first part of every decode
-// workspace, so that calls of different shapes can share one.
+// Workgroups that may hold a ticket: two words each are the fixed first part of
+// every decode workspace, so that calls of different shapes can share one.
 constexpr int MAX_TICKETS = 8192;
-constexpr size_t TICKET_BYTES = (size_t)MAX_TICKETS * 4;
+constexpr size_t TICKET_BYTES = (size_t)MAX_TICKETS * 2 * 4;
 
 // One of the two caches: rows of head_dim elements, found by page, position in
 // the page and KV head.  Strides are in 16-byte vectors.
@@ -51,9 +52,14 @@ struct AttendParams {
     int32_t rows;      // query rows that share one list of positions: draft * group, or group
     int32_t row_blocks;  // blocks of 16 * MT rows
     int32_t workers;   // workgroups per row block
+    // 1: a workgroup's waves take a KV head each and walk the same places, so that
+    // it reads whole rows of the cache; 0: they take 32 places each of one head
+    int32_t heads_on_waves;
     uint32_t* tickets;
-    float* part_o;   // two per workgroup: [2 * workers * row_blocks][16 * MT][D]
-    float* part_ml;  // two per workgroup: [..][16 * MT][2]
+    // two parts per workgroup, of 16 * MT rows (times four heads): outputs
+    // [..][D], maximum and sum [..][2]
+    float* part_o;
+    float* part_ml;
 };
 
 struct WeighParams {
@@ -69,6 +75,7 @@ struct WeighParams {
     int32_t width;
     int32_t rows;
     int32_t workers;
+    int32_t heads_on_waves;  // as in AttendParams
 };
 
 struct EvictParams {

@@ -103,15 +103,15 @@ int check_q(const void* q, const int64_t* strides) {
 }
 
 struct AttendPlan {
-    int32_t rows, mt, row_blocks, workers;
+    int32_t rows, mt, row_blocks, workers, heads_on_waves;
     size_t part_o, part_ml, total;
 };
 
 // Rows go to blocks of 16, 32 or 64, the smallest that holds them (64 from 33
 // on); workgroups per block of rows: what the compute units hold at once
 // (two workgroups each, one of 64 rows), shared among the blocks.
-int attend_plan(int32_t draft, int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t top_k,
-                AttendPlan* out) {
+int attend_plan(int64_t batch, int32_t draft, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                int32_t top_k, AttendPlan* out) {
     const int32_t group = heads / kv_heads;
     out->rows = top_k > 0 ? group : draft * group;
     out->mt = out->rows <= 16 ? 1 : out->rows <= 32 ? 2 : 4;
@@ -122,7 +122,15 @@ int attend_plan(int32_t draft, int32_t heads, int32_t kv_heads, int32_t head_dim
     out->workers = hold / out->row_blocks;
     if (out->workers < 8) out->workers = 8;
     if (out->workers > MAX_TICKETS / out->row_blocks) out->workers = MAX_TICKETS / out->row_blocks;
-    const size_t parts = 2 * (size_t)out->workers * out->row_blocks * block;
+    // A workgroup that reads whole rows of the cache, four heads of them, reads
+    // faster than one that reads every kv_heads-th 256 bytes (see vts_attend.hip);
+    // 64 rows a head do not fit, and slots lie apart in either case.
+    // The workgroups that share a list leave four times the parts, so not where
+    // many share one.
+    out->heads_on_waves =
+        top_k == 0 && out->mt <= 2 && kv_heads % 4 == 0 && batch * kv_heads >= 128;
+    const size_t parts =
+        2 * (size_t)out->workers * out->row_blocks * block * (out->heads_on_waves ? 4 : 1);
     out->part_o = TICKET_BYTES;
     out->part_ml = out->part_o + align256(parts * head_dim * 4);
     out->total = out->part_ml + align256(parts * 2 * 4);
@@ -144,13 +152,13 @@ int32_t verify_slices(int64_t batch, int64_t vocab) {
 
 extern "C" {
 
-size_t vts_tree_attention_workspace_bytes(int32_t draft, int32_t heads, int32_t kv_heads,
+size_t vts_tree_attention_workspace_bytes(int32_t batch, int32_t draft, int32_t heads, int32_t kv_heads,
                                           int32_t head_dim, int32_t top_k) {
     AttendPlan plan;
-    if (draft < 1 || draft > MAX_DRAFT || kv_heads < 1 || heads < kv_heads ||
+    if (batch < 0 || draft < 1 || draft > MAX_DRAFT || kv_heads < 1 || heads < kv_heads ||
         heads % kv_heads != 0 || heads > MAX_HEADS || head_dim < 1 || head_dim > 1024)
         return 0;
-    if (attend_plan(draft, heads, kv_heads, head_dim, top_k, &plan) != VTS_OK) return 0;
+    if (attend_plan(batch, draft, heads, kv_heads, head_dim, top_k, &plan) != VTS_OK) return 0;
     return plan.total;
 }
 
@@ -173,7 +181,7 @@ int vts_tree_attention(const vts_paged_cache* cache, const void* q, const int64_
     if (out == nullptr || !aligned(out, 16)) return VTS_ERR_INVALID;
     if (lse && (!aligned(lse, 4) || overlap(out, out_bytes, lse, rows * 4))) return VTS_ERR_INVALID;
     AttendPlan plan;
-    st = attend_plan(draft, heads, cache->kv_heads, cache->head_dim, top_k, &plan);
+    st = attend_plan(cache->batch, draft, heads, cache->kv_heads, cache->head_dim, top_k, &plan);
     if (st != VTS_OK) return st;
     if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < plan.total)
         return VTS_ERR_WORKSPACE;
@@ -192,6 +200,7 @@ int vts_tree_attention(const vts_paged_cache* cache, const void* q, const int64_
     p.rows = plan.rows;
     p.row_blocks = plan.row_blocks;
     p.workers = plan.workers;
+    p.heads_on_waves = plan.heads_on_waves;
     char* w = static_cast<char*>(workspace);
     p.tickets = reinterpret_cast<uint32_t*>(w);
     p.part_o = reinterpret_cast<float*>(w + plan.part_o);
@@ -234,6 +243,7 @@ int vts_attention_weight_add(const vts_paged_cache* cache, const void* q,
     p.width = (int32_t)(width > INT32_MAX ? INT32_MAX : width);
     p.rows = draft * p.c.group;
     p.workers = 4 * CUS;
+    p.heads_on_waves = p.c.kv_heads % 4 == 0;
     return launch_weigh(cache->dtype, cache->head_dim, p, static_cast<hipStream_t>(stream)) ==
                    hipSuccess
                ? VTS_OK

@@ -127,13 +127,17 @@ __device__ __forceinline__ uint32_t from_lane(uint32_t v, int lane) {
     return (uint32_t)__builtin_amdgcn_ds_bpermute(lane << 2, (int)v);
 }
 
-template <class V>
+template <class V, bool ONCE = false>
 __device__ __forceinline__ V row_load(const void* base, uint32_t off16, uint32_t byte) {
-    return *(const VTS_GLOBAL V*)((const VTS_GLOBAL char*)base + ((uint64_t)off16 << 4) + byte);
+    const VTS_GLOBAL V* at =
+        (const VTS_GLOBAL V*)((const VTS_GLOBAL char*)base + ((uint64_t)off16 << 4) + byte);
+    if constexpr (ONCE) return __builtin_nontemporal_load(at);  // read by nobody else
+    return *at;
 }
 
-// ---- shares of the work: units of UNIT places, in order of request and KV
-// head; worker w of W takes units [w * total / W, (w + 1) * total / W).
+// ---- shares of the work: units of `UNIT` places (of 32 where the four waves
+// take a KV head each), in order of request and KV head (or four heads);
+// worker w of W takes units [w * total / W, (w + 1) * total / W).
 
 __device__ __forceinline__ int64_t share_start(int64_t total, int32_t workers, int32_t w) {
     return total * w / workers;
@@ -143,8 +147,15 @@ __device__ __forceinline__ int32_t share_of(int64_t total, int32_t workers, int6
     return (int32_t)(((x + 1) * workers - 1) / total);
 }
 
+template <bool HEADS>
 __device__ __forceinline__ int32_t units_of(int32_t count) {
-    return count <= 0 ? 1 : (count + UNIT - 1) / UNIT;
+    constexpr int32_t U = HEADS ? 32 : UNIT;
+    return count <= 0 ? 1 : (count + U - 1) / U;
+}
+// units that differ by KV head alone
+template <bool HEADS>
+__device__ __forceinline__ int32_t head_units(const PagedParams& c) {
+    return HEADS ? c.kv_heads / WAVES : c.kv_heads;
 }
 
 // Sum over the block of one value per thread, and the sum over the threads
@@ -179,13 +190,15 @@ struct Share {
 };
 
 // Shares over the batch's dense lengths.  Every thread of the block calls it.
+template <bool HEADS>
 __device__ __forceinline__ Share dense_share(const PagedParams& c, int32_t workers, int32_t w,
                                              int64_t* sm, int32_t* found) {
     Share s;
+    const int32_t heads = head_units<HEADS>(c);
     int64_t total = 0, sum = 0;
     for (int32_t b0 = 0; b0 < c.batch; b0 += NT) {
         const int32_t b = b0 + (int32_t)threadIdx.x;
-        const int64_t u = b < c.batch ? (int64_t)units_of(clamped_len(c, b)) * c.kv_heads : 0;
+        const int64_t u = b < c.batch ? (int64_t)units_of<HEADS>(clamped_len(c, b)) * heads : 0;
         block_prefix(u, sm, sum);
         total += sum;
     }
@@ -202,7 +215,7 @@ __device__ __forceinline__ Share dense_share(const PagedParams& c, int32_t worke
     int64_t base = 0;
     for (int32_t b0 = 0; b0 < c.batch; b0 += NT) {
         const int32_t b = b0 + (int32_t)threadIdx.x;
-        const int64_t u = b < c.batch ? (int64_t)units_of(clamped_len(c, b)) * c.kv_heads : 0;
+        const int64_t u = b < c.batch ? (int64_t)units_of<HEADS>(clamped_len(c, b)) * heads : 0;
         const int64_t at = base + block_prefix(u, sm, sum);
         if (s.begin >= at && s.begin < at + u) {
             found[0] = b;

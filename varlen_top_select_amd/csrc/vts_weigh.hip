@@ -15,22 +15,24 @@ struct WeighShared {
     int32_t found;
 };
 
-template <int DT, int D>
+template <int DT, int D, bool HEADS>
 __global__ __launch_bounds__(NT, 2) void weigh_kernel(WeighParams p) {
     constexpr int KS = D / 32;
     __shared__ WeighShared sm;
     const PagedParams& c = p.c;
-    const Share sh = dense_share(c, p.workers, (int32_t)blockIdx.x, sm.scan, &sm.found);
+    const Share sh = dense_share<HEADS>(c, p.workers, (int32_t)blockIdx.x, sm.scan, &sm.found);
     if ((int32_t)blockIdx.x >= sh.workers) return;
-    const int lane = lane_id(), wave = threadIdx.x >> 6, col = lane & 15, grp = lane >> 4;
+    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = lane & 15, grp = lane >> 4;
     int64_t x = sh.begin;
     int32_t b = sh.b;
     int64_t b_unit = sh.b_unit;
     while (x < sh.end) {
         const int32_t n = clamped_len(c, b);
-        const int32_t units = units_of(n);
-        const int32_t h = (int32_t)((x - b_unit) / units);
-        const int64_t g0 = b_unit + (int64_t)h * units, g1 = g0 + units;
+        const int32_t units = units_of<HEADS>(n);
+        const int32_t hu = (int32_t)((x - b_unit) / units);
+        const int32_t h = HEADS ? hu * WAVES + wave : hu;
+        const int64_t g0 = b_unit + (int64_t)hu * units, g1 = g0 + units;
         const int64_t x1 = g1 < sh.end ? g1 : sh.end;
         Places pl;
         pl.count = n;
@@ -42,7 +44,7 @@ __global__ __launch_bounds__(NT, 2) void weigh_kernel(WeighParams p) {
         const char* kbase = (const char*)c.k.base + (((uint64_t)h * c.k.head_stride) << 4);
         float* wrow = p.weights + b * p.w_batch + h * p.w_head;
         for (int32_t u = (int32_t)(x - g0); u < (int32_t)(x1 - g0); ++u) {
-            const int32_t j0 = u * UNIT + wave * 32;
+            const int32_t j0 = HEADS ? u * 32 : u * UNIT + wave * 32;
             const Entry e = issue_entry<false>(c, pl, j0 + (lane & 31));
             const uint32_t off =
                 resolve_entry<false>(c, c.k.page_stride, c.k.pos_stride, e);
@@ -55,7 +57,7 @@ __global__ __launch_bounds__(NT, 2) void weigh_kernel(WeighParams p) {
                 const uint32_t r = from_lane(safe, hh * 16 + col);
 #pragma unroll
                 for (int s = 0; s < KS; ++s)
-                    k[hh][s] = row_load<u32x4>(kbase, r, s * 64 + grp * 16);
+                    k[hh][s] = row_load<u32x4, HEADS>(kbase, r, s * 64 + grp * 16);
             }
             float acc[8];
 #pragma unroll
@@ -108,27 +110,27 @@ __global__ __launch_bounds__(NT, 2) void weigh_kernel(WeighParams p) {
             }
         }
         x = x1;
-        if (h + 1 == c.kv_heads && x1 == g1) {
+        if (hu + 1 == head_units<HEADS>(c) && x1 == g1) {
             b_unit = g1;
             ++b;
         }
     }
 }
 
-hipError_t launch_weigh(int dtype, int head_dim, const WeighParams& p, hipStream_t stream) {
+template <int DT, int D>
+static hipError_t launch_dt(const WeighParams& p, hipStream_t stream) {
     const dim3 grid((uint32_t)p.workers), block(NT);
-    if (dtype == BF16) {
-        if (head_dim == 64)
-            hipLaunchKernelGGL((weigh_kernel<BF16, 64>), grid, block, 0, stream, p);
-        else
-            hipLaunchKernelGGL((weigh_kernel<BF16, 128>), grid, block, 0, stream, p);
-    } else {
-        if (head_dim == 64)
-            hipLaunchKernelGGL((weigh_kernel<F16, 64>), grid, block, 0, stream, p);
-        else
-            hipLaunchKernelGGL((weigh_kernel<F16, 128>), grid, block, 0, stream, p);
-    }
+    if (p.heads_on_waves)
+        hipLaunchKernelGGL((weigh_kernel<DT, D, true>), grid, block, 0, stream, p);
+    else
+        hipLaunchKernelGGL((weigh_kernel<DT, D, false>), grid, block, 0, stream, p);
     return hipGetLastError();
+}
+
+hipError_t launch_weigh(int dtype, int head_dim, const WeighParams& p, hipStream_t stream) {
+    if (dtype == BF16)
+        return head_dim == 64 ? launch_dt<BF16, 64>(p, stream) : launch_dt<BF16, 128>(p, stream);
+    return head_dim == 64 ? launch_dt<F16, 64>(p, stream) : launch_dt<F16, 128>(p, stream);
 }
 
 }  // namespace vts

@@ -153,7 +153,8 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
                         device=device) if out is None else out
         lse = torch.empty((batch, draft, heads), dtype=torch.float32,
                           device=device) if return_lse else None
-        need = lib.vts_tree_attention_workspace_bytes(draft, heads, kv_heads, head_dim, top_k)
+        need = lib.vts_tree_attention_workspace_bytes(batch, draft, heads, kv_heads, head_dim,
+                                                      top_k)
         ws = _workspace(workspace, need, device, sp)
         _check("vts_tree_attention", lib.vts_tree_attention(
             cache, q.data_ptr(), q_strides, draft, heads, mask_ptr, slots_ptr, top_k, scale,
@@ -315,7 +316,7 @@ def declare(lib):
     vp, i32, i64, sz, f32 = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t,
                              ctypes.c_float)
     lib.vts_tree_attention_workspace_bytes.restype = sz
-    lib.vts_tree_attention_workspace_bytes.argtypes = [i32] * 5
+    lib.vts_tree_attention_workspace_bytes.argtypes = [i32] * 6
     lib.vts_tree_attention.restype = ctypes.c_int
     lib.vts_tree_attention.argtypes = [vp, vp, vp, i32, i32, vp, vp, i32, f32, vp, vp, vp, sz, vp]
     lib.vts_attention_weight_add.restype = ctypes.c_int
