@@ -24,6 +24,8 @@ struct AttendShared {
     static constexpr int ROWS = (HEADS ? WAVES : 1) * 16 * MT;
     // query rows as operands, from 32 rows on
     u32x4 q[MT > 1 ? (HEADS ? WAVES : 1) * MT * (D / 32) : 1][64];
+    // a wave's K rows on their way from the order of whole rows to operands
+    u32x4 k[MT <= 2 ? WAVES : 1][MT <= 2 ? 32 * (D / 8) : 1];
     // padded: the 16 rows of a store fall on all banks
     float o[HEADS ? 1 : 2][HEADS ? 1 : 16 * MT][D + 4];
     float ml[HEADS ? 1 : WAVES][ROWS][2];
@@ -50,6 +52,13 @@ struct Attend {
     int32_t req, head_unit, mb, t0;  // t0: the row of a slot list
     Places pl;
     static constexpr bool QL = MT > 1;  // query rows in LDS
+    // K through LDS: a load instruction then takes whole rows (as the operand's
+    // order it would take 64 bytes of each of 16), which the memory gives 8 % faster
+    // (64 requests up to 16384: 454 us for 492); with 64 rows to multiply the
+    // time is not the memory's.
+    static constexpr bool KL = MT <= 2;
+    static constexpr int CH = D / 8;        // 16-byte chunks of a row
+    static constexpr int RPL = 64 / CH;     // rows of one load instruction
     u32x4 q[QL ? 1 : KS];
     uint64_t bits[MT];
     f32x4 o[MT][NTILE];
@@ -158,12 +167,38 @@ struct Attend {
     }
     __device__ __forceinline__ void load_k(uint32_t off) {
         const uint32_t safe = off == NO_PLACE ? 0 : off;
+        if constexpr (KL) {
+#pragma unroll
+            for (int i = 0; i < 2 * KS; ++i)
+                k[i / KS][i % KS] = row_load<u32x4, HEADS>(
+                    kbase, from_lane(safe, i * RPL + lane / CH), (lane % CH) * 16);
+            return;
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const uint32_t r = from_lane(safe, h * 16 + col);
 #pragma unroll
             for (int s = 0; s < KS; ++s) k[h][s] = row_load<u32x4, HEADS>(kbase, r, s * 64 + grp * 16);
         }
+    }
+    // Chunk c of row r lies at chunk c ^ swizzle(r) of the row, so that neither the
+    // stores (whole rows) nor the loads (one chunk of 16 rows) meet in a bank.
+    static __device__ __forceinline__ int swizzle(int r) { return D == 128 ? r & 15 : (r >> 1) & 7; }
+    __device__ __forceinline__ void stage_k() {
+#pragma unroll
+        for (int i = 0; i < 2 * KS; ++i) {
+            const int r = i * RPL + lane / CH;
+            sm.k[wave][r * CH + ((lane % CH) ^ swizzle(r))] = k[i / KS][i % KS];
+        }
+        // the wave's own stores come before its loads; the compiler has to know
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    }
+    __device__ __forceinline__ u32x4 operand_k(int h, int s) const {
+        if constexpr (!KL) return k[h][s];
+        const int r = h * 16 + col;
+        return sm.k[wave][r * CH + ((s * 4 + grp) ^ swizzle(r))];
     }
     // register j: place 4 * grp + j of the first half, or of the second for j >= 4
     __device__ __forceinline__ int v_place(int j) const {
@@ -261,6 +296,10 @@ struct Attend {
         const float c = p.scale_log2e;
         const bool masked = have != ~0u || drafted;
         u32x4 pv[MT];
+        if constexpr (KL) {
+            stage_k();
+            if (more) load_k(off_next);
+        }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             f32x4 s[2];
@@ -269,9 +308,9 @@ struct Attend {
                 s[h] = f32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
-                    s[h] = mfma<DT>(k[h][ks], QL ? sm.q[q_at(mt, ks)][lane] : q[QL ? 0 : ks], s[h]);
+                    s[h] = mfma<DT>(operand_k(h, ks), QL ? sm.q[q_at(mt, ks)][lane] : q[QL ? 0 : ks], s[h]);
             }
-            if (mt == MT - 1 && more) load_k(off_next);
+            if (!KL && mt == MT - 1 && more) load_k(off_next);
 #pragma unroll
             for (int e = 0; e < 8; ++e) s[e >> 2][e & 3] *= c;
             if (masked) {
@@ -325,6 +364,8 @@ struct Attend {
         second_product(pv);
         if (bad) add_rows(bad, off, j0, pv);
         if (more) load_v(off_next);
+        // the next tile's stores to sm.k come after these loads
+        if constexpr (KL) __builtin_amdgcn_wave_barrier();
     }
 
     // Units [u0, u1) of the places, this wave's 32 of each.
@@ -611,7 +652,7 @@ struct Attend {
 };
 
 template <int DT, int D, int MT, bool SLOTS, bool HEADS>
-__global__ __launch_bounds__(NT, MT == 4 ? 1 : 2) void attend_kernel(AttendParams p) {
+__global__ __launch_bounds__(NT, 1) void attend_kernel(AttendParams p) {
     __shared__ AttendShared<D, MT, HEADS> sm;
     // the row blocks of one share run next to each other on one XCD
     const int32_t per = 8 * p.row_blocks;
