@@ -59,6 +59,10 @@ struct Attend {
     static constexpr bool KL = MT <= 2;
     static constexpr int CH = D / 8;        // 16-byte chunks of a row
     static constexpr int RPL = 64 / CH;     // rows of one load instruction
+    // With 64 rows O is kept in accumulation registers (the empty asm in tile()):
+    // left to itself the compiler keeps it where the rare rescaling wants it
+    // and copies it to and from the matrix instructions in every tile.
+    static constexpr bool OA = MT == 4;
     u32x4 q[QL ? 1 : KS];
     uint64_t bits[MT];
     f32x4 o[MT][NTILE];
@@ -131,6 +135,8 @@ struct Attend {
                 u32x4 x = {0, 0, 0, 0};
                 if (QL && !HEADS && (mt * KS + s) % WAVES != wave) continue;
                 if (ok) x = gload((const u32x4*)(at + s * 64 + grp * 16));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] ^= p.q_sign;
                 if constexpr (QL)
                     sm.q[q_at(mt, s)][lane] = x;
                 else
@@ -295,43 +301,60 @@ struct Attend {
                                          bool more, uint32_t off_next) {
         const float c = p.scale_log2e;
         const bool masked = have != ~0u || drafted;
-        u32x4 pv[MT];
         if constexpr (KL) {
             stage_k();
             if (more) load_k(off_next);
         }
+        f32x4 s[MT][2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            f32x4 s[2];
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                s[h] = f32x4{0, 0, 0, 0};
+            for (int h = 0; h < 2; ++h) s[mt][h] = f32x4{0, 0, 0, 0};
+        // step by step over all rows, so that independent products stand between
+        // dependent ones
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks)
-                    s[h] = mfma<DT>(operand_k(h, ks), QL ? sm.q[q_at(mt, ks)][lane] : q[QL ? 0 : ks], s[h]);
+        for (int ks = 0; ks < KS; ++ks) {
+            const u32x4 k0 = operand_k(0, ks), k1 = operand_k(1, ks);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const u32x4 qq = QL ? sm.q[q_at(mt, ks)][lane] : q[QL ? 0 : ks];
+                s[mt][0] = mfma<DT>(k0, qq, s[mt][0]);
+                s[mt][1] = mfma<DT>(k1, qq, s[mt][1]);
             }
-            if (!KL && mt == MT - 1 && more) load_k(off_next);
+        }
+        if (!KL && more) load_k(off_next);
+        if (masked) {
+            int g = grp;  // opaque: nothing of this is kept in registers between tiles
+            asm volatile("" : "+v"(g));
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s[e >> 2][e & 3] *= c;
-            if (masked) {
-                int g = grp;  // opaque: nothing of this is kept in registers between tiles
-                asm volatile("" : "+v"(g));
+            for (int e = 0; e < 8; ++e) {
+                const int kk = (e >> 2) * 16 + g * 4 + (e & 3);
+                const int32_t i = j0 + kk - pl.first;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int kk = (e >> 2) * 16 + g * 4 + (e & 3);
-                    const int32_t i = j0 + kk - pl.first;
+                for (int mt = 0; mt < MT; ++mt) {
                     const uint32_t see = (have >> kk) & (((uint32_t)i >> 31) |
                                                          (uint32_t)(bits[mt] >> (i & 63)));
-                    s[e >> 2][e & 3] = (see & 1u) ? s[e >> 2][e & 3] : NEG_INF;
+                    s[mt][e >> 2][e & 3] = (see & 1u) ? s[mt][e >> 2][e & 3] : NEG_INF;
                 }
             }
-            float top = NEG_INF;
+        }
+        float top[MT];
+        bool past = false;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) top = fmaxf(top, s[e >> 2][e & 3]);
-            if (ballot(top > m[mt] + 8.0f)) {
-                top = fmaxf(top, __shfl_xor(top, 16));
-                top = fmaxf(top, __shfl_xor(top, 32));
-                const float up = fmaxf(top, m[mt]);
+        for (int mt = 0; mt < MT; ++mt) {
+            top[mt] = NEG_INF;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top[mt] = fmaxf(top[mt], s[mt][e >> 2][e & 3]);
+            top[mt] *= c;
+            past = past || top[mt] > m[mt] + 8.0f;
+        }
+        if (ballot(past)) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                float up = fmaxf(top[mt], __shfl_xor(top[mt], 16));
+                up = fmaxf(up, __shfl_xor(up, 32));
+                // (a row that is not past its maximum keeps it)
+                up = up > m[mt] + 8.0f ? up : m[mt];
                 const float f = up == NEG_INF ? 1.0f : __builtin_amdgcn_exp2f(m[mt] - up);
                 m[mt] = up;
                 l[mt] *= f;
@@ -340,11 +363,22 @@ struct Attend {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[mt][n][e] *= f;
             }
+        }
+        if constexpr (OA)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int n = 0; n < NTILE; ++n) asm volatile("" : "+a"(o[mt][n]));
+        u32x4 pv[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
             const float base = m[mt] == NEG_INF ? 0.0f : m[mt];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float a = __builtin_amdgcn_exp2f(s[e >> 1][2 * (e & 1)] - base);
-                const float b = __builtin_amdgcn_exp2f(s[e >> 1][2 * (e & 1) + 1] - base);
+                const float a =
+                    __builtin_amdgcn_exp2f(fmaf(s[mt][e >> 1][2 * (e & 1)], c, -base));
+                const float b =
+                    __builtin_amdgcn_exp2f(fmaf(s[mt][e >> 1][2 * (e & 1) + 1], c, -base));
                 l[mt] += a + b;
                 pv[mt][e] = pack2<DT>(a, b);
             }

@@ -45,7 +45,8 @@ struct AttendParams {
     const int64_t* tree_mask;        // [batch, draft] or null (chain)
     const int32_t* slots;            // [batch * draft, top_k] or null
     int32_t top_k;
-    float scale_log2e;
+    float scale_log2e;  // > 0: a negative scale's sign goes to q, and 0 is the least normal
+    uint32_t q_sign;    // 0x80008000 for a negative scale
     void* out;
     float* lse;  // or null
     // plan

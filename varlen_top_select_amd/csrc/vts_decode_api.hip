@@ -2,6 +2,7 @@
 // paged cache, accumulated attention weight, eviction, draft verification):
 // argument checks on the host before any HIP call, plans that are pure functions
 // of the shape, and the launches.
+#include <float.h>
 #include <math.h>
 #include <string.h>
 
@@ -195,7 +196,9 @@ int vts_tree_attention(const vts_paged_cache* cache, const void* q, const int64_
     p.tree_mask = tree_mask;
     p.slots = slots;
     p.top_k = top_k;
-    p.scale_log2e = (float)((double)scale * 1.4426950408889634);
+    p.scale_log2e = (float)(fabs((double)scale) * 1.4426950408889634);
+    if (p.scale_log2e < FLT_MIN) p.scale_log2e = FLT_MIN;  // (0 * -inf is no -inf)
+    p.q_sign = scale < 0 ? 0x80008000u : 0;
     p.out = out;
     p.lse = lse;
     p.rows = plan.rows;
