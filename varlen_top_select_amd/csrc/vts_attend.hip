@@ -41,7 +41,7 @@ struct Attend {
     static constexpr int VB = D / 16 * 2;   // bytes of a V row per lane
     static constexpr int VW = VB / 4;       // words of a V row per lane
     static constexpr int NTILE = D / 16;    // 16-row tiles of the second product
-    static constexpr int JOIN = 16;         // parts joined by one workgroup
+    static constexpr int JOIN = 32;         // parts joined by one workgroup
     static constexpr int ROWS = AttendShared<D, MT, HEADS>::ROWS;
     using VRow = typename std::conditional<D == 128, u32x4, u32x2>::type;
 
@@ -116,7 +116,7 @@ struct Attend {
             t0 = 0;
             pl.slots = nullptr;
         }
-        const int32_t n = clamped_len(c, req);
+        const int32_t n = uniform_len(c, req);
         pl.table = c.table + (int64_t)req * c.table_stride;
         pl.top_k = p.top_k;
         pl.draft_pos = n - c.draft;
@@ -187,14 +187,11 @@ struct Attend {
             for (int s = 0; s < KS; ++s) k[h][s] = row_load<u32x4, HEADS>(kbase, r, s * 64 + grp * 16);
         }
     }
-    // Chunk c of row r lies at chunk c ^ swizzle(r) of the row, so that neither the
-    // stores (whole rows) nor the loads (one chunk of 16 rows) meet in a bank.
-    static __device__ __forceinline__ int swizzle(int r) { return D == 128 ? r & 15 : (r >> 1) & 7; }
     __device__ __forceinline__ void stage_k() {
 #pragma unroll
         for (int i = 0; i < 2 * KS; ++i) {
             const int r = i * RPL + lane / CH;
-            sm.k[wave][r * CH + ((lane % CH) ^ swizzle(r))] = k[i / KS][i % KS];
+            sm.k[wave][r * CH + ((lane % CH) ^ swizzled<D>(r))] = k[i / KS][i % KS];
         }
         // the wave's own stores come before its loads; the compiler has to know
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -204,7 +201,7 @@ struct Attend {
     __device__ __forceinline__ u32x4 operand_k(int h, int s) const {
         if constexpr (!KL) return k[h][s];
         const int r = h * 16 + col;
-        return sm.k[wave][r * CH + ((s * 4 + grp) ^ swizzle(r))];
+        return sm.k[wave][r * CH + ((s * 4 + grp) ^ swizzled<D>(r))];
     }
     // register j: place 4 * grp + j of the first half, or of the second for j >= 4
     __device__ __forceinline__ int v_place(int j) const {
@@ -713,7 +710,7 @@ __global__ __launch_bounds__(NT, 1) void attend_kernel(AttendParams p) {
     int64_t b_unit = sh.b_unit;
     while (x < sh.end) {
         const int32_t units =
-            units_of<HEADS>(SLOTS ? place_count<true>(p, 0) : clamped_len(p.c, b));
+            units_of<HEADS>(SLOTS ? place_count<true>(p, 0) : uniform_len(p.c, b));
         const int32_t h = (int32_t)((x - b_unit) / units);
         const int64_t g0 = b_unit + (int64_t)h * units, g1 = g0 + units;
         const int64_t x1 = g1 < sh.end ? g1 : sh.end;

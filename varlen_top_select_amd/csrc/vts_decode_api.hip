@@ -246,8 +246,8 @@ int vts_attention_weight_add(const vts_paged_cache* cache, const void* q,
     p.w_head = weights_head_stride;
     p.width = (int32_t)(width > INT32_MAX ? INT32_MAX : width);
     p.rows = draft * p.c.group;
-    p.workers = 4 * CUS;
-    p.heads_on_waves = p.c.kv_heads % 4 == 0;
+    p.heads_on_waves = p.c.kv_heads % 4 == 0 && p.rows <= 64;
+    p.workers = 2 * CUS;
     return launch_weigh(cache->dtype, cache->head_dim, p, static_cast<hipStream_t>(stream)) ==
                    hipSuccess
                ? VTS_OK

@@ -72,6 +72,10 @@ __device__ __forceinline__ int32_t clamped_len(const PagedParams& c, int32_t b) 
     const int32_t n = gload(c.seq_lens + b);
     return n < 0 ? 0 : n > c.capacity ? c.capacity : n;
 }
+// the same of a request that is the same in every lane, as a scalar
+__device__ __forceinline__ int32_t uniform_len(const PagedParams& c, int32_t b) {
+    return __builtin_amdgcn_readfirstlane(clamped_len(c, b));
+}
 
 template <bool SLOTS>
 __device__ __forceinline__ int32_t place_count(const AttendParams& p, int32_t n) {
@@ -135,6 +139,14 @@ __device__ __forceinline__ V row_load(const void* base, uint32_t off16, uint32_t
     return *at;
 }
 
+// K rows on their way from the order of whole rows to operands, in LDS: chunk c
+// (16 bytes) of row r lies at chunk c ^ swizzled(r) of the row, so that neither
+// the stores (whole rows) nor the loads (one chunk of 16 rows) meet in a bank.
+template <int D>
+__device__ __forceinline__ int swizzled(int r) {
+    return D == 128 ? r & 15 : (r >> 1) & 7;
+}
+
 // ---- shares of the work: units of `UNIT` places (of 32 where the four waves
 // take a KV head each), in order of request and KV head (or four heads);
 // worker w of W takes units [w * total / W, (w + 1) * total / W).
@@ -189,33 +201,57 @@ struct Share {
     int32_t workers;
 };
 
+// a value that is the same in every lane, as a scalar
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+    const uint32_t lo = first_lane_value((uint32_t)v), hi = first_lane_value((uint32_t)(v >> 32));
+    return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
 // Shares over the batch's dense lengths.  Every thread of the block calls it.
 template <bool HEADS>
 __device__ __forceinline__ Share dense_share(const PagedParams& c, int32_t workers, int32_t w,
                                              int64_t* sm, int32_t* found) {
     Share s;
     const int32_t heads = head_units<HEADS>(c);
+    const auto units = [&](int32_t b) -> int64_t {
+        return b < c.batch ? (int64_t)units_of<HEADS>(clamped_len(c, b)) * heads : 0;
+    };
     int64_t total = 0, sum = 0;
-    for (int32_t b0 = 0; b0 < c.batch; b0 += NT) {
-        const int32_t b = b0 + (int32_t)threadIdx.x;
-        const int64_t u = b < c.batch ? (int64_t)units_of<HEADS>(clamped_len(c, b)) * heads : 0;
-        block_prefix(u, sm, sum);
-        total += sum;
-    }
-    s.total = total;
-    s.workers = total < workers ? (int32_t)total : workers;
-    if (w >= s.workers) {
-        s.begin = s.end = 0;
+    if (c.batch <= 64) {  // a request to a lane; every wave finds the same
+        const int lane = lane_id();
+        const int64_t u = units(lane);
+        int64_t inc = u;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int64_t o = __shfl_up(inc, d);
+            if (lane >= d) inc += o;
+        }
+        s.total = uniform64(__shfl(inc, 63));
+        s.workers = s.total < workers ? (int32_t)s.total : workers;
+        s.begin = s.end = s.b_unit = 0;
         s.b = 0;
-        s.b_unit = 0;
+        if (w >= s.workers) return s;
+        s.begin = share_start(s.total, s.workers, w);
+        s.end = share_start(s.total, s.workers, w + 1);
+        s.b = __builtin_ctzll(ballot(s.begin < inc));
+        s.b_unit = uniform64(__shfl(inc - u, s.b));
         return s;
     }
+    for (int32_t b0 = 0; b0 < c.batch; b0 += NT) {
+        block_prefix(units(b0 + (int32_t)threadIdx.x), sm, sum);
+        total += sum;
+    }
+    s.total = total = uniform64(total);
+    s.workers = total < workers ? (int32_t)total : workers;
+    s.begin = s.end = s.b_unit = 0;
+    s.b = 0;
+    if (w >= s.workers) return s;
     s.begin = share_start(total, s.workers, w);
     s.end = share_start(total, s.workers, w + 1);
     int64_t base = 0;
     for (int32_t b0 = 0; b0 < c.batch; b0 += NT) {
         const int32_t b = b0 + (int32_t)threadIdx.x;
-        const int64_t u = b < c.batch ? (int64_t)units_of<HEADS>(clamped_len(c, b)) * heads : 0;
+        const int64_t u = units(b);
         const int64_t at = base + block_prefix(u, sm, sum);
         if (s.begin >= at && s.begin < at + u) {
             found[0] = b;
@@ -225,7 +261,7 @@ __device__ __forceinline__ Share dense_share(const PagedParams& c, int32_t worke
     }
     __syncthreads();
     s.b = __builtin_amdgcn_readfirstlane(found[0]);
-    s.b_unit = sm[WAVES];
+    s.b_unit = uniform64(sm[WAVES]);
     __syncthreads();
     return s;
 }
