@@ -95,6 +95,16 @@ struct EvictParams {
     float* out_weights;
 };
 
+// A request's walk between two launches.
+struct VerifyState {
+    int32_t cur, next, steps;
+    int32_t more;  // 0: ended
+    int32_t sums;  // which half of VerifyParams::sums holds the residual's
+    int32_t pad;
+    double a, mass;
+    int32_t path[MAX_DRAFT];
+};
+
 struct VerifyParams {
     const void* target;
     int64_t target_batch, target_row;
@@ -109,7 +119,8 @@ struct VerifyParams {
     int32_t* count;  // [batch]
     int32_t* token;  // [batch]
     uint32_t* tickets;
-    double* sums;    // [batch][16 * slices]
+    double* sums;    // [2][batch][16 * slices]
+    VerifyState* states;  // [batch][2]
 };
 
 hipError_t launch_attend(int dtype, int head_dim, int mt, const AttendParams& p, hipStream_t stream);

@@ -139,15 +139,29 @@ int attend_plan(int64_t batch, int32_t draft, int32_t heads, int32_t kv_heads, i
     return VTS_OK;
 }
 
-// Workgroups per request: as many as the device holds at once (two of 16 waves
-// on each compute unit), of at least 4096 values each.
+// Workgroups per request: as many as the device holds at once (one of 16 waves
+// on each compute unit; with two rounds of them 64 requests of 131072 fp32 took
+// 49 us for 33), of at least 4096 values each.
 int32_t verify_slices(int64_t batch, int64_t vocab) {
     if (batch < 1 || batch > MAX_TICKETS) return 1;
-    int64_t s = 2 * CUS / batch;
+    int64_t s = CUS / batch;
     const int64_t most = (vocab + 4095) / 4096;
     if (s > most) s = most;
     if (s > 64) s = 64;  // 1024 segments, one to a thread of the joining workgroup
     return s < 1 ? 1 : (int32_t)s;
+}
+
+struct VerifyLayout {
+    size_t sums, states, total;
+};
+
+VerifyLayout verify_layout(int64_t batch, int64_t vocab) {
+    const size_t n = batch < 1 ? 1 : (size_t)batch;
+    VerifyLayout v;
+    v.sums = TICKET_BYTES;
+    v.states = v.sums + align256(2 * n * verify_slices(batch, vocab) * 16 * sizeof(double));
+    v.total = v.states + align256(2 * n * sizeof(VerifyState));
+    return v;
 }
 
 }  // namespace
@@ -310,8 +324,7 @@ int vts_evict_cache(const vts_paged_cache* cache, const float* weights,
 }
 
 size_t vts_verify_draft_workspace_bytes(int64_t batch, int64_t vocab) {
-    const int64_t n = batch < 1 ? 1 : batch;
-    return TICKET_BYTES + align256((size_t)n * verify_slices(batch, vocab) * 16 * 8);
+    return verify_layout(batch, vocab).total;
 }
 
 int vts_verify_draft(const void* target_probs, int32_t dtype, int64_t target_batch_stride,
@@ -336,7 +349,7 @@ int vts_verify_draft(const void* target_probs, int32_t dtype, int64_t target_bat
         next_token == nullptr)
         return VTS_ERR_INVALID;
     if (workspace == nullptr || !aligned(workspace, 16) ||
-        workspace_bytes < vts_verify_draft_workspace_bytes(batch, vocab))
+        workspace_bytes < verify_layout(batch, vocab).total)
         return VTS_ERR_WORKSPACE;
     const int st = check_device(stream);
     if (st != VTS_OK) return st;
@@ -360,7 +373,9 @@ int vts_verify_draft(const void* target_probs, int32_t dtype, int64_t target_bat
     p.token = next_token;
     char* w = static_cast<char*>(workspace);
     p.tickets = reinterpret_cast<uint32_t*>(w);
-    p.sums = reinterpret_cast<double*>(w + TICKET_BYTES);
+    const VerifyLayout layout = verify_layout(batch, vocab);
+    p.sums = reinterpret_cast<double*>(w + layout.sums);
+    p.states = reinterpret_cast<VerifyState*>(w + layout.states);
     return launch_verify(dtype, p, static_cast<hipStream_t>(stream)) == hipSuccess ? VTS_OK
                                                                                   : VTS_ERR_HIP;
 }

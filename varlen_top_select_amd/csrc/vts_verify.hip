@@ -15,14 +15,19 @@
 // as far as it goes without a sum, which is a few dozen scalars and gives all
 // the same state, and every wave sums one segment of the vocabulary; the last
 // workgroup to arrive joins the sums in order, finishes the walk, and scans the
-// one segment that the token lies in.  A sum that the rest of the walk needs
-// (a second rejection) it takes alone, a sixteenth of the row to a wave.
+// one segment that the token lies in.  A chain needs no other sum.  In a tree of
+// drawn tokens a rejection's sum decides over the next sibling, so there the
+// walk goes in ROUNDS launches that each end with a sum by all workgroups, and
+// a last one of one workgroup per request that takes what sums are left alone, a
+// sixteenth of the row to a wave (10 us for 100003 bf16; with all but the first
+// sum taken so, 16 trees of 24 took 80 us).
 #include "vts_paged.hpp"
 
 namespace vts {
 
 constexpr int VT = 1024;  // threads
 constexpr int VW = VT / 64;
+constexpr int ROUNDS = 3;  // launches of a tree's walk that end with a sum by all
 
 // a 16-byte load from any element's address
 typedef u32x4 Unaligned __attribute__((aligned(2)));
@@ -173,7 +178,7 @@ struct Verify {
         if (k.a > 0) {
 #pragma unroll
             for (int i = 0; i < VE; ++i)
-                r[i] = fmax((double)prob(f.x[i]) - k.a * (double)prob(f.y[i]), 0.0);
+                r[i] = fmax((double)f.x[i] - k.a * (double)prob(f.y[i]), 0.0);  // NaN: 0
         } else {
 #pragma unroll
             for (int i = 0; i < VE; ++i) r[i] = prob(f.x[i]);
@@ -300,8 +305,7 @@ struct Verify {
         return tail;
     }
 
-    __device__ __forceinline__ void run(int32_t slice) {
-        gather();
+    static __device__ __forceinline__ Walk root() {
         Walk k;
         k.cur = -1;
         k.next = 0;
@@ -309,9 +313,15 @@ struct Verify {
         k.a = 0;
         k.mass = 1;
         k.gone = 0;
-        bool more = advance(k);
+        return k;
+    }
+
+    __device__ __forceinline__ void run(int32_t slice) {
+        gather();
+        Walk k = root();
+        const bool more = advance(k);
         const int wave = threadIdx.x >> 6;
-        int32_t segments = p.slices * VW;  // whose sums are in sm.sums
+        const int32_t segments = p.slices * VW;
         if (p.slices > 1) {
             double* sums = p.sums + (int64_t)b * segments;
             const double mine = sum_segment(k, segments, slice * VW + wave);
@@ -338,6 +348,82 @@ struct Verify {
         } else {
             sum_alone(k);
         }
+        finish(k, more, segments);
+    }
+
+    // Round `r` of the walk: its state and sums come from the round before (of
+    // the other parity) and go to the next.
+    __device__ __forceinline__ void round(int32_t slice, int32_t r) {
+        const int wave = threadIdx.x >> 6;
+        const int32_t segments = p.slices * VW;
+        Walk k = root();
+        bool more;
+        VerifyState* to = p.states + 2 * b + (r & 1);
+        if (r == 0) {
+            gather();
+            more = advance(k);
+        } else {
+            const VerifyState* from = p.states + 2 * b + (~r & 1);
+            if (!gload(&from->more)) {  // ended: the state goes on as it is
+                if (slice == 0 && threadIdx.x < sizeof(VerifyState) / 4)
+                    gstore((uint32_t*)to + threadIdx.x, gload((const uint32_t*)from + threadIdx.x));
+                return;
+            }
+            gather();
+            more = load_state(k, from);
+            double total;
+            block_scan((int32_t)threadIdx.x < segments ? sm.sums[threadIdx.x] : 0.0, total);
+            const int32_t cur = k.cur;
+            const double a = k.a;
+            k.mass = total;
+            more = advance(k);
+            if (!more && k.cur == cur && k.a == a) {  // ended, with the sums at hand
+                if (slice == 0) store_state(k, more, gload(&from->sums), to);
+                return;
+            }
+        }
+        double* sums = p.sums + ((int64_t)(r & 1) * p.batch + b) * segments;
+        const double mine = sum_segment(k, segments, slice * VW + wave);
+        if (lane_id() == 0) gstore(sums + slice * VW + wave, mine);
+        if (slice == 0) store_state(k, more, r & 1, to);
+    }
+    __device__ __forceinline__ void last_round(int32_t rounds) {
+        gather();
+        Walk k = root();
+        const bool more = load_state(k, p.states + 2 * b + (~rounds & 1));
+        finish(k, more, p.slices * VW);
+    }
+    __device__ __forceinline__ bool load_state(Walk& k, const VerifyState* from) {
+        k.cur = gload(&from->cur);
+        k.next = gload(&from->next);
+        k.steps = gload(&from->steps);
+        k.a = gload(&from->a);
+        k.mass = gload(&from->mass);
+        if (threadIdx.x < MAX_DRAFT) sm.path[threadIdx.x] = gload(from->path + threadIdx.x);
+        const int32_t segments = p.slices * VW;
+        const double* sums = p.sums + ((int64_t)gload(&from->sums) * p.batch + b) * segments;
+        if ((int32_t)threadIdx.x < segments) sm.sums[threadIdx.x] = gload(sums + threadIdx.x);
+        __syncthreads();
+        return gload(&from->more) != 0;
+    }
+    __device__ __forceinline__ void store_state(const Walk& k, bool more, int32_t sums,
+                                                VerifyState* to) {
+        __syncthreads();
+        if (threadIdx.x < MAX_DRAFT) gstore(to->path + threadIdx.x, sm.path[threadIdx.x]);
+        if (threadIdx.x == 0) {
+            gstore(&to->cur, k.cur);
+            gstore(&to->next, k.next);
+            gstore(&to->steps, k.steps);
+            gstore(&to->more, more ? 1 : 0);
+            gstore(&to->sums, sums);
+            gstore(&to->a, k.a);
+            gstore(&to->mass, k.mass);
+        }
+    }
+
+    // From the sums of the state at hand (`segments` of them in sm.sums) to the
+    // outputs.
+    __device__ __forceinline__ void finish(Walk k, bool more, int32_t segments) {
         double total, inc;
         for (;;) {
             __syncthreads();
@@ -396,14 +482,42 @@ __global__ __launch_bounds__(VT) void verify_kernel(VerifyParams p) {
     v.run(slice);
 }
 
-hipError_t launch_verify(int dtype, const VerifyParams& p, hipStream_t stream) {
+template <int DT>
+__global__ __launch_bounds__(VT) void verify_round_kernel(VerifyParams p, int32_t r) {
+    __shared__ VerifyShared sm;
+    const int32_t b = (int32_t)(blockIdx.x / p.slices), slice = (int32_t)(blockIdx.x % p.slices);
+    Verify<DT> v(p, sm, b);
+    v.round(slice, r);
+}
+
+template <int DT>
+__global__ __launch_bounds__(VT) void verify_last_kernel(VerifyParams p, int32_t rounds) {
+    __shared__ VerifyShared sm;
+    Verify<DT> v(p, sm, (int32_t)blockIdx.x);
+    v.last_round(rounds);
+}
+
+template <int DT>
+static hipError_t launch_dt(const VerifyParams& p, hipStream_t stream) {
     const dim3 grid((uint32_t)p.batch * (uint32_t)p.slices), block(VT);
-    switch (dtype) {
-        case F32: hipLaunchKernelGGL((verify_kernel<F32>), grid, block, 0, stream, p); break;
-        case BF16: hipLaunchKernelGGL((verify_kernel<BF16>), grid, block, 0, stream, p); break;
-        default: hipLaunchKernelGGL((verify_kernel<F16>), grid, block, 0, stream, p);
+    // only a drawn token's rejected sibling makes the walk wait for a sum
+    if (!p.draft_probs || !p.parents || p.draft == 1 || p.slices == 1) {
+        hipLaunchKernelGGL((verify_kernel<DT>), grid, block, 0, stream, p);
+        return hipGetLastError();
     }
+    for (int32_t r = 0; r < ROUNDS; ++r)
+        hipLaunchKernelGGL((verify_round_kernel<DT>), grid, block, 0, stream, p, r);
+    hipLaunchKernelGGL((verify_last_kernel<DT>), dim3((uint32_t)p.batch), block, 0, stream, p,
+                       ROUNDS);
     return hipGetLastError();
+}
+
+hipError_t launch_verify(int dtype, const VerifyParams& p, hipStream_t stream) {
+    switch (dtype) {
+        case F32: return launch_dt<F32>(p, stream);
+        case BF16: return launch_dt<BF16>(p, stream);
+    }
+    return launch_dt<F16>(p, stream);
 }
 
 }  // namespace vts
