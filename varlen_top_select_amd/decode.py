@@ -14,6 +14,7 @@ tokens, as ``next_n`` does in ``topk_varlen``.
 """
 from __future__ import annotations
 
+import functools
 import math
 import struct
 
@@ -29,17 +30,21 @@ _STRIDES = struct.Struct("@qqq")
 MAX_DRAFT = 64
 
 
-def _run(stream, device, call):
-    """call(stream pointer) with `device` and, where one is given, `stream`
+# The checks below run before every launch; sizes and devices are compared as
+# plain numbers, which costs a fraction of comparing torch.device objects.
+
+
+def _run(stream, index, call):
+    """call(stream pointer) with device `index` and, where one is given, `stream`
     current, so that what the call allocates belongs to the stream it runs on."""
     if stream is None:
-        if device.index == torch.cuda.current_device():
-            return call(torch.cuda.current_stream(device).cuda_stream)
-        with torch.cuda.device(device):
-            return call(torch.cuda.current_stream(device).cuda_stream)
+        if index == torch.cuda.current_device():
+            return call(torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.device(index):
+            return call(torch.cuda.current_stream().cuda_stream)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    with torch.cuda.device(device), torch.cuda.stream(stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=index)
+    with torch.cuda.device(index), torch.cuda.stream(stream):
         return call(stream.cuda_stream)
 
 
@@ -51,6 +56,16 @@ def _workspace(workspace, need, device, sp):
     return workspace
 
 
+@functools.lru_cache(maxsize=256)
+def _attention_bytes(batch, draft, heads, kv_heads, head_dim, top_k):
+    return library().vts_tree_attention_workspace_bytes(batch, draft, heads, kv_heads, head_dim, top_k)
+
+
+@functools.lru_cache(maxsize=256)
+def _verify_bytes(batch, vocab):
+    return library().vts_verify_draft_workspace_bytes(batch, vocab)
+
+
 def _cache(name, t, like=None):
     if not isinstance(t, torch.Tensor) or t.dim() != 4:
         raise ValueError(f"{name} must be a 4-D tensor [pages, page_size, kv_heads, head_dim]")
@@ -58,7 +73,7 @@ def _cache(name, t, like=None):
         raise ValueError(f"{name} dtype must be bfloat16 or float16")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on the GPU")
-    if like is not None and (t.dtype is not like.dtype or t.device != like.device):
+    if like is not None and (t.dtype is not like.dtype or t.get_device() != like.get_device()):
         raise ValueError(f"{name} must have the other cache's dtype and device")
     sp, ss, sh, sd = t.stride()
     if sd != 1 or (sp | ss | sh) & 7 or t.data_ptr() & 15:
@@ -67,25 +82,25 @@ def _cache(name, t, like=None):
     return sp, ss, sh
 
 
-def _tensor(name, t, dtype, shape, device):
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device:
-        raise ValueError(f"{name} must be a {dtype} tensor on {device}")
-    if tuple(t.shape) != shape or not t.is_contiguous():
+def _tensor(name, t, dtype, shape, index):
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index:
+        raise ValueError(f"{name} must be a {dtype} tensor on cuda:{index}")
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, of shape {shape}")
     return t
 
 
-def _table(name, t, batch, device):
-    if (not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.device != device
+def _table(name, t, batch, index):
+    if (not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.get_device() != index
             or t.dim() != 2 or t.shape[0] != batch or t.shape[1] < 1 or t.stride(1) != 1):
-        raise ValueError(f"{name} must be an int32 tensor of {batch} contiguous rows on {device}")
+        raise ValueError(f"{name} must be an int32 tensor of {batch} contiguous rows on cuda:{index}")
     return t.stride(0) if batch > 1 else t.shape[1]
 
 
 def _paged(k_cache, v_cache, page_table, seq_lens):
-    """(vts_paged_cache as bytes, device, batch, kv_heads, head_dim)"""
+    """(vts_paged_cache as bytes, device index, batch, kv_heads, head_dim)"""
     ks = _cache("k_cache", k_cache)
-    device = k_cache.device
+    index = k_cache.get_device()
     pages, page_size, kv_heads, head_dim = k_cache.shape
     if v_cache is None:
         vs, vp = ks, 0
@@ -96,19 +111,19 @@ def _paged(k_cache, v_cache, page_table, seq_lens):
     if not isinstance(seq_lens, torch.Tensor) or seq_lens.dim() != 1:
         raise ValueError("seq_lens must be a 1-D tensor")
     batch = seq_lens.shape[0]
-    _tensor("seq_lens", seq_lens, torch.int32, (batch,), device)
-    stride = _table("page_table", page_table, batch, device)
+    _tensor("seq_lens", seq_lens, torch.int32, (batch,), index)
+    stride = _table("page_table", page_table, batch, index)
     packed = _CACHE.pack(k_cache.data_ptr(), vp, *ks, *vs, page_table.data_ptr(), stride,
                          page_table.shape[1], seq_lens.data_ptr(), pages, page_size, kv_heads,
                          head_dim, batch, _DTYPE[k_cache.dtype])
-    return packed, device, batch, kv_heads, head_dim
+    return packed, index, batch, kv_heads, head_dim
 
 
-def _query(q, k_cache, batch, kv_heads, head_dim, device):
+def _query(q, k_cache, batch, kv_heads, head_dim, index):
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be a 4-D tensor [batch, draft, heads, head_dim]")
     n, draft, heads, dim = q.shape
-    if q.dtype is not k_cache.dtype or q.device != device or n != batch or dim != head_dim:
+    if q.dtype is not k_cache.dtype or q.get_device() != index or n != batch or dim != head_dim:
         raise ValueError("q must have the cache's dtype, device and head_dim, and the batch of "
                          "seq_lens")
     if not 1 <= draft <= MAX_DRAFT:
@@ -130,46 +145,45 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     """Attention of q[batch, draft, heads, head_dim] over each request's cached
     prefix (or the listed ``slots``) and the drafted tokens that ``tree_mask``
     names (vts_tree_attention in include/vts.h)."""
-    cache, device, batch, kv_heads, head_dim = _paged(k_cache, v_cache, page_table, seq_lens)
-    draft, heads, q_strides = _query(q, k_cache, batch, kv_heads, head_dim, device)
+    cache, index, batch, kv_heads, head_dim = _paged(k_cache, v_cache, page_table, seq_lens)
+    draft, heads, q_strides = _query(q, k_cache, batch, kv_heads, head_dim, index)
     mask_ptr = slots_ptr = None
     top_k = 0
     if tree_mask is not None:
-        mask_ptr = _tensor("tree_mask", tree_mask, torch.int64, (batch, draft), device).data_ptr()
+        mask_ptr = _tensor("tree_mask", tree_mask, torch.int64, (batch, draft), index).data_ptr()
     if slots is not None:
         if not isinstance(slots, torch.Tensor) or slots.numel() == 0 and batch:
             raise ValueError("slots must be a non-empty tensor")
         top_k = slots.shape[-1]
         shape = (batch, draft, top_k) if slots.dim() == 3 else (batch * draft, top_k)
-        slots_ptr = _tensor("slots", slots, torch.int32, shape, device).data_ptr()
+        slots_ptr = _tensor("slots", slots, torch.int32, shape, index).data_ptr()
     if out is not None:
-        _tensor("out", out, q.dtype, (batch, draft, heads, head_dim), device)
+        _tensor("out", out, q.dtype, (batch, draft, heads, head_dim), index)
     if scale is None:
         scale = 1.0 / math.sqrt(head_dim)
-    lib = library()
+    lib, device = library(), q.device
 
     def call(sp):
         o = torch.empty((batch, draft, heads, head_dim), dtype=q.dtype,
                         device=device) if out is None else out
         lse = torch.empty((batch, draft, heads), dtype=torch.float32,
                           device=device) if return_lse else None
-        need = lib.vts_tree_attention_workspace_bytes(batch, draft, heads, kv_heads, head_dim,
-                                                      top_k)
-        ws = _workspace(workspace, need, device, sp)
+        ws = _workspace(workspace, _attention_bytes(batch, draft, heads, kv_heads, head_dim, top_k),
+                        device, sp)
         _check("vts_tree_attention", lib.vts_tree_attention(
             cache, q.data_ptr(), q_strides, draft, heads, mask_ptr, slots_ptr, top_k, scale,
             o.data_ptr(), lse.data_ptr() if return_lse else None, ws.data_ptr(),
             ws.numel() * ws.element_size(), sp))
         return o, lse
 
-    return _run(stream, device, call)
+    return _run(stream, index, call)
 
 
-def _weights(name, w, batch, kv_heads, device):
-    if (not isinstance(w, torch.Tensor) or w.dtype is not torch.float32 or w.device != device
+def _weights(name, w, batch, kv_heads, index):
+    if (not isinstance(w, torch.Tensor) or w.dtype is not torch.float32 or w.get_device() != index
             or w.dim() != 3 or w.shape[0] != batch or w.shape[1] != kv_heads or w.stride(2) != 1):
         raise ValueError(f"{name} must be a float32 tensor [{batch}, {kv_heads}, width] with "
-                         f"contiguous rows on {device}")
+                         f"contiguous rows on cuda:{index}")
     return w.stride(0), w.stride(1), w.shape[2]
 
 
@@ -181,19 +195,19 @@ def attention_weight_add(weights: torch.Tensor, q: torch.Tensor, k_cache: torch.
     """weights[batch, kv_heads, width] += the attention weight that each cached
     entry got from the rows of q that ``row_keep`` counts; lse as
     tree_attention returned it (vts_attention_weight_add in include/vts.h)."""
-    cache, device, batch, kv_heads, head_dim = _paged(k_cache, None, page_table, seq_lens)
-    draft, heads, q_strides = _query(q, k_cache, batch, kv_heads, head_dim, device)
-    wb, wh, width = _weights("weights", weights, batch, kv_heads, device)
+    cache, index, batch, kv_heads, head_dim = _paged(k_cache, None, page_table, seq_lens)
+    draft, heads, q_strides = _query(q, k_cache, batch, kv_heads, head_dim, index)
+    wb, wh, width = _weights("weights", weights, batch, kv_heads, index)
     if (batch > 1 and wb < width) or (kv_heads > 1 and wh < width):
         raise ValueError("weights rows must not overlap")
-    _tensor("lse", lse, torch.float32, (batch, draft, heads), device)
+    _tensor("lse", lse, torch.float32, (batch, draft, heads), index)
     mask_ptr = keep_ptr = None
     if tree_mask is not None:
-        mask_ptr = _tensor("tree_mask", tree_mask, torch.int64, (batch, draft), device).data_ptr()
+        mask_ptr = _tensor("tree_mask", tree_mask, torch.int64, (batch, draft), index).data_ptr()
     if row_keep is not None:
         if not isinstance(row_keep, torch.Tensor) or row_keep.dtype not in (torch.bool, torch.uint8):
             raise ValueError("row_keep must be a bool or uint8 tensor")
-        keep_ptr = _tensor("row_keep", row_keep, row_keep.dtype, (batch, draft), device).data_ptr()
+        keep_ptr = _tensor("row_keep", row_keep, row_keep.dtype, (batch, draft), index).data_ptr()
     if scale is None:
         scale = 1.0 / math.sqrt(head_dim)
     lib = library()
@@ -204,7 +218,7 @@ def attention_weight_add(weights: torch.Tensor, q: torch.Tensor, k_cache: torch.
             scale, weights.data_ptr(), wb, wh, width, sp))
         return weights
 
-    return _run(stream, device, call)
+    return _run(stream, index, call)
 
 
 def evict_cache(weights: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -216,17 +230,17 @@ def evict_cache(weights: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     to the pages of ``out_page_table`` in ``k_out`` and ``v_out`` (vts_evict_cache in
     include/vts.h).  Returns the kept positions [batch, kv_heads, keep] (-1 in
     unused entries), the new lengths [batch] and the kept weights."""
-    cache, device, batch, kv_heads, head_dim = _paged(k_cache, v_cache, page_table, seq_lens)
-    wb, wh, width = _weights("weights", weights, batch, kv_heads, device)
+    cache, index, batch, kv_heads, head_dim = _paged(k_cache, v_cache, page_table, seq_lens)
+    wb, wh, width = _weights("weights", weights, batch, kv_heads, index)
     if keep < 1 or sinks < 0 or recent < 0 or sinks + recent > keep:
         raise ValueError("keep must be at least 1 and at least sinks + recent")
     ko, vo = _cache("k_out", k_out, k_cache), _cache("v_out", v_out, k_cache)
     if k_out.shape[1:] != k_cache.shape[1:] or v_out.shape != k_out.shape:
         raise ValueError("k_out and v_out must be caches of the same page_size, heads and head_dim")
-    stride = _table("out_page_table", out_page_table, batch, device)
+    stride = _table("out_page_table", out_page_table, batch, index)
     if out_page_table.shape[1] * k_cache.shape[1] < keep:
         raise ValueError("out_page_table must have pages for `keep` entries")
-    lib = library()
+    lib, device = library(), k_cache.device
 
     def call(sp):
         kept = torch.empty((batch, kv_heads, keep), dtype=torch.int32, device=device)
@@ -239,7 +253,7 @@ def evict_cache(weights: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
             lens.data_ptr(), w.data_ptr(), sp))
         return kept, lens, w
 
-    return _run(stream, device, call)
+    return _run(stream, index, call)
 
 
 def verify_draft(target_probs: torch.Tensor, draft_tokens: torch.Tensor, uniforms: torch.Tensor, *,
@@ -256,34 +270,34 @@ def verify_draft(target_probs: torch.Tensor, draft_tokens: torch.Tensor, uniform
         raise ValueError("target_probs dtype must be float32, bfloat16 or float16")
     if not target_probs.is_cuda:
         raise ValueError("target_probs must be on the GPU")
-    device = target_probs.device
+    index = target_probs.get_device()
     batch, draft, vocab = target_probs.shape
     draft -= 1
     if not 1 <= draft <= MAX_DRAFT or vocab < 1:
         raise ValueError(f"target_probs must have 2..{MAX_DRAFT + 1} rows a request, not empty")
     if target_probs.stride(2) != 1 and vocab > 1:
         raise ValueError("target_probs rows must be contiguous")
-    _tensor("draft_tokens", draft_tokens, torch.int32, (batch, draft), device)
-    _tensor("uniforms", uniforms, torch.float32, (batch, draft + 1), device)
+    _tensor("draft_tokens", draft_tokens, torch.int32, (batch, draft), index)
+    _tensor("uniforms", uniforms, torch.float32, (batch, draft + 1), index)
     q_ptr = parents_ptr = None
     qb = qr = 0
     if draft_probs is not None:
         if (not isinstance(draft_probs, torch.Tensor) or draft_probs.dtype is not target_probs.dtype
-                or draft_probs.device != device or tuple(draft_probs.shape) != (batch, draft, vocab)
+                or draft_probs.get_device() != index or draft_probs.shape != (batch, draft, vocab)
                 or (draft_probs.stride(2) != 1 and vocab > 1)):
             raise ValueError("draft_probs must be a tensor [batch, draft, vocab] with contiguous "
                              "rows, of target_probs' dtype and device")
         q_ptr = draft_probs.data_ptr()
         qb, qr = draft_probs.stride(0), draft_probs.stride(1)
     if parents is not None:
-        parents_ptr = _tensor("parents", parents, torch.int32, (batch, draft), device).data_ptr()
-    lib = library()
+        parents_ptr = _tensor("parents", parents, torch.int32, (batch, draft), index).data_ptr()
+    lib, device = library(), target_probs.device
 
     def call(sp):
         path = torch.empty((batch, draft), dtype=torch.int32, device=device)
         count = torch.empty((batch,), dtype=torch.int32, device=device)
         token = torch.empty((batch,), dtype=torch.int32, device=device)
-        ws = _workspace(workspace, lib.vts_verify_draft_workspace_bytes(batch, vocab), device, sp)
+        ws = _workspace(workspace, _verify_bytes(batch, vocab), device, sp)
         _check("vts_verify_draft", lib.vts_verify_draft(
             target_probs.data_ptr(), _DTYPE[target_probs.dtype], target_probs.stride(0),
             target_probs.stride(1), q_ptr, qb, qr, draft_tokens.data_ptr(), parents_ptr,
@@ -291,7 +305,7 @@ def verify_draft(target_probs: torch.Tensor, draft_tokens: torch.Tensor, uniform
             token.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), sp))
         return path, count, token
 
-    return _run(stream, device, call)
+    return _run(stream, index, call)
 
 
 def tree_mask_from_parents(parents: torch.Tensor) -> torch.Tensor:
