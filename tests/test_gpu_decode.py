@@ -90,6 +90,11 @@ CASES = [
     ([(x * 61) % 300 for x in range(16)] + [4000] * 16, 1, 16, 4, 64, 16, False, torch.bfloat16),
     ([100] * 31 + [9000], 2, 16, 4, 128, 32, True, torch.float16),  # one list over most workgroups
     ([20000], 1, 2, 1, 64, 64, False, torch.bfloat16),  # blocks of parts
+    # wide: 64, 128 rows and more to a KV head, lists that end anywhere
+    ([1, 0, 63, 64, 65, 129, 700], 16, 8, 2, 128, 16, True, torch.bfloat16),
+    ([3000, 17], 20, 12, 2, 64, 24, True, torch.float16),
+    ([1500, 129, 64], 40, 8, 2, 128, 32, True, torch.float16),
+    ([900, 70], 64, 10, 2, 64, 64, False, torch.bfloat16),
 ]
 
 
@@ -166,14 +171,15 @@ def test_attend_empty_mask_rows():
 
 
 @pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
-@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
-def test_attend_unseen_infinities(bad, dtype):
+@pytest.mark.parametrize("dtype,heads", [(torch.bfloat16, 4), (torch.float16, 4),
+                                         (torch.bfloat16, 16), (torch.float16, 40)])
+def test_attend_unseen_infinities(bad, dtype, heads):
     """Values of unseen places (past the length, unused pages, drafted tokens of
     other branches) do not reach a row, whatever they are."""
     gen = torch.Generator().manual_seed(12)
     lens, page, draft = [70, 21, 5], 16, 5
     k, v, table, n = make_cache(gen, lens, page, 2, 128, dtype)
-    q = torch.randn(3, draft, 4, 128, generator=gen).to(dtype).to(DEV)
+    q = torch.randn(3, draft, heads, 128, generator=gen).to(dtype).to(DEV)
     mask = torch.tensor([[1, 2, 4, 9, 0]] * 3, dtype=torch.int64, device=DEV)
     clean, clean_lse = vts.tree_attention(q, k, v, table, n, tree_mask=mask, return_lse=True)
     live = torch.zeros(k.shape[0], page, dtype=torch.bool, device=DEV)
@@ -216,6 +222,18 @@ def test_attend_slots(tree, page, dim, top_k):
     slots[2, 1, 0] = -2 ** 31
     mask = random_mask(gen, 3, draft)[0] if tree else None
     check_attend(q, k, v, table, n, mask, slots.to(DEV))
+
+
+@pytest.mark.parametrize("heads,dim,dtype", [(40, 128, torch.bfloat16), (80, 64, torch.float16),
+                                             (150, 64, torch.bfloat16)])
+def test_attend_slots_of_many_heads(heads, dim, dtype):
+    gen = torch.Generator().manual_seed(15 + heads)
+    k, v, table, n = make_cache(gen, [300, 5], 16, 1, dim, dtype)
+    q = torch.randn(2, 2, heads, dim, generator=gen).to(dtype).to(DEV)
+    slots = torch.randint(-1, k.shape[0] * 16, (2, 2, 150), generator=gen, dtype=torch.int32)
+    slots[1, 0] = -1
+    check_attend(q, k, v, table, n, random_mask(gen, 2, 2)[0], slots.to(DEV))
+    check_attend(q, k, v, table, n, None, slots.to(DEV))
 
 
 def test_attend_slots_of_the_selection():

@@ -5,7 +5,7 @@
 // over the places a query row sees: the cached prefix (or a list of slots per
 // row) and the drafted tokens its mask names.  All query rows that share a KV
 // head and a list of places are taken together (drafted tokens x grouped
-// heads), so each K and V row is read once per 16 * MT of them.
+// heads), up to 128 of them for each time that K and V are read.
 //
 // One pass: each wave walks its 32-place tiles with a running maximum m, sum l
 // and output O per query row (32-bit), and the waves, then the workgroups that
@@ -19,60 +19,87 @@
 
 namespace vts {
 
-template <int D, int MT, bool HEADS>
-struct AttendShared {
-    static constexpr int ROWS = (HEADS ? WAVES : 1) * 16 * MT;
-    // query rows as operands, from 32 rows on
-    u32x4 q[MT > 1 ? (HEADS ? WAVES : 1) * MT * (D / 32) : 1][64];
-    // a wave's K rows on their way from the order of whole rows to operands
-    u32x4 k[MT <= 2 ? WAVES : 1][MT <= 2 ? 32 * (D / 8) : 1];
-    // padded: the 16 rows of a store fall on all banks
-    float o[HEADS ? 1 : 2][HEADS ? 1 : 16 * MT][D + 4];
-    float ml[HEADS ? 1 : WAVES][ROWS][2];
-    float tops[NT];
-    int64_t scan[WAVES + 1];
-    int32_t found;
+// How a workgroup's waves share the work.
+enum Mode : int {
+    KEYS = 0,   // four waves, 32 places each of the same rows
+    HEADS = 1,  // four waves, a KV head each at the same 32 places
+    WIDE2 = 2,  // eight waves: two groups of 32 rows, four times 32 places
+    WIDE4 = 4,  // eight waves: four groups of 32 rows, twice 32 places
+};
+
+constexpr int threads_of(int mode) { return mode >= WIDE2 ? 512 : NT; }
+
+template <int D, int MT, int MODE>
+struct AttendShape {
+    static constexpr bool WIDE = MODE >= WIDE2;
+    static constexpr int NW = threads_of(MODE) / 64;       // waves
+    static constexpr int RG = WIDE ? MODE : 1;             // groups of rows
+    static constexpr int KG = WIDE ? NW / RG : MODE == HEADS ? 1 : NW;  // groups of places
+    static constexpr int SUBS = MODE == HEADS ? NW : RG;   // blocks of 16 * MT rows
+    static constexpr int ROWS = SUBS * 16 * MT;
+};
+
+// A wide workgroup's places, K as operands (swizzled) and V in whole rows.
+template <int D, int PLACES>
+struct WideTiles {
+    u32x4 k[2][PLACES * (D / 8)], v[2][PLACES * (D / 8)];
+    uint8_t there[2][PLACES];
+};
+
+template <int D, int MT, int MODE>
+struct AttendShared : AttendShape<D, MT, MODE> {
+    using S = AttendShape<D, MT, MODE>;
+    u32x4 q[MT > 1 ? S::SUBS * MT * (D / 32) : 1][64];  // query rows as operands, from 32 rows on
+    union {
+        // a wave's K rows on their way from the order of whole rows to operands
+        u32x4 k[S::WIDE ? 1 : WAVES][S::WIDE ? 1 : 32 * (D / 8)];
+        WideTiles<D, S::WIDE ? S::KG * 32 : 1> w;
+        // outputs of waves to be joined, padded: the 16 rows of a store fall on all banks
+        float o[MODE == HEADS ? 1 : S::WIDE ? S::KG - 1 : 2][MODE == HEADS ? 1 : S::ROWS][D + 4];
+    };
+    float ml[S::KG][S::ROWS][2];
+    float tops[S::NW * 64];
     uint32_t last;
 };
 
-template <int DT, int D, int MT, bool SLOTS, bool HEADS>
+template <int DT, int D, int MT, bool SLOTS, int MODE>
 struct Attend {
     static constexpr int KS = D / 32;       // steps of the first product
     static constexpr int VB = D / 16 * 2;   // bytes of a V row per lane
     static constexpr int VW = VB / 4;       // words of a V row per lane
     static constexpr int NTILE = D / 16;    // 16-row tiles of the second product
     static constexpr int JOIN = 32;         // parts joined by one workgroup
-    static constexpr int ROWS = AttendShared<D, MT, HEADS>::ROWS;
+    using S = AttendShape<D, MT, MODE>;
+    static constexpr bool HEAD = MODE == HEADS, WIDE = S::WIDE;
+    static constexpr int T = S::NW * 64;    // threads
+    static constexpr int ROWS = S::ROWS;
     using VRow = typename std::conditional<D == 128, u32x4, u32x2>::type;
 
     const AttendParams& p;
-    AttendShared<D, MT, HEADS>& sm;
+    AttendShared<D, MT, MODE>& sm;
     int tid, lane, wave, col, grp;
+    int rg, kg;  // the wave's group of rows and of places
     uint32_t page_stride, pos_stride;  // of K in lanes 0..31, of V above
     int32_t req, head_unit, mb, t0;  // t0: the row of a slot list
     Places pl;
     static constexpr bool QL = MT > 1;  // query rows in LDS
-    // K through LDS: a load instruction then takes whole rows (as the operand's
-    // order it would take 64 bytes of each of 16), which the memory gives 8 % faster
-    // (64 requests up to 16384: 454 us for 492); with 64 rows to multiply the
-    // time is not the memory's.
-    static constexpr bool KL = MT <= 2;
-    static constexpr int CH = D / 8;        // 16-byte chunks of a row
-    static constexpr int RPL = 64 / CH;     // rows of one load instruction
-    // With 64 rows O is kept in accumulation registers (the empty asm in tile()):
-    // left to itself the compiler keeps it where the rare rescaling wants it
-    // and copies it to and from the matrix instructions in every tile.
-    static constexpr bool OA = MT == 4;
+    static constexpr int CH = D / 8;    // 16-byte chunks of a row
+    static constexpr int RPL = 64 / CH; // rows of one load instruction
+    // Wide: a thread's chunks of a unit's places, and a wave's rows of them
+    static constexpr int LOADS = WIDE ? S::KG * 32 * CH / T : 1;
+    static constexpr int MINE = LOADS * RPL;
     u32x4 q[QL ? 1 : KS];
     uint64_t bits[MT];
     f32x4 o[MT][NTILE];
     float m[MT], l[MT];
-    u32x4 k[2][KS];
+    // the tile on its way: 32 places to a wave, or the wave's rows of the unit
+    u32x4 k[WIDE ? LOADS : 2 * KS];
     VRow v[8];
+    u32x4 vw[LOADS];
     const void* kbase;
     const void* vbase;
 
-    __device__ Attend(const AttendParams& p_, AttendShared<D, MT, HEADS>& s_, int32_t mb_)
+    __device__ Attend(const AttendParams& p_, AttendShared<D, MT, MODE>& s_, int32_t mb_)
         : p(p_), sm(s_), mb(mb_) {
         fresh();
     }
@@ -86,12 +113,19 @@ struct Attend {
         wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         col = lane & 15;
         grp = lane >> 4;
+        rg = WIDE ? wave % S::RG : 0;
+        kg = WIDE ? wave / S::RG : HEAD ? 0 : wave;
     }
+    // the block of rows that the wave works on
+    __device__ __forceinline__ int sub() const { return HEAD ? wave : rg; }
 
-    // row r of the block (of its head `sub`): the drafted token and the query head
+    // row r of block `sub` (a head's, or a group's): the drafted token and the query head
+    __device__ __forceinline__ int32_t row_at(int sub, int r) const {
+        return HEAD ? r : (mb * S::SUBS + sub) * 16 * MT + r;
+    }
     __device__ __forceinline__ bool row_of(int sub, int r, int32_t& t, int32_t& head) const {
-        const int32_t row = mb * 16 * MT + r;
-        const int32_t h = HEADS ? head_unit * WAVES + sub : head_unit;
+        const int32_t row = row_at(sub, r);
+        const int32_t h = HEAD ? head_unit * WAVES + sub : head_unit;
         if (SLOTS) {
             t = t0;
             head = h * p.c.group + row;
@@ -105,7 +139,7 @@ struct Attend {
     __device__ __forceinline__ void begin(int32_t b, int32_t h) {
         fresh();
         head_unit = h;
-        if (HEADS) h = h * WAVES + wave;
+        if (HEAD) h = h * WAVES + wave;
         const PagedParams& c = p.c;
         if (SLOTS) {
             req = b / c.draft;
@@ -127,13 +161,13 @@ struct Attend {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             int32_t t, head;
-            const bool ok = row_of(wave, mt * 16 + col, t, head);
+            const bool ok = row_of(sub(), mt * 16 + col, t, head);
             const char* at = (const char*)p.q +
                              2 * (req * p.q_batch + (ok ? t * p.q_row + head * p.q_head : 0));
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 u32x4 x = {0, 0, 0, 0};
-                if (QL && !HEADS && (mt * KS + s) % WAVES != wave) continue;
+                if (QL && !HEAD && (mt * KS + s) % S::KG != kg) continue;
                 if (ok) x = gload((const u32x4*)(at + s * 64 + grp * 16));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[e] ^= p.q_sign;
@@ -155,53 +189,80 @@ struct Attend {
 #pragma unroll
             for (int n2 = 0; n2 < NTILE; ++n2) o[mt][n2] = f32x4{0, 0, 0, 0};
         }
-        if constexpr (QL && !HEADS) __syncthreads();
+        if constexpr (QL && !HEAD) __syncthreads();
     }
     __device__ __forceinline__ int q_at(int mt, int s) const {
-        return ((HEADS ? wave * MT : 0) + mt) * KS + s;
+        return (sub() * MT + mt) * KS + s;
     }
 
     __device__ __forceinline__ int32_t first_place(int32_t u) const {
-        return HEADS ? u * 32 : u * UNIT + wave * 32;
+        return (u * S::KG + kg) * 32;
     }
+    // the place that lane l of a wave looks up: of its own 32, or (wide) of its
+    // rows of the unit
     __device__ __forceinline__ Entry issue(int32_t u) const {
-        return issue_entry<SLOTS>(p.c, pl, first_place(u) + (lane & 31));
+        const int l = lane & 31;
+        if constexpr (WIDE)
+            return issue_entry<SLOTS>(p.c, pl, l < MINE ? u * S::KG * 32 + wide_row(l) : -1);
+        return issue_entry<SLOTS>(p.c, pl, first_place(u) + l);
+    }
+    // row i of the wave's rows of a unit
+    __device__ __forceinline__ int wide_row(int i) const {
+        return (i / RPL * S::NW + wave) * RPL + i % RPL;
     }
     // K offsets in lanes 0..31, V offsets in lanes 32..63
     __device__ __forceinline__ uint32_t resolve(const Entry& e) const {
         return resolve_entry<SLOTS>(p.c, page_stride, pos_stride, e);
     }
+    // K goes through LDS: a load instruction then takes whole rows (as the
+    // operand's order it would take 64 bytes of each of 16), which the memory gives
+    // 8 % faster (64 requests up to 16384: 454 us for 492).
     __device__ __forceinline__ void load_k(uint32_t off) {
         const uint32_t safe = off == NO_PLACE ? 0 : off;
-        if constexpr (KL) {
 #pragma unroll
-            for (int i = 0; i < 2 * KS; ++i)
-                k[i / KS][i % KS] = row_load<u32x4, HEADS>(
-                    kbase, from_lane(safe, i * RPL + lane / CH), (lane % CH) * 16);
-            return;
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t r = from_lane(safe, h * 16 + col);
-#pragma unroll
-            for (int s = 0; s < KS; ++s) k[h][s] = row_load<u32x4, HEADS>(kbase, r, s * 64 + grp * 16);
-        }
+        for (int i = 0; i < (WIDE ? LOADS : 2 * KS); ++i)
+            k[i] = row_load<u32x4, HEAD>(kbase, from_lane(safe, i * RPL + lane / CH),
+                                         (lane % CH) * 16);
     }
     __device__ __forceinline__ void stage_k() {
 #pragma unroll
         for (int i = 0; i < 2 * KS; ++i) {
             const int r = i * RPL + lane / CH;
-            sm.k[wave][r * CH + ((lane % CH) ^ swizzled<D>(r))] = k[i / KS][i % KS];
+            sm.k[wave][r * CH + ((lane % CH) ^ swizzled<D>(r))] = k[i];
         }
         // the wave's own stores come before its loads; the compiler has to know
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     }
-    __device__ __forceinline__ u32x4 operand_k(int h, int s) const {
-        if constexpr (!KL) return k[h][s];
-        const int r = h * 16 + col;
-        return sm.k[wave][r * CH + ((s * 4 + grp) ^ swizzled<D>(r))];
+    // A wide workgroup's unit: whole rows of K and V, each once, to half `buf`.
+    __device__ __forceinline__ void load_wide(uint32_t off) {
+        const uint32_t safe = off == NO_PLACE ? 0 : off;
+        load_k(off);
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            vw[i] = row_load<u32x4>(vbase, from_lane(safe, 32 + i * RPL + lane / CH),
+                                    (lane % CH) * 16);
+    }
+    __device__ __forceinline__ void stage_wide(uint32_t off, int buf) {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int r = wide_row(i * RPL + lane / CH);
+            const bool there = from_lane(off, i * RPL + lane / CH) != NO_PLACE;
+            const u32x4 z = {0, 0, 0, 0};
+            sm.w.k[buf][r * CH + ((lane % CH) ^ swizzled<D>(r))] = k[i];
+            sm.w.v[buf][r * CH + lane % CH] = there ? vw[i] : z;
+            if (lane % CH == 0) sm.w.there[buf][r] = there;
+        }
+    }
+    __device__ __forceinline__ u32x4 operand_k(int h, int s, int buf) const {
+        const int r = (WIDE ? kg * 32 : 0) + h * 16 + col;
+        const int at = r * CH + ((s * 4 + grp) ^ swizzled<D>(r));
+        if constexpr (WIDE) return sm.w.k[buf][at];
+        return sm.k[wave][at];
+    }
+    __device__ __forceinline__ VRow wide_v(int buf, int place, int part) const {
+        return *(const VRow*)((const char*)&sm.w.v[buf][(kg * 32 + place) * CH] + part * VB);
     }
     // register j: place 4 * grp + j of the first half, or of the second for j >= 4
     __device__ __forceinline__ int v_place(int j) const {
@@ -211,7 +272,7 @@ struct Attend {
         const uint32_t safe = off == NO_PLACE ? 0 : off;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            v[j] = row_load<VRow, HEADS>(vbase, from_lane(safe, 32 + v_place(j)), col * VB);
+            v[j] = row_load<VRow, HEAD>(vbase, from_lane(safe, 32 + v_place(j)), col * VB);
     }
 
     // The tile's share of O: V rows turned so that each lane holds eight places
@@ -257,16 +318,18 @@ struct Attend {
         }
         return bad;
     }
-    __device__ __forceinline__ void add_rows(uint32_t bad, uint32_t off, int32_t j0,
+    __device__ __forceinline__ void add_rows(uint32_t bad, uint32_t off, int32_t j0, int buf,
                                              const u32x4 (&pv)[MT]) {
 #pragma unroll 1
         while (bad) {
             const int kk = __builtin_ctz(bad);
             bad &= bad - 1;
-            const uint32_t r = from_lane(off, 32 + kk);
+            const uint32_t r = WIDE ? 0 : from_lane(off, 32 + kk);
             VRow x[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = row_load<VRow>(vbase, r, (grp * 4 + e) * VB);
+            for (int e = 0; e < 4; ++e)
+                x[e] = WIDE ? wide_v(buf, kk, grp * 4 + e)
+                            : row_load<VRow>(vbase, r, (grp * 4 + e) * VB);
             const int src = ((kk & 15) >> 2) * 16 + col;
             const int idx = (kk >> 4) * 4 + (kk & 3);
             const int32_t i = j0 + kk - pl.first;
@@ -295,10 +358,10 @@ struct Attend {
     // as soon as this tile's are used up, and its V rows after the second
     // product, so one of the two is always on its way.
     __device__ __forceinline__ void tile(uint32_t have, bool drafted, uint32_t off, int32_t j0,
-                                         bool more, uint32_t off_next) {
+                                         bool more, uint32_t off_next, int buf) {
         const float c = p.scale_log2e;
         const bool masked = have != ~0u || drafted;
-        if constexpr (KL) {
+        if constexpr (!WIDE) {
             stage_k();
             if (more) load_k(off_next);
         }
@@ -311,7 +374,7 @@ struct Attend {
         // dependent ones
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-            const u32x4 k0 = operand_k(0, ks), k1 = operand_k(1, ks);
+            const u32x4 k0 = operand_k(0, ks, buf), k1 = operand_k(1, ks, buf);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 const u32x4 qq = QL ? sm.q[q_at(mt, ks)][lane] : q[QL ? 0 : ks];
@@ -319,7 +382,6 @@ struct Attend {
                 s[mt][1] = mfma<DT>(k1, qq, s[mt][1]);
             }
         }
-        if (!KL && more) load_k(off_next);
         if (masked) {
             int g = grp;  // opaque: nothing of this is kept in registers between tiles
             asm volatile("" : "+v"(g));
@@ -361,11 +423,6 @@ struct Attend {
                     for (int e = 0; e < 4; ++e) o[mt][n][e] *= f;
             }
         }
-        if constexpr (OA)
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int n = 0; n < NTILE; ++n) asm volatile("" : "+a"(o[mt][n]));
         u32x4 pv[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -380,12 +437,15 @@ struct Attend {
                 pv[mt][e] = pack2<DT>(a, b);
             }
         }
+        if constexpr (WIDE)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = wide_v(buf, v_place(j), col);
         uint32_t bad = 0;
         if (masked) {
             int g = grp;
             asm volatile("" : "+v"(g));
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < (WIDE ? 0 : 8); ++j) {  // (a wide unit's are zero already)
                 const uint32_t there = (have >> ((j >> 2) * 16 + g * 4 + (j & 3))) & 1u;
 #pragma unroll
                 for (int w = 0; w < VW; ++w) v[j][w] = there ? v[j][w] : 0;
@@ -393,10 +453,12 @@ struct Attend {
             if (drafted) bad = clear_not_finite();
         }
         second_product(pv);
-        if (bad) add_rows(bad, off, j0, pv);
-        if (more) load_v(off_next);
-        // the next tile's stores to sm.k come after these loads
-        if constexpr (KL) __builtin_amdgcn_wave_barrier();
+        if (bad) add_rows(bad, off, j0, buf, pv);
+        if constexpr (!WIDE) {
+            if (more) load_v(off_next);
+            // the next tile's stores to sm.k come after these loads
+            __builtin_amdgcn_wave_barrier();
+        }
     }
 
     // Units [u0, u1) of the places, this wave's 32 of each.
@@ -406,16 +468,34 @@ struct Attend {
         pos_stride = lane < 32 ? p.c.k.pos_stride : p.c.v.pos_stride;
         uint32_t off = resolve(issue(u0));
         Entry next = issue(u0 + 1);
-        load_k(off);
-        load_v(off);
+        if constexpr (WIDE) {
+            load_wide(off);
+        } else {
+            load_k(off);
+            load_v(off);
+        }
 #pragma unroll 1
         for (int32_t u = u0; u < u1; ++u) {
             const int32_t j0 = first_place(u);
-            const uint32_t off_next = resolve(next);
-            next = issue(u + 2);
-            const uint32_t have = (uint32_t)ballot(off != NO_PLACE);
+            const int buf = u & 1;
+            uint32_t have;
+            uint32_t off_next;
+            if constexpr (WIDE) {
+                // the other half may still be read; this one was done with before
+                // the last barrier
+                stage_wide(off, buf);
+                off_next = resolve(next);
+                next = issue(u + 2);
+                if (u + 1 < u1) load_wide(off_next);
+                __syncthreads();
+                have = (uint32_t)ballot(sm.w.there[buf][kg * 32 + (lane & 31)]);
+            } else {
+                off_next = resolve(next);
+                next = issue(u + 2);
+                have = (uint32_t)ballot(off != NO_PLACE);
+            }
             const bool drafted = j0 + 31 >= pl.first;
-            tile(have, drafted, off, j0, u + 1 < u1, off_next);
+            tile(have, drafted, off, j0, u + 1 < u1, off_next, buf);
             off = off_next;
         }
     }
@@ -428,7 +508,7 @@ struct Attend {
             for (int n = 0; n < NTILE; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    sm.o[slot][mt * 16 + col][(grp * 4 + e) * NTILE + n] = o[mt][n][e];
+                    sm.o[slot][rg * 16 * MT + mt * 16 + col][(grp * 4 + e) * NTILE + n] = o[mt][n][e];
     }
     __device__ __forceinline__ void take(int slot) {
 #pragma unroll
@@ -437,19 +517,22 @@ struct Attend {
             for (int n = 0; n < NTILE; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    o[mt][n][e] += sm.o[slot][mt * 16 + col][(grp * 4 + e) * NTILE + n];
+                    o[mt][n][e] +=
+                        sm.o[slot][rg * 16 * MT + mt * 16 + col][(grp * 4 + e) * NTILE + n];
     }
 
-    // Joins the four waves; the block's rows are then in sm.o[0], sm.ml[0].
+    // Joins the waves of different places.  Four waves: the block's rows are
+    // then in sm.o[0], sm.ml[0]; wide: in the registers of the first group's.
     __device__ __forceinline__ void join_waves() {
         fresh();
+        const int r0 = rg * 16 * MT + col;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             l[mt] += __shfl_xor(l[mt], 16);
             l[mt] += __shfl_xor(l[mt], 32);
             if (grp == 0) {
-                sm.ml[wave][mt * 16 + col][0] = m[mt];
-                sm.ml[wave][mt * 16 + col][1] = l[mt];
+                sm.ml[kg][r0 + mt * 16][0] = m[mt];
+                sm.ml[kg][r0 + mt * 16][1] = l[mt];
             }
         }
         __syncthreads();
@@ -457,10 +540,10 @@ struct Attend {
         for (int mt = 0; mt < MT; ++mt) {
             float top = NEG_INF, sum = 0;
 #pragma unroll
-            for (int w = 0; w < WAVES; ++w) top = fmaxf(top, sm.ml[w][mt * 16 + col][0]);
+            for (int w = 0; w < S::KG; ++w) top = fmaxf(top, sm.ml[w][r0 + mt * 16][0]);
 #pragma unroll
-            for (int w = 0; w < WAVES; ++w)
-                sum += sm.ml[w][mt * 16 + col][1] * scale_to(sm.ml[w][mt * 16 + col][0], top);
+            for (int w = 0; w < S::KG; ++w)
+                sum += sm.ml[w][r0 + mt * 16][1] * scale_to(sm.ml[w][r0 + mt * 16][0], top);
             const float f = scale_to(m[mt], top);
             m[mt] = top;
             l[mt] = sum;
@@ -468,6 +551,14 @@ struct Attend {
             for (int n = 0; n < NTILE; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[mt][n][e] *= f;
+        }
+        if constexpr (WIDE) {
+            if (kg > 0) put(kg - 1);
+            __syncthreads();
+            if (kg == 0)
+#pragma unroll 1
+                for (int w = 0; w < S::KG - 1; ++w) take(w);
+            return;
         }
         if (wave >= 2) put(wave - 2);
         __syncthreads();
@@ -491,12 +582,6 @@ struct Attend {
     static __device__ __forceinline__ float scale_to(float from, float top) {
         return top == NEG_INF ? 1.0f : __builtin_amdgcn_exp2f(from - top);
     }
-    // rows of this block that are there
-    __device__ __forceinline__ int rows_here() const {
-        const int32_t n = p.rows - mb * 16 * MT;
-        return n < 16 * MT ? n : 16 * MT;
-    }
-
     // Normalises four outputs of row r and writes them, and its lse.
     __device__ __forceinline__ void write_row(int sub, int r, int d, f32x4 x, float top,
                                               float sum) const {
@@ -530,18 +615,27 @@ struct Attend {
         }
     }
 
-    __device__ __forceinline__ void finish_whole() {
-        if constexpr (HEADS) {
+    // Leaves a wave's rows in its registers (false: in another wave's).
+    __device__ __forceinline__ bool own_rows() {
+        if constexpr (HEAD)
             close();
+        else
+            join_waves();
+        return kg == 0;
+    }
+
+    __device__ __forceinline__ void finish_whole() {
+        if constexpr (HEAD || WIDE) {
+            if (own_rows())
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+                for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int i = 0; i < NTILE; ++i)
-                    write_row(wave, mt * 16 + col, four_at(i), four(mt, i), m[mt], l[mt]);
+                    for (int i = 0; i < NTILE; ++i)
+                        write_row(sub(), mt * 16 + col, four_at(i), four(mt, i), m[mt], l[mt]);
+            if constexpr (WIDE) __syncthreads();
         } else {
             join_waves();
-            const int n = rows_here() * D;
-            for (int x = tid * 4; x < n; x += NT * 4) {
+            for (int x = tid * 4; x < ROWS * D; x += T * 4) {
                 const int r = x / D, d = x % D;
                 write_row(0, r, d, *(const f32x4*)&sm.o[0][r][d], sm.ml[0][r][0], sm.ml[0][r][1]);
             }
@@ -555,26 +649,26 @@ struct Attend {
                                                 bool w0_whole_start) {
         float* po = p.part_o + mine * (ROWS * D);
         float* pm = p.part_ml + mine * (ROWS * 2);
-        const int rows = rows_here();
-        if constexpr (HEADS) {
-            close();
+        if constexpr (HEAD || WIDE) {
+            if (own_rows())
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                const int r = mt * 16 + col, at = wave * 16 * MT + r;
-                if (r >= rows) continue;
+                for (int mt = 0; mt < MT; ++mt) {
+                    const int r = mt * 16 + col, at = sub() * 16 * MT + r;
+                    if (row_at(sub(), r) >= p.rows) continue;
 #pragma unroll
-                for (int i = 0; i < NTILE; ++i)
-                    gstore((f32x4*)(po + at * D + four_at(i)), four(mt, i));
-                if (grp == 0) {
-                    gstore(pm + at * 2, m[mt]);
-                    gstore(pm + at * 2 + 1, l[mt]);
+                    for (int i = 0; i < NTILE; ++i)
+                        gstore((f32x4*)(po + at * D + four_at(i)), four(mt, i));
+                    if (grp == 0) {
+                        gstore(pm + at * 2, m[mt]);
+                        gstore(pm + at * 2 + 1, l[mt]);
+                    }
                 }
-            }
         } else {
             join_waves();
-            for (int x = tid * 4; x < rows * D; x += NT * 4)
-                gstore((f32x4*)(po + x), *(const f32x4*)&sm.o[0][x / D][x % D]);
-            if (tid < rows * 2) gstore(pm + tid, (&sm.ml[0][0][0])[tid]);
+            for (int x = tid * 4; x < ROWS * D; x += T * 4)
+                if (row_at(0, x / D) < p.rows)
+                    gstore((f32x4*)(po + x), *(const f32x4*)&sm.o[0][x / D][x % D]);
+            if (tid < ROWS * 2) gstore(pm + tid, (&sm.ml[0][0][0])[tid]);
         }
         // The parts are joined in blocks of JOIN workers, each by the block's last
         // to arrive, and the blocks by the last of those: with one joiner for
@@ -584,9 +678,9 @@ struct Attend {
         const int32_t members = w1 - wb + 1 < JOIN ? w1 - wb + 1 : JOIN;
         if (members == 1 || last_of(p.tickets + MAX_TICKETS + (int64_t)mb * p.workers + wb, members)) {
             if (blocks == 1 || members > 1)
-                join_parts(rows, wb, 1, members, w0, w0_whole_start, blocks == 1);
+                join_parts(wb, 1, members, w0, w0_whole_start, blocks == 1);
             if (blocks > 1 && last_of(p.tickets + (int64_t)mb * p.workers + w0, blocks))
-                join_parts(rows, w0, JOIN, blocks, w0, w0_whole_start, true);
+                join_parts(w0, JOIN, blocks, w0, w0_whole_start, true);
         }
         __syncthreads();
     }
@@ -616,27 +710,28 @@ struct Attend {
     // to the first one's slot.  Other workgroups' parts come from beyond this
     // XCD, so their loads are issued eight at a time: one after the other,
     // 32 parts took 40 us.
-    __device__ __forceinline__ void join_parts(int rows, int32_t first, int32_t stride, int32_t count,
+    __device__ __forceinline__ void join_parts(int32_t first, int32_t stride, int32_t count,
                                                int32_t w0, bool w0_whole_start, bool to_outputs) {
-        constexpr int LANES = NT / ROWS;  // threads to a row for the maxima
-        const int row = tid % ROWS, sub = tid / ROWS;
+        constexpr int LANES = T / ROWS;  // threads to a row for the maxima
+        const int row = tid % ROWS, lane0 = tid / ROWS;
+        const auto there = [&](int r) { return row_at(r / (16 * MT), r % (16 * MT)) < p.rows; };
         float top = NEG_INF;
-        if (row % (16 * MT) < rows)
-            for (int32_t i = sub; i < count; i += LANES)
+        if (there(row))
+            for (int32_t i = lane0; i < count; i += LANES)
                 top = fmaxf(top, gload(p.part_ml + part(first + i * stride, w0, w0_whole_start) *
                                                        (ROWS * 2) + row * 2));
-        sm.tops[sub * ROWS + row] = top;
+        sm.tops[lane0 * ROWS + row] = top;
         __syncthreads();
-        if (sub == 0) {
+        if (lane0 == 0) {
 #pragma unroll
             for (int i = 1; i < LANES; ++i) top = fmaxf(top, sm.tops[i * ROWS + row]);
             sm.ml[0][row][0] = top;
         }
         __syncthreads();
         const int64_t to = part(first, w0, w0_whole_start);
-        for (int x = tid * 4; x < ROWS * D; x += NT * 4) {
+        for (int x = tid * 4; x < ROWS * D; x += T * 4) {
             const int r = x / D;
-            if (r % (16 * MT) >= rows) continue;
+            if (!there(r)) continue;
             const float base = sm.ml[0][r][0];
             float sum = 0;
             f32x4 acc = {0, 0, 0, 0};
@@ -670,7 +765,7 @@ struct Attend {
         }
         if (to_outputs) return;
         __syncthreads();  // everyone has read the slot's maxima and sums
-        if (sub == 0 && row % (16 * MT) < rows) {
+        if (lane0 == 0 && there(row)) {
             gstore(p.part_ml + to * (ROWS * 2) + row * 2, sm.ml[0][row][0]);
             gstore(p.part_ml + to * (ROWS * 2) + row * 2 + 1, sm.ml[0][row][1]);
         }
@@ -682,9 +777,11 @@ struct Attend {
     }
 };
 
-template <int DT, int D, int MT, bool SLOTS, bool HEADS>
-__global__ __launch_bounds__(NT, 1) void attend_kernel(AttendParams p) {
-    __shared__ AttendShared<D, MT, HEADS> sm;
+template <int DT, int D, int MT, bool SLOTS, int MODE>
+__global__ __launch_bounds__(threads_of(MODE), MODE >= WIDE2 ? 2 : 1) void attend_kernel(AttendParams p) {
+    constexpr bool HEAD = MODE == HEADS;
+    constexpr int PLACES = AttendShape<D, MT, MODE>::KG * 32;
+    __shared__ AttendShared<D, MT, MODE> sm;
     // the row blocks of one share run next to each other on one XCD
     const int32_t per = 8 * p.row_blocks;
     const int32_t w = (int32_t)(blockIdx.x / per) * 8 + (int32_t)(blockIdx.x & 7);
@@ -692,7 +789,7 @@ __global__ __launch_bounds__(NT, 1) void attend_kernel(AttendParams p) {
     if (w >= p.workers) return;
     Share sh;
     if constexpr (SLOTS) {
-        const int32_t each = units_of<HEADS>(place_count<true>(p, 0)) * head_units<HEADS>(p.c);
+        const int32_t each = units_of<PLACES>(place_count<true>(p, 0)) * head_units<HEAD>(p.c);
         sh.total = (int64_t)p.c.batch * p.c.draft * each;
         sh.workers = sh.total < p.workers ? (int32_t)sh.total : p.workers;
         if (w >= sh.workers) return;
@@ -701,16 +798,16 @@ __global__ __launch_bounds__(NT, 1) void attend_kernel(AttendParams p) {
         sh.b = (int32_t)(sh.begin / each);
         sh.b_unit = (int64_t)sh.b * each;
     } else {
-        sh = dense_share<HEADS>(p.c, p.workers, w, sm.scan, &sm.found);
+        sh = dense_share<PLACES, HEAD>(p.c, p.workers, w);
         if (w >= sh.workers) return;
     }
-    Attend<DT, D, MT, SLOTS, HEADS> a(p, sm, mb);
+    Attend<DT, D, MT, SLOTS, MODE> a(p, sm, mb);
     int64_t x = sh.begin;
     int32_t b = sh.b;
     int64_t b_unit = sh.b_unit;
     while (x < sh.end) {
         const int32_t units =
-            units_of<HEADS>(SLOTS ? place_count<true>(p, 0) : uniform_len(p.c, b));
+            units_of<PLACES>(SLOTS ? place_count<true>(p, 0) : uniform_len(p.c, b));
         const int32_t h = (int32_t)((x - b_unit) / units);
         const int64_t g0 = b_unit + (int64_t)h * units, g1 = g0 + units;
         const int64_t x1 = g1 < sh.end ? g1 : sh.end;
@@ -725,48 +822,49 @@ __global__ __launch_bounds__(NT, 1) void attend_kernel(AttendParams p) {
             a.finish_part(a.part(w, w0, whole_start), w0, w1, whole_start);
         }
         x = x1;
-        if (h + 1 == head_units<HEADS>(p.c) && x1 == g1) {
+        if (h + 1 == head_units<HEAD>(p.c) && x1 == g1) {
             b_unit = g1;
             ++b;
         }
     }
 }
 
-template <int DT, int D, int MT, bool SLOTS, bool HEADS>
+template <int DT, int D, int MT, bool SLOTS, int MODE>
 static hipError_t launch_one(const AttendParams& p, hipStream_t stream) {
     const uint32_t grid = (uint32_t)((p.workers + 7) / 8 * 8 * p.row_blocks);
-    hipLaunchKernelGGL((attend_kernel<DT, D, MT, SLOTS, HEADS>), dim3(grid), dim3(NT), 0, stream, p);
+    hipLaunchKernelGGL((attend_kernel<DT, D, MT, SLOTS, MODE>), dim3(grid),
+                       dim3(threads_of(MODE)), 0, stream, p);
     return hipGetLastError();
 }
 
 template <int DT, int D, bool SLOTS>
-static hipError_t launch_mt(int mt, const AttendParams& p, hipStream_t stream) {
+static hipError_t launch_mode(const AttendParams& p, hipStream_t stream) {
     if constexpr (!SLOTS) {
         if (p.heads_on_waves)
-            return mt == 1 ? launch_one<DT, D, 1, SLOTS, true>(p, stream)
-                           : launch_one<DT, D, 2, SLOTS, true>(p, stream);
+            return p.rows <= 16 ? launch_one<DT, D, 1, SLOTS, HEADS>(p, stream)
+                                : launch_one<DT, D, 2, SLOTS, HEADS>(p, stream);
     }
-    switch (mt) {
-        case 1: return launch_one<DT, D, 1, SLOTS, false>(p, stream);
-        case 2: return launch_one<DT, D, 2, SLOTS, false>(p, stream);
+    switch (p.block_rows) {
+        case 16: return launch_one<DT, D, 1, SLOTS, KEYS>(p, stream);
+        case 32: return launch_one<DT, D, 2, SLOTS, KEYS>(p, stream);
+        case 64: return launch_one<DT, D, 2, SLOTS, WIDE2>(p, stream);
     }
-    return launch_one<DT, D, 4, SLOTS, false>(p, stream);
+    return launch_one<DT, D, 2, SLOTS, WIDE4>(p, stream);
 }
 
-hipError_t launch_attend(int dtype, int head_dim, int mt, const AttendParams& p,
-                         hipStream_t stream) {
+hipError_t launch_attend(int dtype, int head_dim, const AttendParams& p, hipStream_t stream) {
     if (dtype == BF16) {
         if (head_dim == 64)
-            return p.slots ? launch_mt<BF16, 64, true>(mt, p, stream)
-                           : launch_mt<BF16, 64, false>(mt, p, stream);
-        return p.slots ? launch_mt<BF16, 128, true>(mt, p, stream)
-                       : launch_mt<BF16, 128, false>(mt, p, stream);
+            return p.slots ? launch_mode<BF16, 64, true>(p, stream)
+                           : launch_mode<BF16, 64, false>(p, stream);
+        return p.slots ? launch_mode<BF16, 128, true>(p, stream)
+                       : launch_mode<BF16, 128, false>(p, stream);
     }
     if (head_dim == 64)
-        return p.slots ? launch_mt<F16, 64, true>(mt, p, stream)
-                       : launch_mt<F16, 64, false>(mt, p, stream);
-    return p.slots ? launch_mt<F16, 128, true>(mt, p, stream)
-                   : launch_mt<F16, 128, false>(mt, p, stream);
+        return p.slots ? launch_mode<F16, 64, true>(p, stream)
+                       : launch_mode<F16, 64, false>(p, stream);
+    return p.slots ? launch_mode<F16, 128, true>(p, stream)
+                   : launch_mode<F16, 128, false>(p, stream);
 }
 
 }  // namespace vts

@@ -12,9 +12,6 @@ namespace vts {
 // Drafted tokens of a request, at most: the bits of one tree_mask word.
 constexpr int MAX_DRAFT = 64;
 constexpr int MAX_HEADS = 8192;
-// Positions of one unit of work: four waves of 32 (32 where each wave has a KV
-// head of its own).
-constexpr int UNIT = 128;
 // Workgroups that may hold a ticket: two words each are the fixed first part of
 // every decode workspace, so that calls of different shapes can share one.
 constexpr int MAX_TICKETS = 8192;
@@ -51,13 +48,14 @@ struct AttendParams {
     float* lse;  // or null
     // plan
     int32_t rows;      // query rows that share one list of positions: draft * group, or group
-    int32_t row_blocks;  // blocks of 16 * MT rows
+    int32_t block_rows;  // 16, 32, 64 or 128 rows to a workgroup (times four heads)
+    int32_t row_blocks;
     int32_t workers;   // workgroups per row block
     // 1: a workgroup's waves take a KV head each and walk the same places, so that
     // it reads whole rows of the cache; 0: they take 32 places each of one head
     int32_t heads_on_waves;
     uint32_t* tickets;
-    // two parts per workgroup, of 16 * MT rows (times four heads): outputs
+    // two parts per workgroup, of block_rows rows (times four heads): outputs
     // [..][D], maximum and sum [..][2]
     float* part_o;
     float* part_ml;
@@ -123,7 +121,7 @@ struct VerifyParams {
     VerifyState* states;  // [batch][2]
 };
 
-hipError_t launch_attend(int dtype, int head_dim, int mt, const AttendParams& p, hipStream_t stream);
+hipError_t launch_attend(int dtype, int head_dim, const AttendParams& p, hipStream_t stream);
 hipError_t launch_weigh(int dtype, int head_dim, const WeighParams& p, hipStream_t stream);
 hipError_t launch_evict(const EvictParams& p, hipStream_t stream);
 hipError_t launch_verify(int dtype, const VerifyParams& p, hipStream_t stream);

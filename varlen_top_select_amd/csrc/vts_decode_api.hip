@@ -17,6 +17,8 @@ using namespace vts;
 // Compute units the plans are made for; a constant, so that the plan and the
 // workspace size do not depend on a device query.
 constexpr int32_t CUS = 256;
+// Kernels look a few units past the end of a list: places stay below 2^31.
+constexpr int32_t MARGIN = 1024;
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
@@ -83,9 +85,9 @@ int paged(const vts_paged_cache* c, int32_t draft, int32_t heads, bool with_v, P
     out->page_shift = -1;
     if ((c->page_size & (c->page_size - 1)) == 0) out->page_shift = __builtin_ctz(c->page_size);
     const int64_t cap = c->page_table_width > INT32_MAX / c->page_size
-                            ? INT32_MAX - UNIT * 4
+                            ? INT32_MAX - MARGIN
                             : c->page_table_width * c->page_size;
-    out->capacity = (int32_t)(cap > INT32_MAX - UNIT * 4 ? INT32_MAX - UNIT * 4 : cap);
+    out->capacity = (int32_t)(cap > INT32_MAX - MARGIN ? INT32_MAX - MARGIN : cap);
     out->seq_lens = c->seq_lens;
     out->batch = c->batch;
     out->draft = draft;
@@ -104,12 +106,12 @@ int check_q(const void* q, const int64_t* strides) {
 }
 
 struct AttendPlan {
-    int32_t rows, mt, row_blocks, workers, heads_on_waves;
+    int32_t rows, block_rows, row_blocks, workers, heads_on_waves;
     size_t part_o, part_ml, total;
 };
 
-// Rows go to blocks of 16, 32 or 64, the smallest that holds them (64 from 33
-// on).  One workgroup per compute unit, shared among the blocks of rows: with
+// Rows go to blocks of 16, 32, 64 or 128, the smallest that holds them (128 from
+// 65 on).  One workgroup per compute unit, shared among the blocks of rows: with
 // 16 KB on its way per wave it keeps the memory busy, and two of them per unit
 // read more places of the cache at once and are slower (64 requests up to
 // 16384, 64 heads: 504 us with two, 467 with one, 546 with three).
@@ -117,8 +119,9 @@ int attend_plan(int64_t batch, int32_t draft, int32_t heads, int32_t kv_heads, i
                 int32_t top_k, AttendPlan* out) {
     const int32_t group = heads / kv_heads;
     out->rows = top_k > 0 ? group : draft * group;
-    out->mt = out->rows <= 16 ? 1 : out->rows <= 32 ? 2 : 4;
-    const int32_t block = 16 * out->mt;
+    int32_t block = 16;
+    while (block < out->rows && block < 128) block *= 2;
+    out->block_rows = block;
     out->row_blocks = (out->rows + block - 1) / block;
     if (out->row_blocks > MAX_TICKETS) return VTS_ERR_UNSUPPORTED;
     out->workers = CUS / out->row_blocks;
@@ -126,11 +129,11 @@ int attend_plan(int64_t batch, int32_t draft, int32_t heads, int32_t kv_heads, i
     if (out->workers > MAX_TICKETS / out->row_blocks) out->workers = MAX_TICKETS / out->row_blocks;
     // A workgroup that reads whole rows of the cache, four heads of them, reads
     // faster than one that reads every kv_heads-th 256 bytes (see vts_attend.hip);
-    // 64 rows a head do not fit, and slots lie apart in either case.
+    // more rows a head do not fit, and slots lie apart in either case.
     // The workgroups that share a list leave four times the parts, so not where
     // many share one.
     out->heads_on_waves =
-        top_k == 0 && out->mt <= 2 && kv_heads % 4 == 0 && batch * kv_heads >= 128;
+        top_k == 0 && block <= 32 && kv_heads % 4 == 0 && batch * kv_heads >= 128;
     const size_t parts =
         2 * (size_t)out->workers * out->row_blocks * block * (out->heads_on_waves ? 4 : 1);
     out->part_o = TICKET_BYTES;
@@ -187,7 +190,7 @@ int vts_tree_attention(const vts_paged_cache* cache, const void* q, const int64_
     int st = paged(cache, draft, heads, true, &p.c);
     if (st != VTS_OK) return st;
     if (slots != nullptr ? top_k < 1 : top_k != 0) return VTS_ERR_INVALID;
-    if (top_k > INT32_MAX - 4 * UNIT) return VTS_ERR_UNSUPPORTED;
+    if (top_k > INT32_MAX - MARGIN) return VTS_ERR_UNSUPPORTED;
     if (isnan(scale)) return VTS_ERR_INVALID;
     if (p.c.batch == 0) return VTS_OK;
     st = check_q(q, q_strides);
@@ -216,6 +219,7 @@ int vts_tree_attention(const vts_paged_cache* cache, const void* q, const int64_
     p.out = out;
     p.lse = lse;
     p.rows = plan.rows;
+    p.block_rows = plan.block_rows;
     p.row_blocks = plan.row_blocks;
     p.workers = plan.workers;
     p.heads_on_waves = plan.heads_on_waves;
@@ -223,7 +227,7 @@ int vts_tree_attention(const vts_paged_cache* cache, const void* q, const int64_
     p.tickets = reinterpret_cast<uint32_t*>(w);
     p.part_o = reinterpret_cast<float*>(w + plan.part_o);
     p.part_ml = reinterpret_cast<float*>(w + plan.part_ml);
-    return launch_attend(cache->dtype, cache->head_dim, plan.mt, p,
+    return launch_attend(cache->dtype, cache->head_dim, p,
                          static_cast<hipStream_t>(stream)) == hipSuccess
                ? VTS_OK
                : VTS_ERR_HIP;

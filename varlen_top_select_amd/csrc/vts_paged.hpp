@@ -99,7 +99,7 @@ __device__ __forceinline__ Entry issue_entry(const PagedParams& c, const Places&
     e.entry = -1;
     e.pos = j;
     if constexpr (SLOTS) {
-        if (j < pl.top_k) e.slot = gload(pl.slots + j);
+        if (j >= 0 && j < pl.top_k) e.slot = gload(pl.slots + j);
         e.pos = j < pl.top_k ? -1 : pl.draft_pos + (j - pl.top_k);
     }
     if (j < pl.count && e.pos >= 0 && e.pos < c.capacity) {
@@ -147,9 +147,9 @@ __device__ __forceinline__ int swizzled(int r) {
     return D == 128 ? r & 15 : (r >> 1) & 7;
 }
 
-// ---- shares of the work: units of `UNIT` places (of 32 where the four waves
-// take a KV head each), in order of request and KV head (or four heads);
-// worker w of W takes units [w * total / W, (w + 1) * total / W).
+// ---- shares of the work: units of PLACES places, in order of request and KV
+// head (or four heads); worker w of W takes units [w * total / W,
+// (w + 1) * total / W).
 
 __device__ __forceinline__ int64_t share_start(int64_t total, int32_t workers, int32_t w) {
     return total * w / workers;
@@ -159,38 +159,14 @@ __device__ __forceinline__ int32_t share_of(int64_t total, int32_t workers, int6
     return (int32_t)(((x + 1) * workers - 1) / total);
 }
 
-template <bool HEADS>
+template <int PLACES>
 __device__ __forceinline__ int32_t units_of(int32_t count) {
-    constexpr int32_t U = HEADS ? 32 : UNIT;
-    return count <= 0 ? 1 : (count + U - 1) / U;
+    return count <= 0 ? 1 : (count + PLACES - 1) / PLACES;
 }
 // units that differ by KV head alone
 template <bool HEADS>
 __device__ __forceinline__ int32_t head_units(const PagedParams& c) {
     return HEADS ? c.kv_heads / WAVES : c.kv_heads;
-}
-
-// Sum over the block of one value per thread, and the sum over the threads
-// before this one.  `sm`: WAVES words.
-__device__ __forceinline__ int64_t block_prefix(int64_t v, int64_t* sm, int64_t& total) {
-    int64_t inc = v;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int64_t o = __shfl_up(inc, d);
-        if ((int)lane_id() >= d) inc += o;
-    }
-    const int wave = threadIdx.x >> 6;
-    __syncthreads();
-    if (lane_id() == 63) sm[wave] = inc;
-    __syncthreads();
-    int64_t before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
-        if (w < wave) before += sm[w];
-        total += sm[w];
-    }
-    return before + inc - v;
 }
 
 // Where a worker's share begins: request, KV head, unit, and the totals.
@@ -207,62 +183,68 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
     return (int64_t)(((uint64_t)hi << 32) | lo);
 }
 
-// Shares over the batch's dense lengths.  Every thread of the block calls it.
-template <bool HEADS>
-__device__ __forceinline__ Share dense_share(const PagedParams& c, int32_t workers, int32_t w,
-                                             int64_t* sm, int32_t* found) {
-    Share s;
+// Shares over the batch's dense lengths.  Every wave finds the same by itself,
+// four requests to a lane and 256 at a time.
+template <int PLACES, bool HEADS>
+__device__ __forceinline__ Share dense_share(const PagedParams& c, int32_t workers, int32_t w) {
+    constexpr int PER = 4, STEP = 64 * PER;
     const int32_t heads = head_units<HEADS>(c);
-    const auto units = [&](int32_t b) -> int64_t {
-        return b < c.batch ? (int64_t)units_of<HEADS>(clamped_len(c, b)) * heads : 0;
-    };
-    int64_t total = 0, sum = 0;
-    if (c.batch <= 64) {  // a request to a lane; every wave finds the same
-        const int lane = lane_id();
-        const int64_t u = units(lane);
-        int64_t inc = u;
+    const int lane = lane_id();
+    int64_t u[PER];
+    // the lane's units, their sum over the lanes up to this one, and over all
+    const auto scan = [&](int32_t b0, int64_t& all) -> int64_t {
+        int64_t inc = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int32_t b = b0 + lane * PER + i;
+            u[i] = b < c.batch ? (int64_t)units_of<PLACES>(clamped_len(c, b)) * heads : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) inc += u[i];
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
             const int64_t o = __shfl_up(inc, d);
             if (lane >= d) inc += o;
         }
-        s.total = uniform64(__shfl(inc, 63));
-        s.workers = s.total < workers ? (int32_t)s.total : workers;
-        s.begin = s.end = s.b_unit = 0;
-        s.b = 0;
-        if (w >= s.workers) return s;
-        s.begin = share_start(s.total, s.workers, w);
-        s.end = share_start(s.total, s.workers, w + 1);
-        s.b = __builtin_ctzll(ballot(s.begin < inc));
-        s.b_unit = uniform64(__shfl(inc - u, s.b));
-        return s;
+        all = uniform64(__shfl(inc, 63));
+        return inc;
+    };
+    Share s;
+    s.total = 0;
+    int64_t all, inc = 0;
+    for (int32_t b0 = 0; b0 < c.batch; b0 += STEP) {
+        inc = scan(b0, all);
+        s.total += all;
     }
-    for (int32_t b0 = 0; b0 < c.batch; b0 += NT) {
-        block_prefix(units(b0 + (int32_t)threadIdx.x), sm, sum);
-        total += sum;
-    }
-    s.total = total = uniform64(total);
-    s.workers = total < workers ? (int32_t)total : workers;
+    s.workers = s.total < workers ? (int32_t)s.total : workers;
     s.begin = s.end = s.b_unit = 0;
     s.b = 0;
     if (w >= s.workers) return s;
-    s.begin = share_start(total, s.workers, w);
-    s.end = share_start(total, s.workers, w + 1);
+    s.begin = share_start(s.total, s.workers, w);
+    s.end = share_start(s.total, s.workers, w + 1);
     int64_t base = 0;
-    for (int32_t b0 = 0; b0 < c.batch; b0 += NT) {
-        const int32_t b = b0 + (int32_t)threadIdx.x;
-        const int64_t u = units(b);
-        const int64_t at = base + block_prefix(u, sm, sum);
-        if (s.begin >= at && s.begin < at + u) {
-            found[0] = b;
-            sm[WAVES] = at;
+    for (int32_t b0 = 0; b0 < c.batch; b0 += STEP) {
+        if (c.batch > STEP) inc = scan(b0, all);  // (of one step the first scan is at hand)
+        const uint64_t past = ballot(s.begin < base + inc);
+        if (past) {
+            const int at = __builtin_ctzll(past);
+            // within that lane's requests
+            int64_t start = base + inc;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) start -= u[i];
+            int32_t b = b0 + lane * PER;
+#pragma unroll
+            for (int i = 0; i < PER - 1; ++i)
+                if (s.begin >= start + u[i] && b == b0 + lane * PER + i) {
+                    start += u[i];
+                    ++b;
+                }
+            s.b = __builtin_amdgcn_readfirstlane(__shfl(b, at));
+            s.b_unit = uniform64(__shfl(start, at));
+            return s;
         }
-        base += sum;
+        base += all;
     }
-    __syncthreads();
-    s.b = __builtin_amdgcn_readfirstlane(found[0]);
-    s.b_unit = uniform64(sm[WAVES]);
-    __syncthreads();
     return s;
 }
 

@@ -22,8 +22,6 @@ template <int D, int ROWS>
 struct WeighShared {
     u32x4 k[WAVES][32 * (D / 8)];
     u32x4 q[ROWS == ROWS_LDS ? 16 * (D / 32) : 1][64];  // 256 rows, or 64 of each wave's
-    int64_t scan[WAVES + 1];
-    int32_t found;
 };
 
 // What a lane holds of row `row`: its operands, and when it counts its log-sum-exp.
@@ -60,10 +58,10 @@ struct WeighRow {
 
 template <int DT, int D, bool HEADS, int ROWS>
 __global__ __launch_bounds__(NT, ROWS == ROWS_LDS && D == 128 ? 1 : 2) void weigh_kernel(WeighParams p) {
-    constexpr int KS = D / 32, CH = D / 8, RPL = 64 / CH;
+    constexpr int KS = D / 32, CH = D / 8, RPL = 64 / CH, PLACES = HEADS ? 32 : 32 * WAVES;
     __shared__ WeighShared<D, ROWS> sm;
     const PagedParams& c = p.c;
-    const Share sh = dense_share<HEADS>(c, p.workers, (int32_t)blockIdx.x, sm.scan, &sm.found);
+    const Share sh = dense_share<PLACES, HEADS>(c, p.workers, (int32_t)blockIdx.x);
     if ((int32_t)blockIdx.x >= sh.workers) return;
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, grp = lane >> 4;
@@ -74,7 +72,7 @@ __global__ __launch_bounds__(NT, ROWS == ROWS_LDS && D == 128 ? 1 : 2) void weig
     int64_t b_unit = sh.b_unit;
     while (x < sh.end) {
         const int32_t n = uniform_len(c, b);
-        const int32_t units = units_of<HEADS>(n);
+        const int32_t units = units_of<PLACES>(n);
         const int32_t hu = (int32_t)((x - b_unit) / units);
         const int32_t h = HEADS ? hu * WAVES + wave : hu;
         const int64_t g0 = b_unit + (int64_t)hu * units, g1 = g0 + units;
@@ -89,7 +87,7 @@ __global__ __launch_bounds__(NT, ROWS == ROWS_LDS && D == 128 ? 1 : 2) void weig
         pl.table = c.table + (int64_t)b * c.table_stride;
         const char* kbase = (const char*)c.k.base + (((uint64_t)h * c.k.head_stride) << 4);
         float* wrow = p.weights + b * p.w_batch + h * p.w_head;
-        const auto first_place = [&](int32_t u) { return HEADS ? u * 32 : u * UNIT + wave * 32; };
+        const auto first_place = [&](int32_t u) { return HEADS ? u * 32 : u * PLACES + wave * 32; };
         const auto issue = [&](int32_t u) {
             return issue_entry<false>(c, pl, first_place(u) + (lane & 31));
         };

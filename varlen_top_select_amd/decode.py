@@ -34,14 +34,19 @@ MAX_DRAFT = 64
 # plain numbers, which costs a fraction of comparing torch.device objects.
 
 
+# the current stream's handle of a device, without making a Stream object of it
+_current = getattr(torch._C, "_cuda_getCurrentRawStream",
+                   lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _run(stream, index, call):
     """call(stream pointer) with device `index` and, where one is given, `stream`
     current, so that what the call allocates belongs to the stream it runs on."""
     if stream is None:
         if index == torch.cuda.current_device():
-            return call(torch.cuda.current_stream().cuda_stream)
+            return call(_current(index))
         with torch.cuda.device(index):
-            return call(torch.cuda.current_stream().cuda_stream)
+            return call(_current(index))
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=index)
     with torch.cuda.device(index), torch.cuda.stream(stream):
