@@ -72,6 +72,10 @@ struct Attend {
     using S = AttendShape<D, MT, MODE>;
     static constexpr bool HEAD = MODE == HEADS, WIDE = S::WIDE;
     static constexpr int T = S::NW * 64;    // threads
+    // whether a cache row is read once by the whole call, as far as it is known
+    // (the slots of two rows may be the same): such loads leave the caches alone.
+    // 128 lists of 2048 slots, 64 heads: 112 us without, 104 with.
+    static constexpr bool ONCE = HEAD || (SLOTS && !WIDE);
     static constexpr int ROWS = S::ROWS;
     using VRow = typename std::conditional<D == 128, u32x4, u32x2>::type;
 
@@ -221,7 +225,7 @@ struct Attend {
         const uint32_t safe = off == NO_PLACE ? 0 : off;
 #pragma unroll
         for (int i = 0; i < (WIDE ? LOADS : 2 * KS); ++i)
-            k[i] = row_load<u32x4, HEAD>(kbase, from_lane(safe, i * RPL + lane / CH),
+            k[i] = row_load<u32x4, ONCE>(kbase, from_lane(safe, i * RPL + lane / CH),
                                          (lane % CH) * 16);
     }
     __device__ __forceinline__ void stage_k() {
@@ -272,7 +276,7 @@ struct Attend {
         const uint32_t safe = off == NO_PLACE ? 0 : off;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            v[j] = row_load<VRow, HEAD>(vbase, from_lane(safe, 32 + v_place(j)), col * VB);
+            v[j] = row_load<VRow, ONCE>(vbase, from_lane(safe, 32 + v_place(j)), col * VB);
     }
 
     // The tile's share of O: V rows turned so that each lane holds eight places

@@ -114,7 +114,8 @@ struct AttendPlan {
 // 65 on).  One workgroup per compute unit, shared among the blocks of rows: with
 // 16 KB on its way per wave it keeps the memory busy, and two of them per unit
 // read more places of the cache at once and are slower (64 requests up to
-// 16384, 64 heads: 504 us with two, 467 with one, 546 with three).
+// 16384, 64 heads: 504 us with two, 467 with one, 546 with three).  Slots lie
+// apart in any case, and two are faster there (99 us for 104).
 int attend_plan(int64_t batch, int32_t draft, int32_t heads, int32_t kv_heads, int32_t head_dim,
                 int32_t top_k, AttendPlan* out) {
     const int32_t group = heads / kv_heads;
@@ -124,7 +125,7 @@ int attend_plan(int64_t batch, int32_t draft, int32_t heads, int32_t kv_heads, i
     out->block_rows = block;
     out->row_blocks = (out->rows + block - 1) / block;
     if (out->row_blocks > MAX_TICKETS) return VTS_ERR_UNSUPPORTED;
-    out->workers = CUS / out->row_blocks;
+    out->workers = CUS * (top_k > 0 && block == 16 ? 2 : 1) / out->row_blocks;
     if (out->workers < 8) out->workers = 8;
     if (out->workers > MAX_TICKETS / out->row_blocks) out->workers = MAX_TICKETS / out->row_blocks;
     // A workgroup that reads whole rows of the cache, four heads of them, reads
