@@ -466,6 +466,7 @@ def check_evict(weights, k, v, table, n, keep, sinks, recent, same_cache=False, 
     ([300, 40], 24, 3, 128, 64, 0, 0),
     ([300, 64, 65], 64, 1, 64, 64, 10, 54),       # nothing but sinks and recent entries
     ([5000, 1025, 3000], 16, 2, 64, 1024, 1, 7),  # many tiles
+    ([16383, 16384, 16385, 30000], 64, 1, 64, 9000, 4, 100),
     ([9, 8, 7], 1, 2, 64, 1, 0, 1),
     ([9, 8, 7], 1, 2, 64, 1, 0, 0),
 ])

@@ -4,7 +4,14 @@
 // weight of the last entry to stay by a radix select over order-preserving
 // keys (8 bits a pass), then writes the kept positions in order; of equal
 // weights the lowest positions stay.  evict_move: the kept K and V rows go to
-// the new pages, 16 bytes a lane.
+// the new pages, 16 bytes a lane; that is nearly all of the traffic and runs at
+// the rate of a large copy (32 requests of up to 8192 to 4096, 8 heads of 128:
+// 208 us of 233, 5.0 TB/s).
+//
+// The select reads the weights again in each pass, from the cache.  With the
+// keys of 16384 entries in registers, its loops unrolled, the same batch took 228
+// us, but one row of 1088 18 us for 13: code that runs once waits for its own
+// instructions.
 #include "vts_paged.hpp"
 
 namespace vts {

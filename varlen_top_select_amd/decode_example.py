@@ -145,8 +145,8 @@ class Decoder:
 
 
 def main() -> None:
-    steps = int(sys.argv[1]) if len(sys.argv) > 1 else 60
-    decoder = Decoder()
+    steps = int(sys.argv[1]) if len(sys.argv) > 1 else 150
+    decoder = Decoder(capacity=4 * (steps + 1))
     accepted = 0
     for _ in range(steps):
         count, _ = decoder.step()
