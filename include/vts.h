@@ -1,13 +1,21 @@
 /*
- * vts.h -- exact batched variable-length top-K selection (C ABI).
+ * vts.h -- exact batched variable-length top-K selection and the operators
+ * that follow it in a decode step (C ABI).
  *
- * Two operations, both asynchronous on the caller's HIP stream, both exact
- * with ties interchangeable:
+ * The selections, asynchronous on the caller's HIP stream, exact with ties
+ * interchangeable:
  *
  *   vts_topk_varlen                 decode-step top-k with per-request lengths
  *   vts_topk_varlen_ordered         the same in canonical order with a tie-break
  *   vts_topk_page_table_transform   top-k over row windows, fused with a
  *                                   page-table translation of the indices
+ *
+ * The decode-step operators over a paged KV cache (further down):
+ *
+ *   vts_tree_attention              attention of drafted tokens
+ *   vts_attention_weight_add        attention weight per cached entry
+ *   vts_evict_cache                 eviction by that weight
+ *   vts_verify_draft                acceptance of drafted tokens
  *
  * The unprefixed names topk_varlen and topk_page_table_transform are exported
  * as aliases of the two entry points.
