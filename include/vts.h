@@ -362,7 +362,8 @@ int topk_page_table_transform(const void* scores, int32_t dtype, int64_t num_row
  *            128) consecutive elements.
  * k_strides, v_strides  elements between pages, positions of a page, and
  *            heads, multiples of 8: any order of the three dimensions is
- *            possible.  A cache spans at most 2^32 16-byte vectors.
+ *            possible.  A cache spans at most 2^32 16-byte vectors and
+ *            2^31 - 1 positions.
  * page_table device int32[batch, page_table_width], rows page_table_stride
  *            entries apart.
  * seq_lens   device int32[batch].
@@ -406,7 +407,8 @@ typedef struct {
  * heads      a multiple of kv_heads, at most 8192.
  * tree_mask  device int64[batch, draft] or NULL.
  * slots      device int32[batch, draft, top_k] or NULL (then top_k is 0).
- * out        device, dtype[batch, draft, heads, head_dim], 16-byte aligned.
+ * out        device, dtype[batch, draft, heads, head_dim], 16-byte aligned; must
+ *            not overlap q or the caches.
  * lse        device float[batch, draft, heads] or NULL.
  * workspace  device, 16-byte aligned, at least
  *            vts_tree_attention_workspace_bytes(...) bytes, zeroed once.  The
@@ -463,7 +465,8 @@ int vts_attention_weight_add(const vts_paged_cache* cache, const void* q,
  * An entry whose page is not there is moved as zeros; a row whose out_page_table
  * entry is outside [0, out_pages) is not written.
  *
- * sinks + recent <= keep; out_page_table_width >= ceil(keep / page_size).
+ * sinks + recent <= keep; out_page_table_width >= ceil(keep / page_size).  At most
+ * 2^21 pairs of request and KV head, and 2^23 blocks of 64 kept entries in all.
  */
 int vts_evict_cache(const vts_paged_cache* cache, const float* weights,
                     int64_t weights_batch_stride, int64_t weights_head_stride, int64_t width,
@@ -491,6 +494,7 @@ int vts_evict_cache(const vts_paged_cache* cache, const float* weights,
  * first v whose running sum of r passes uniforms[b, draft] times r's whole sum
  * (if r has no mass, p's; if p has none, -1).
  *
+ * At most 64 drafted tokens, 2^21 requests and 2^31 - 2^16 - 1 tokens of vocabulary.
  * Probabilities are used as they are given; NaN and negative values count as
  * 0.  A token outside [0, vocab) or a parent outside [-1, t) makes a node that
  * is never accepted.  Sums and comparisons are in 64 bits.

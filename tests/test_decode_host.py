@@ -134,6 +134,7 @@ def test_evict_refuses_caches(lib, kw, want):
     (dict(vo=A + 2), INVALID), (dict(os=(64, 4, 8)), INVALID), (dict(w=None), INVALID),
     (dict(table=None), INVALID), (dict(kept=None), INVALID), (dict(lens=None), INVALID),
     (dict(ow=None), INVALID), (dict(ow=A + 64), INVALID),
+    (dict(keep=1 << 30, twidth=1 << 24, stride=1 << 24), UNSUPPORTED),
 ])
 def test_evict_refuses(lib, kw, want):
     assert evict(lib, **kw) == want
@@ -156,7 +157,7 @@ def verify(lib, **kw):
     (dict(q=A + 1), INVALID), (dict(tokens=None), INVALID), (dict(u=None), INVALID),
     (dict(path=None), INVALID), (dict(count=None), INVALID), (dict(token=None), INVALID),
     (dict(ws=None), WORKSPACE), (dict(ws=A + 8), WORKSPACE), (dict(bytes=64), WORKSPACE),
-    (dict(batch=0), OK),
+    (dict(batch=0), OK), (dict(batch=(1 << 21) + 1), UNSUPPORTED),
 ])
 def test_verify_refuses(lib, kw, want):
     assert verify(lib, **kw) == want

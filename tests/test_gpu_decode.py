@@ -312,6 +312,27 @@ def test_attend_repeats_and_shares_workspaces():
         assert all(torch.equal(x, y) for x, y in zip(first, again))
 
 
+def test_own_workspace():
+    gen = torch.Generator().manual_seed(23)
+    k, v, table, n = make_cache(gen, [900, 50], 16, 2, 128, torch.bfloat16)
+    q = torch.randn(2, 2, 16, 128, generator=gen).bfloat16().to(DEV)
+    need = vts.decode.tree_attention_workspace_bytes(2, 2, 16, 2, 128)
+    ws = torch.zeros(need, dtype=torch.uint8, device=DEV)
+    want = vts.tree_attention(q, k, v, table, n)[0]
+    assert torch.equal(vts.tree_attention(q, k, v, table, n, workspace=ws)[0], want)
+    tickets = ws[:65536].clone()
+    assert not tickets.any()  # left as they were
+    with pytest.raises(vts.VtsError):
+        vts.tree_attention(q, k, v, table, n, workspace=ws[: need - 256])
+    with pytest.raises(ValueError, match="workspace"):
+        vts.tree_attention(q, k, v, table, n, workspace=ws.cpu())
+    probs = torch.softmax(torch.randn(2, 3, 9000, generator=gen), -1).to(DEV)
+    toks, u = torch.zeros(2, 2, dtype=torch.int32, device=DEV), torch.rand(2, 3, generator=gen).to(DEV)
+    ws = torch.zeros(vts.decode.verify_draft_workspace_bytes(2, 9000), dtype=torch.uint8, device=DEV)
+    want = vts.verify_draft(probs, toks, u)
+    assert all(torch.equal(a, b) for a, b in zip(want, vts.verify_draft(probs, toks, u, workspace=ws)))
+
+
 def test_streams():
     """A stream that is not the current one: its own outputs and workspace."""
     gen = torch.Generator().manual_seed(21)

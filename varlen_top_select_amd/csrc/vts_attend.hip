@@ -793,14 +793,14 @@ __global__ __launch_bounds__(threads_of(MODE), MODE >= WIDE2 ? 2 : 1) void atten
     if (w >= p.workers) return;
     Share sh;
     if constexpr (SLOTS) {
-        const int32_t each = units_of<PLACES>(place_count<true>(p, 0)) * head_units<HEAD>(p.c);
-        sh.total = (int64_t)p.c.batch * p.c.draft * each;
+        const int64_t each = (int64_t)units_of<PLACES>(place_count<true>(p, 0)) * head_units<HEAD>(p.c);
+        sh.total = p.c.batch * p.c.draft * each;
         sh.workers = sh.total < p.workers ? (int32_t)sh.total : p.workers;
         if (w >= sh.workers) return;
         sh.begin = share_start(sh.total, sh.workers, w);
         sh.end = share_start(sh.total, sh.workers, w + 1);
         sh.b = (int32_t)(sh.begin / each);
-        sh.b_unit = (int64_t)sh.b * each;
+        sh.b_unit = sh.b * each;
     } else {
         sh = dense_share<PLACES, HEAD>(p.c, p.workers, w);
         if (w >= sh.workers) return;

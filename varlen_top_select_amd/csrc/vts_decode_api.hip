@@ -302,7 +302,8 @@ int vts_evict_cache(const vts_paged_cache* cache, const float* weights,
     if (st != VTS_OK) return st;
     if (p.c.batch == 0) return VTS_OK;
     const int64_t rows = (int64_t)p.c.batch * cache->kv_heads;
-    if (rows * ((keep + 63) / 64) > INT32_MAX) return VTS_ERR_UNSUPPORTED;
+    // a grid has below 2^32 threads: 1024 to a row, then 256 to 64 kept rows
+    if (rows > (1 << 21) || rows * (((int64_t)keep + 63) / 64) > (1 << 23)) return VTS_ERR_UNSUPPORTED;
     if (weights == nullptr || out_page_table == nullptr || kept == nullptr ||
         out_lens == nullptr || out_weights == nullptr || !aligned(weights, 4) ||
         !aligned(kept, 4) || !aligned(out_weights, 4))
@@ -343,7 +344,8 @@ int vts_verify_draft(const void* target_probs, int32_t dtype, int64_t target_bat
     if (target_batch_stride < 0 || target_row_stride < 0 || draft_batch_stride < 0 ||
         draft_row_stride < 0)
         return VTS_ERR_INVALID;
-    if (draft > MAX_DRAFT || vocab > INT32_MAX - 4096 || batch > INT32_MAX / 64)
+    // (a grid has below 2^32 threads; the scans look past the vocabulary's end)
+    if (draft > MAX_DRAFT || vocab > INT32_MAX - 65536 || batch > (1 << 21))
         return VTS_ERR_UNSUPPORTED;
     if (batch == 0) return VTS_OK;
     const size_t e = dtype == VTS_F32 ? 4 : 2;

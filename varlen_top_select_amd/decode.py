@@ -11,6 +11,10 @@ A cache is a 4-D tensor ``[num_pages, page_size, kv_heads, head_dim]`` of any
 strides that are multiples of 8 elements (so a cache laid out heads first is
 passed as a permuted view), bfloat16 or float16.  Lengths count the drafted
 tokens, as ``next_n`` does in ``topk_varlen``.
+
+Without ``workspace`` the calls share one per device and stream, made at the first
+eager call; one of one's own is ``torch.zeros`` of the bytes that
+``tree_attention_workspace_bytes`` or ``verify_draft_workspace_bytes`` says.
 """
 from __future__ import annotations
 
@@ -23,7 +27,8 @@ import torch
 from . import _DTYPE, _check, _default_workspace, library
 
 __all__ = ["tree_attention", "attention_weight_add", "evict_cache", "verify_draft",
-           "tree_mask_from_parents"]
+           "tree_mask_from_parents", "tree_attention_workspace_bytes",
+           "verify_draft_workspace_bytes"]
 
 _CACHE = struct.Struct("@QQqqqqqqQqqQqiiiii4x")  # vts_paged_cache
 _STRIDES = struct.Struct("@qqq")
@@ -56,18 +61,21 @@ def _run(stream, index, call):
 def _workspace(workspace, need, device, sp):
     if workspace is None:
         return _default_workspace(need, device, sp, "decode")
-    if workspace.device != device or not workspace.is_contiguous():
+    if (not isinstance(workspace, torch.Tensor) or workspace.device != device
+            or not workspace.is_contiguous()):
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     return workspace
 
 
 @functools.lru_cache(maxsize=256)
-def _attention_bytes(batch, draft, heads, kv_heads, head_dim, top_k):
+def tree_attention_workspace_bytes(batch, draft, heads, kv_heads, head_dim, top_k=0):
+    """Bytes of a workspace (zeroed once) for tree_attention calls of this shape."""
     return library().vts_tree_attention_workspace_bytes(batch, draft, heads, kv_heads, head_dim, top_k)
 
 
 @functools.lru_cache(maxsize=256)
-def _verify_bytes(batch, vocab):
+def verify_draft_workspace_bytes(batch, vocab):
+    """Bytes of a workspace (zeroed once) for verify_draft calls of this shape."""
     return library().vts_verify_draft_workspace_bytes(batch, vocab)
 
 
@@ -173,7 +181,7 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
                         device=device) if out is None else out
         lse = torch.empty((batch, draft, heads), dtype=torch.float32,
                           device=device) if return_lse else None
-        ws = _workspace(workspace, _attention_bytes(batch, draft, heads, kv_heads, head_dim, top_k),
+        ws = _workspace(workspace, tree_attention_workspace_bytes(batch, draft, heads, kv_heads, head_dim, top_k),
                         device, sp)
         _check("vts_tree_attention", lib.vts_tree_attention(
             cache, q.data_ptr(), q_strides, draft, heads, mask_ptr, slots_ptr, top_k, scale,
@@ -302,7 +310,7 @@ def verify_draft(target_probs: torch.Tensor, draft_tokens: torch.Tensor, uniform
         path = torch.empty((batch, draft), dtype=torch.int32, device=device)
         count = torch.empty((batch,), dtype=torch.int32, device=device)
         token = torch.empty((batch,), dtype=torch.int32, device=device)
-        ws = _workspace(workspace, _verify_bytes(batch, vocab), device, sp)
+        ws = _workspace(workspace, verify_draft_workspace_bytes(batch, vocab), device, sp)
         _check("vts_verify_draft", lib.vts_verify_draft(
             target_probs.data_ptr(), _DTYPE[target_probs.dtype], target_probs.stride(0),
             target_probs.stride(1), q_ptr, qb, qr, draft_tokens.data_ptr(), parents_ptr,
