@@ -58,7 +58,6 @@ struct AttendShared : AttendShape<D, MT, MODE> {
         float o[MODE == HEADS ? 1 : S::WIDE ? S::KG - 1 : 2][MODE == HEADS ? 1 : S::ROWS][D + 4];
     };
     float ml[S::KG][S::ROWS][2];
-    float tops[S::NW * 64];
     uint32_t last;
 };
 
@@ -712,34 +711,20 @@ struct Attend {
 
     // Joins the parts of workers first, first + stride, ..: to the outputs, or
     // to the first one's slot.  Other workgroups' parts come from beyond this
-    // XCD, so their loads are issued eight at a time: one after the other,
-    // 32 parts took 40 us.
+    // XCD, so a thread's loads of 16 parts are issued together and its maximum is a
+    // running one: with the maxima in a pass of their own and eight parts at a
+    // time, one list of 4096 in 32 parts took 20 us for 18, one after the other
+    // 48.
     __device__ __forceinline__ void join_parts(int32_t first, int32_t stride, int32_t count,
                                                int32_t w0, bool w0_whole_start, bool to_outputs) {
-        constexpr int LANES = T / ROWS;  // threads to a row for the maxima
-        const int row = tid % ROWS, lane0 = tid / ROWS;
-        const auto there = [&](int r) { return row_at(r / (16 * MT), r % (16 * MT)) < p.rows; };
-        float top = NEG_INF;
-        if (there(row))
-            for (int32_t i = lane0; i < count; i += LANES)
-                top = fmaxf(top, gload(p.part_ml + part(first + i * stride, w0, w0_whole_start) *
-                                                       (ROWS * 2) + row * 2));
-        sm.tops[lane0 * ROWS + row] = top;
-        __syncthreads();
-        if (lane0 == 0) {
-#pragma unroll
-            for (int i = 1; i < LANES; ++i) top = fmaxf(top, sm.tops[i * ROWS + row]);
-            sm.ml[0][row][0] = top;
-        }
-        __syncthreads();
+        constexpr int U = 16;
         const int64_t to = part(first, w0, w0_whole_start);
         for (int x = tid * 4; x < ROWS * D; x += T * 4) {
             const int r = x / D;
-            if (!there(r)) continue;
-            const float base = sm.ml[0][r][0];
-            float sum = 0;
+            if (row_at(r / (16 * MT), r % (16 * MT)) >= p.rows) continue;
+            float top = NEG_INF, sum = 0;
             f32x4 acc = {0, 0, 0, 0};
-            constexpr int U = 8;
+#pragma unroll 1
             for (int32_t i = 0; i < count; i += U) {
                 f32x4 o4[U];
                 float mm[U], ll[U];
@@ -747,31 +732,44 @@ struct Attend {
                 for (int u = 0; u < U; ++u) {
                     const int32_t w = first + (i + u < count ? i + u : count - 1) * stride;
                     const int64_t at = part(w, w0, w0_whole_start);
+                    const u32x2 ml = gload((const u32x2*)(p.part_ml + at * (ROWS * 2) + r * 2));
                     o4[u] = gload((const f32x4*)(p.part_o + at * (ROWS * D) + x));
-                    mm[u] = gload(p.part_ml + at * (ROWS * 2) + r * 2);
-                    ll[u] = gload(p.part_ml + at * (ROWS * 2) + r * 2 + 1);
+                    const uint32_t m0 = ml[0], l0 = ml[1];
+                    mm[u] = __builtin_bit_cast(float, m0);
+                    ll[u] = __builtin_bit_cast(float, l0);
                 }
+                float up = top;
+#pragma unroll
+                for (int u = 0; u < U; ++u) up = fmaxf(up, mm[u]);  // (the last one again past count)
+                const float f0 = scale_to(top, up);
+                sum *= f0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[e] *= f0;
+                top = up;
 #pragma unroll
                 for (int u = 0; u < U; ++u)
                     if (i + u < count) {
-                        const float f = scale_to(mm[u], base);
+                        const float f = scale_to(mm[u], top);
                         sum += f * ll[u];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) acc[e] += f * o4[u][e];
                     }
             }
             if (to_outputs) {
-                write_row(r / (16 * MT), r % (16 * MT), x % D, acc, base, sum);
+                write_row(r / (16 * MT), r % (16 * MT), x % D, acc, top, sum);
             } else {
                 gstore((f32x4*)(p.part_o + to * (ROWS * D) + x), acc);
-                if (x % D == 0) sm.ml[0][r][1] = sum;
+                if (x % D == 0) {
+                    sm.ml[0][r][0] = top;
+                    sm.ml[0][r][1] = sum;
+                }
             }
         }
         if (to_outputs) return;
         __syncthreads();  // everyone has read the slot's maxima and sums
-        if (lane0 == 0 && there(row)) {
-            gstore(p.part_ml + to * (ROWS * 2) + row * 2, sm.ml[0][row][0]);
-            gstore(p.part_ml + to * (ROWS * 2) + row * 2 + 1, sm.ml[0][row][1]);
+        if (tid < ROWS && row_at(tid / (16 * MT), tid % (16 * MT)) < p.rows) {
+            gstore(p.part_ml + to * (ROWS * 2) + tid * 2, sm.ml[0][tid][0]);
+            gstore(p.part_ml + to * (ROWS * 2) + tid * 2 + 1, sm.ml[0][tid][1]);
         }
     }
     // A worker's slot: its first segment's, or the one of a list that begins
