@@ -710,68 +710,106 @@ struct Attend {
     }
 
     // Joins the parts of workers first, first + stride, ..: to the outputs, or
-    // to the first one's slot.  Other workgroups' parts come from beyond this
-    // XCD, so a thread's loads of 16 parts are issued together and its maximum is a
-    // running one: with the maxima in a pass of their own and eight parts at a
-    // time, one list of 4096 in 32 parts took 20 us for 18, one after the other
-    // 48.
+    // to the first one's slot.
     __device__ __forceinline__ void join_parts(int32_t first, int32_t stride, int32_t count,
                                                int32_t w0, bool w0_whole_start, bool to_outputs) {
-        constexpr int U = 16;
-        const int64_t to = part(first, w0, w0_whole_start);
-        for (int x = tid * 4; x < ROWS * D; x += T * 4) {
-            const int r = x / D;
-            if (row_at(r / (16 * MT), r % (16 * MT)) >= p.rows) continue;
-            float top = NEG_INF, sum = 0;
-            f32x4 acc = {0, 0, 0, 0};
-#pragma unroll 1
-            for (int32_t i = 0; i < count; i += U) {
-                f32x4 o4[U];
-                float mm[U], ll[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int32_t w = first + (i + u < count ? i + u : count - 1) * stride;
-                    const int64_t at = part(w, w0, w0_whole_start);
-                    const u32x2 ml = gload((const u32x2*)(p.part_ml + at * (ROWS * 2) + r * 2));
-                    o4[u] = gload((const f32x4*)(p.part_o + at * (ROWS * D) + x));
-                    const uint32_t m0 = ml[0], l0 = ml[1];
-                    mm[u] = __builtin_bit_cast(float, m0);
-                    ll[u] = __builtin_bit_cast(float, l0);
-                }
-                float up = top;
-#pragma unroll
-                for (int u = 0; u < U; ++u) up = fmaxf(up, mm[u]);  // (the last one again past count)
-                const float f0 = scale_to(top, up);
-                sum *= f0;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[e] *= f0;
-                top = up;
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (i + u < count) {
-                        const float f = scale_to(mm[u], top);
-                        sum += f * ll[u];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[e] += f * o4[u][e];
-                    }
-            }
-            if (to_outputs) {
-                write_row(r / (16 * MT), r % (16 * MT), x % D, acc, top, sum);
-            } else {
-                gstore((f32x4*)(p.part_o + to * (ROWS * D) + x), acc);
-                if (x % D == 0) {
-                    sm.ml[0][r][0] = top;
-                    sm.ml[0][r][1] = sum;
-                }
-            }
-        }
+        constexpr int FOURS = (ROWS * D + T * 4 - 1) / (T * 4);  // of elements, a thread
+        if (FOURS > 2 && count <= 4)
+            join_some<4, 4>(first, stride, count, w0, w0_whole_start, to_outputs);
+        else
+            join_some<1, 16>(first, stride, count, w0, w0_whole_start, to_outputs);
         if (to_outputs) return;
+        const int64_t to = part(first, w0, w0_whole_start);
         __syncthreads();  // everyone has read the slot's maxima and sums
         if (tid < ROWS && row_at(tid / (16 * MT), tid % (16 * MT)) < p.rows) {
             gstore(p.part_ml + to * (ROWS * 2) + tid * 2, sm.ml[0][tid][0]);
             gstore(p.part_ml + to * (ROWS * 2) + tid * 2 + 1, sm.ml[0][tid][1]);
         }
     }
+
+    // Other workgroups' parts come from beyond this XCD, so the loads of a
+    // thread's X fours of U parts are issued together, the rows that hold nothing
+    // are stepped over and the maximum is a running one: with the maxima in a
+    // pass of their own and eight parts at a time, one list of 4096 in 32 parts
+    // took 20 us for 18, one after the other 48; and with the empty rows read and
+    // one four at a time, 64 lists of up to 16384 under drafts of four 473 us for
+    // 456, 64 lists of 1024 under one token 63 for 61.
+    template <int X, int U>
+    __device__ __forceinline__ void join_some(int32_t first, int32_t stride, int32_t count,
+                                              int32_t w0, bool w0_whole_start, bool to_outputs) {
+        const int64_t to = part(first, w0, w0_whole_start);
+        // rows that hold something: of each head, or the first ones
+        const int valid = HEAD || p.rows - row_at(0, 0) < ROWS ? p.rows - row_at(0, 0) : ROWS;
+        const int all = (HEAD ? S::SUBS * valid : valid) * D;
+        for (int y = tid * 4; y < all; y += T * 4 * X) {
+            int r[X], d[X];
+            float top[X], sum[X];
+            f32x4 acc[X];
+#pragma unroll
+            for (int j = 0; j < X; ++j) {
+                const int at = y + j * T * 4 < all ? y + j * T * 4 : y;
+                const int q = at / D, s = HEAD ? q / valid : 0;
+                r[j] = HEAD ? s * 16 * MT + q - s * valid : q;
+                d[j] = at % D;
+                top[j] = NEG_INF;
+                sum[j] = 0;
+                acc[j] = f32x4{0, 0, 0, 0};
+            }
+#pragma unroll 1
+            for (int32_t i = 0; i < count; i += U) {
+                f32x4 o4[X][U];
+                float mm[X][U], ll[X][U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int32_t w = first + (i + u < count ? i + u : count - 1) * stride;
+                    const int64_t at = part(w, w0, w0_whole_start);
+#pragma unroll
+                    for (int j = 0; j < X; ++j) {
+                        const u32x2 ml =
+                            gload((const u32x2*)(p.part_ml + at * (ROWS * 2) + r[j] * 2));
+                        o4[j][u] = gload((const f32x4*)(p.part_o + at * (ROWS * D) + r[j] * D + d[j]));
+                        const uint32_t m0 = ml[0], l0 = ml[1];
+                        mm[j][u] = __builtin_bit_cast(float, m0);
+                        ll[j][u] = __builtin_bit_cast(float, l0);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < X; ++j) {
+                    float up = top[j];
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        up = fmaxf(up, mm[j][u]);  // (the last one again past count)
+                    const float f0 = scale_to(top[j], up);
+                    sum[j] *= f0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[j][e] *= f0;
+                    top[j] = up;
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (i + u < count) {
+                            const float f = scale_to(mm[j][u], top[j]);
+                            sum[j] += f * ll[j][u];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[j][e] += f * o4[j][u][e];
+                        }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < X; ++j) {
+                if (y + j * T * 4 >= all) continue;
+                if (to_outputs) {
+                    write_row(r[j] / (16 * MT), r[j] % (16 * MT), d[j], acc[j], top[j], sum[j]);
+                } else {
+                    gstore((f32x4*)(p.part_o + to * (ROWS * D) + r[j] * D + d[j]), acc[j]);
+                    if (d[j] == 0) {
+                        sm.ml[0][r[j]][0] = top[j];
+                        sm.ml[0][r[j]][1] = sum[j];
+                    }
+                }
+            }
+        }
+    }
+
     // A worker's slot: its first segment's, or the one of a list that begins
     // inside its share.
     __device__ __forceinline__ int64_t part(int32_t w, int32_t w0, bool w0_whole_start) const {
