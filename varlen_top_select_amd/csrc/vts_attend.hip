@@ -646,6 +646,35 @@ struct Attend {
         }
     }
 
+    // Whether parts are stored through to memory.  A release fence writes all of
+    // the XCD's L2 back, about 4 us in which the joiner waits: one list of 4096
+    // takes 14.8 us without it for 18, 16 of 1024 25 for 32.  Parts of many rows
+    // lie in pieces of 16 bytes, which L2 gathers better: through memory 64 lists
+    // of up to 16384 with 16 rows of four heads take 486 us for 456, 8 lists
+    // with 128 rows 408 for 385.
+    __device__ __forceinline__ bool through() const {
+        return MODE == KEYS || (HEAD && MT == 1 && p.rows <= 8);
+    }
+    template <typename V>
+    __device__ __forceinline__ void pstore(V* a, V v) const {
+        if (!through()) {
+            gstore(a, v);
+            return;
+        }
+        uint32_t w[sizeof(V) / 4];
+        __builtin_memcpy(w, &v, sizeof(V));
+        if constexpr (sizeof(V) == 4) {
+            __hip_atomic_store((VTS_GLOBAL uint32_t*)a, w[0], __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+        } else {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(V) / 8; ++i)
+                __hip_atomic_store((VTS_GLOBAL uint64_t*)a + i,
+                                   w[2 * i] | (uint64_t)w[2 * i + 1] << 32, __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+        }
+    }
+
     // A share of the places: leaves the block's rows in slot `mine`; the
     // last of the workers [w0, w1] to arrive joins all, in their order.
     __device__ __forceinline__ void finish_part(int64_t mine, int32_t w0, int32_t w1,
@@ -660,18 +689,18 @@ struct Attend {
                     if (row_at(sub(), r) >= p.rows) continue;
 #pragma unroll
                     for (int i = 0; i < NTILE; ++i)
-                        gstore((f32x4*)(po + at * D + four_at(i)), four(mt, i));
+                        pstore((f32x4*)(po + at * D + four_at(i)), four(mt, i));
                     if (grp == 0) {
-                        gstore(pm + at * 2, m[mt]);
-                        gstore(pm + at * 2 + 1, l[mt]);
+                        pstore(pm + at * 2, m[mt]);
+                        pstore(pm + at * 2 + 1, l[mt]);
                     }
                 }
         } else {
             join_waves();
             for (int x = tid * 4; x < ROWS * D; x += T * 4)
                 if (row_at(0, x / D) < p.rows)
-                    gstore((f32x4*)(po + x), *(const f32x4*)&sm.o[0][x / D][x % D]);
-            if (tid < ROWS * 2) gstore(pm + tid, (&sm.ml[0][0][0])[tid]);
+                    pstore((f32x4*)(po + x), *(const f32x4*)&sm.o[0][x / D][x % D]);
+            if (tid < ROWS * 2) pstore(pm + tid, (&sm.ml[0][0][0])[tid]);
         }
         // The parts are joined in blocks of JOIN workers, each by the block's last
         // to arrive, and the blocks by the last of those: with one joiner for
@@ -688,14 +717,17 @@ struct Attend {
         __syncthreads();
     }
 
-    // Whether this workgroup is the last of `n` to come here; what the others
-    // stored before is then visible.
+    // Whether this workgroup is the last of `n` to come here; the parts that the
+    // others stored before are then visible.
     __device__ __forceinline__ bool last_of(uint32_t* ticket, int32_t n) {
-        // every wave's stores are complete before the barrier; thread 0's
-        // release fence then covers the workgroup's
+        // every wave's stores are complete before the barrier: at the device's
+        // scope where through(), else thread 0's release fence writes them back
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0);
+        asm volatile("" ::: "memory");
         __syncthreads();
         if (tid == 0) {
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+            if (!through()) __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
             const uint32_t old = __hip_atomic_fetch_add((VTS_GLOBAL uint32_t*)ticket, 1u,
                                                         __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             const bool last = old + 1 == (uint32_t)n;
@@ -722,8 +754,8 @@ struct Attend {
         const int64_t to = part(first, w0, w0_whole_start);
         __syncthreads();  // everyone has read the slot's maxima and sums
         if (tid < ROWS && row_at(tid / (16 * MT), tid % (16 * MT)) < p.rows) {
-            gstore(p.part_ml + to * (ROWS * 2) + tid * 2, sm.ml[0][tid][0]);
-            gstore(p.part_ml + to * (ROWS * 2) + tid * 2 + 1, sm.ml[0][tid][1]);
+            pstore(p.part_ml + to * (ROWS * 2) + tid * 2, sm.ml[0][tid][0]);
+            pstore(p.part_ml + to * (ROWS * 2) + tid * 2 + 1, sm.ml[0][tid][1]);
         }
     }
 
@@ -732,7 +764,7 @@ struct Attend {
     // are stepped over and the maximum is a running one: with the maxima in a
     // pass of their own and eight parts at a time, one list of 4096 in 32 parts
     // took 20 us for 18, one after the other 48; and with the empty rows read and
-    // one four at a time, 64 lists of up to 16384 under drafts of four 473 us for
+    // one four at a time, 64 lists of up to 16384 under drafts of two 473 us for
     // 456, 64 lists of 1024 under one token 63 for 61.
     template <int X, int U>
     __device__ __forceinline__ void join_some(int32_t first, int32_t stride, int32_t count,
@@ -800,7 +832,7 @@ struct Attend {
                 if (to_outputs) {
                     write_row(r[j] / (16 * MT), r[j] % (16 * MT), d[j], acc[j], top[j], sum[j]);
                 } else {
-                    gstore((f32x4*)(p.part_o + to * (ROWS * D) + r[j] * D + d[j]), acc[j]);
+                    pstore((f32x4*)(p.part_o + to * (ROWS * D) + r[j] * D + d[j]), acc[j]);
                     if (d[j] == 0) {
                         sm.ml[0][r[j]][0] = top[j];
                         sm.ml[0][r[j]][1] = sum[j];

@@ -328,8 +328,11 @@ struct Verify {
             double* sums = p.sums + (int64_t)b * segments;
             const double mine = sum_segment(k, segments, slice * VW + wave);
             if (lane_id() == 0) gstore(sums + slice * VW + wave, mine);
-            // every wave's store is complete before the barrier; thread 0's
-            // release fence then covers the workgroup's
+            // every wave's store is complete before the barrier, which does not
+            // wait for it; thread 0's release fence then covers the workgroup's
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(0);
+            asm volatile("" ::: "memory");
             __syncthreads();
             if (threadIdx.x == 0) {
                 __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
