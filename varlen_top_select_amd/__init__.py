@@ -142,6 +142,9 @@ def make_workspace(num_rows: int, width: int, top_k: int, dtype: torch.dtype, de
 # one zeroed workspace per (device, stream) and kind of call, grown on demand
 # (the caller may pass its own)
 _WS_CACHE: dict = {}
+# those that a larger one has replaced: a graph captured with one keeps its
+# address and writes there at every replay, so none is ever given back
+_WS_REPLACED: list = []
 
 
 def _default_workspace(need: int, device, stream_ptr: int, kind: str = "select") -> torch.Tensor:
@@ -154,6 +157,9 @@ def _default_workspace(need: int, device, stream_ptr: int, kind: str = "select")
                 "no workspace for this shape on the capturing stream: pass workspace= "
                 "(make_workspace) or make one eager call of this shape on this stream "
                 "before capture")
+        if ws is not None:
+            _WS_REPLACED.append(ws)
+            need = max(need, 2 * ws.numel())  # so all that are kept hold less than the last
         ws = torch.empty(need, dtype=torch.uint8, device=device)
         _check("vts_workspace_init", library().vts_workspace_init(ws.data_ptr(), need, stream_ptr))
         _WS_CACHE[key] = ws

@@ -13,8 +13,11 @@ passed as a permuted view), bfloat16 or float16.  Lengths count the drafted
 tokens, as ``next_n`` does in ``topk_varlen``.
 
 Without ``workspace`` the calls share one per device and stream, made at the first
-eager call; one of one's own is ``torch.zeros`` of the bytes that
-``tree_attention_workspace_bytes`` or ``verify_draft_workspace_bytes`` says.
+eager call and held until the process ends, also where a larger shape has
+replaced it: graphs captured with it stay valid.  Graphs captured on one stream
+share that stream's workspace, so replay them one after another, or give each
+its own: ``torch.zeros`` of the bytes that ``tree_attention_workspace_bytes`` or
+``verify_draft_workspace_bytes`` says.
 """
 from __future__ import annotations
 
