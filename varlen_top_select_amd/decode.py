@@ -326,12 +326,14 @@ def verify_draft(target_probs: torch.Tensor, draft_tokens: torch.Tensor, uniform
 
 def tree_mask_from_parents(parents: torch.Tensor) -> torch.Tensor:
     """tree_mask[batch, draft] of trees given by parents[batch, draft] (-1: hangs
-    from the context): each node sees its ancestors and itself."""
+    from the context): each node sees its ancestors and itself.  A node whose
+    parent does not exist, outside [-1, draft), sees itself alone."""
     if parents.dim() != 2 or parents.shape[1] > MAX_DRAFT:
         raise ValueError(f"parents must be a 2-D tensor of at most {MAX_DRAFT} columns")
     draft = parents.shape[1]
     bits = (1 << torch.arange(draft, dtype=torch.int64, device=parents.device)).expand_as(parents)
     jump = parents.long()
+    jump = torch.where(jump < draft, jump, -1)  # (an index past the row would end the process on a GPU)
     for _ in range(max(1, draft - 1).bit_length()):  # bits cover twice as many generations each time
         up = jump.clamp(min=0)
         bits = torch.where(jump >= 0, bits | bits.gather(1, up), bits)
