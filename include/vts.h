@@ -441,7 +441,8 @@ int vts_tree_attention(const vts_paged_cache* cache, const void* q, const int64_
  * row_keep   device uint8[batch, draft] or NULL (all rows): for instance the
  *            drafted tokens that were accepted.
  * weights    device float, `width` consecutive per request and KV head, at
- *            the strides given (elements).
+ *            the strides given (elements); no two of these rows may have an
+ *            element in common.
  */
 int vts_attention_weight_add(const vts_paged_cache* cache, const void* q,
                              const int64_t* q_strides, int32_t draft, int32_t heads,

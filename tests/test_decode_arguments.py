@@ -1,8 +1,11 @@
 """Arguments of the decode-step operators at their edges, without a GPU."""
+import os
+
 import pytest
 import torch
 
 import varlen_top_select_amd as vts
+from varlen_top_select_amd import decode
 
 
 @pytest.mark.parametrize("bad", [4, 5, 64, 2 ** 31 - 1, -2, -2 ** 31])
@@ -17,3 +20,47 @@ def test_tree_mask_of_parents_that_are_no_node(bad, dtype):
 def test_tree_mask_of_no_tokens():
     assert vts.tree_mask_from_parents(torch.empty(3, 0, dtype=torch.int32)).shape == (3, 0)
     assert vts.tree_mask_from_parents(torch.empty(0, 5, dtype=torch.int32)).shape == (0, 5)
+
+
+# ---- the C entry points, with pointers that are never dereferenced
+
+OK, INVALID = 0, -1
+A = 1 << 20  # fake, aligned "device" address
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(vts.LIB_PATH):
+        from varlen_top_select_amd import build
+        build.build()
+    return vts.library()
+
+
+def cache(batch=3, kv=4, dim=64, page=16):
+    return decode._CACHE.pack(A, A, page * kv * dim, kv * dim, dim, page * kv * dim, kv * dim, dim, A,
+                              100, 100, A, 50, page, kv, dim, batch, 1)
+
+
+STRIDES = decode._STRIDES.pack(2 * 16 * 64, 16 * 64, 64)
+
+
+@pytest.mark.parametrize("batch,kv,wb,wh,width,apart", [
+    (3, 4, 400, 100, 100, True), (3, 4, 100, 300, 100, True),   # either order, nothing between
+    (3, 4, 100, 100, 100, False),                               # row (0, 1) is row (1, 0)
+    (3, 4, 300, 100, 100, False), (3, 4, 100, 250, 100, False),  # the last of one, the first of the next
+    (3, 4, 399, 100, 100, False), (3, 4, 400, 99, 100, False), (3, 4, 99, 500, 100, False),
+    (3, 4, 0, 100, 100, False), (3, 4, 400, 0, 100, False),
+    (1, 4, 0, 100, 100, True), (3, 1, 100, 0, 100, True), (1, 1, 0, 0, 100, True),
+    (2, 3, 300, 200, 100, True),    # 0 200 400 300 500 700: one within the other, apart
+    (2, 3, 299, 200, 100, False), (3, 4, 150, 400, 100, True), (3, 4, 150, 399, 100, False),
+    (3, 4, 1 << 62, 1 << 60, 100, True), (3, 4, (1 << 62) + 1, 1 << 61, 100, False),
+])
+def test_weights_rows_that_coincide(lib, batch, kv, wb, wh, width, apart):
+    """Two rows that share an element would lose each other's additions."""
+    rows = [b * wb + h * wh for b in range(batch) for h in range(kv)]
+    assert apart == all(abs(x - y) >= width for i, x in enumerate(rows) for y in rows[:i])
+    if apart and torch.cuda.is_available():
+        pytest.skip("the call would run, on addresses that are none")
+    got = lib.vts_attention_weight_add(cache(batch, kv), A, STRIDES, 2, 4 * kv, None, A, None, 0.1, A, wb,
+                                       wh, width, None)
+    assert (got != INVALID) == apart

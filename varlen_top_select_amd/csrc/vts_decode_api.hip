@@ -105,6 +105,29 @@ int check_q(const void* q, const int64_t* strides) {
     return VTS_OK;
 }
 
+// Whether rows of `width` elements at i * s + j * t, i < m and j < n, have no
+// element in common.
+bool rows_apart(int64_t m, int64_t s, int64_t n, int64_t t, int64_t width) {
+    if (n <= 1 || (m > 1 && s < t)) {  // the larger stride first
+        const int64_t m0 = m, s0 = s;
+        m = n, s = t, n = m0, t = s0;
+    }
+    // m <= 1 here means that at most one stride counts
+    if (n > 1 && t < width) return false;
+    if (m <= 1) return true;
+    if (s < width) return false;
+    if (n <= 1) return true;
+    // i rows on, the nearest of the others on either side; s >= t, so the loop
+    // leaves their reach within n steps
+    const __int128 last = (__int128)t * (n - 1);
+    for (int64_t i = 1; i < m && (__int128)i * s < last + width; ++i) {
+        const __int128 at = (__int128)i * s, below = at / t * t;
+        if (at - (below < last ? below : last) < width) return false;
+        if (below < last && below + t - at < width) return false;
+    }
+    return true;
+}
+
 struct AttendPlan {
     int32_t rows, block_rows, row_blocks, workers, heads_on_waves;
     size_t part_o, part_ml, total;
@@ -246,6 +269,8 @@ int vts_attention_weight_add(const vts_paged_cache* cache, const void* q,
     if (isnan(scale) || width < 0 || weights_batch_stride < 0 || weights_head_stride < 0)
         return VTS_ERR_INVALID;
     if (p.c.batch == 0 || width == 0) return VTS_OK;
+    if (!rows_apart(p.c.batch, weights_batch_stride, p.c.kv_heads, weights_head_stride, width))
+        return VTS_ERR_INVALID;
     st = check_q(q, q_strides);
     if (st != VTS_OK) return st;
     if (lse == nullptr || weights == nullptr || !aligned(lse, 4) || !aligned(weights, 4))
