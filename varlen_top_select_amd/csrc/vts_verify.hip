@@ -6,7 +6,12 @@
 // i counting the rejected siblings.  In closed form
 //   r_i = max(p - a_i q, 0) / S_i,  a_0 = 0, S_0 = 1,
 //   a_{i+1} = a_i + S_i,            S_i = sum_v max(p - a_i q, 0),
-// so a rejection costs one sum over the vocabulary and no vector is stored.
+// so a rejection costs one sum over the vocabulary and no vector is stored.  A
+// chosen token (q is 1 at it) takes its own p away and leaves the others': r is p
+// without the rejected tokens over what they leave.  That is the row's sum
+// without any of the node's children, plus the p of those not yet rejected: one
+// sum a node, of positive terms only (1 - p of the rejected would be off by the
+// row's whole rounding, which in 16 bits passes what a few tokens leave).
 // Where no child is accepted, the next token is drawn from the residual: the
 // first v whose running sum passes u S.  Sums are held in 64 bits: the token is
 // a whole number that must not depend on how the sum is split.
@@ -15,12 +20,13 @@
 // as far as it goes without a sum, which is a few dozen scalars and gives all
 // the same state, and every wave sums one segment of the vocabulary; the last
 // workgroup to arrive joins the sums in order, finishes the walk, and scans the
-// one segment that the token lies in.  A chain needs no other sum.  In a tree of
-// drawn tokens a rejection's sum decides over the next sibling, so there the
-// walk goes in ROUNDS launches that each end with a sum by all workgroups, and
-// a last one of one workgroup per request that takes what sums are left alone, a
-// sixteenth of the row to a wave (10 us for 100003 bf16; with all but the first
-// sum taken so, 16 trees of 24 took 80 us).
+// one segment that the token lies in.  A chain needs no other sum, and a tree of
+// chosen tokens one for each node where a child was rejected, the later ones by
+// the last workgroup alone.  In a tree of drawn tokens a rejection's sum decides
+// over the next sibling, so there the walk goes in ROUNDS launches that each end
+// with a sum by all workgroups, and a last one of one workgroup per request that
+// takes what sums are left alone, a sixteenth of the row to a wave (10 us for
+// 100003 bf16; with all but the first sum taken so, 16 trees of 24 took 80 us).
 #include "vts_paged.hpp"
 
 namespace vts {
@@ -59,7 +65,9 @@ struct Walk {
     int32_t next;     // the next node to look at
     int32_t steps;    // accepted so far
     double a, mass;   // of the residual
-    uint64_t gone;    // rejected children (chosen drafts: their tokens leave p)
+    // chosen drafts: once a child was rejected, all children, whose tokens are not
+    // in `mass`
+    uint64_t gone;
 };
 
 template <int DT>
@@ -102,8 +110,9 @@ struct Verify {
         __syncthreads();
     }
 
-    // Goes on until a sum is needed (true: a sibling was rejected and the
-    // residual has to be summed before the walk goes on) or the walk ends.
+    // Goes on until a sum is needed (true: a sibling was rejected, of chosen ones
+    // the first, and the residual has to be summed before the walk goes on) or the
+    // walk ends.
     __device__ __forceinline__ bool advance(Walk& k) const {
         for (int32_t t = k.next; t < p.draft; ++t) {
             if (sm.parent[t] != k.cur) continue;
@@ -113,7 +122,8 @@ struct Verify {
                 const double r = fmax(pt - k.a * (double)sm.q[t], 0.0);
                 yes = r > 0 && (double)sm.u[t] * (double)sm.q[t] * k.mass < r;
             } else {
-                yes = pt > 0 && !is_gone(k.gone, sm.token[t]) && (double)sm.u[t] * k.mass < pt;
+                yes = pt > 0 && !is_token_of(before(k.gone, t), sm.token[t]) &&
+                      (double)sm.u[t] * left(k, t) < pt;
             }
             if (yes) {
                 if (threadIdx.x == 0) sm.path[k.steps] = t;
@@ -130,19 +140,35 @@ struct Verify {
                 k.next = t + 1;
                 return true;
             }
-            if (!is_gone(k.gone, sm.token[t])) k.mass -= pt;
-            k.gone |= 1ull << t;
+            if (k.gone) continue;
+            for (int32_t c = t; c < p.draft; ++c)
+                if (sm.parent[c] == k.cur) k.gone |= 1ull << c;
+            k.next = t + 1;
+            return true;
         }
         k.next = p.draft;
         return false;
     }
-    __device__ __forceinline__ bool is_gone(uint64_t gone, int32_t x) const {
-        while (gone) {
-            const int i = __builtin_ctzll(gone);
-            gone &= gone - 1;
-            if (sm.token[i] == x) return true;
-        }
+    static __device__ __forceinline__ uint64_t before(uint64_t nodes, int32_t t) {
+        return nodes & ((1ull << t) - 1);
+    }
+    __device__ __forceinline__ bool is_token_of(uint64_t nodes, int32_t x) const {
+        for (; nodes; nodes &= nodes - 1)
+            if (sm.token[__builtin_ctzll(nodes)] == x) return true;
         return false;
+    }
+    // Chosen drafts: the mass that the children before t leave.  Before the first
+    // rejection that is the row as it is given; then `mass` and the later
+    // children's tokens, each once.
+    __device__ __forceinline__ double left(const Walk& k, int32_t t) const {
+        double m = k.mass;
+        uint64_t seen = before(k.gone, t);
+        for (uint64_t g = k.gone & ~seen; g; g &= g - 1) {
+            const int i = __builtin_ctzll(g);
+            if (!is_token_of(seen, sm.token[i])) m += (double)sm.p[i];
+            seen |= 1ull << i;
+        }
+        return m;
     }
 
     // A vector of values from element v of a row on, past the vocabulary 0.
@@ -505,7 +531,7 @@ __global__ __launch_bounds__(VT) void verify_last_kernel(VerifyParams p, int32_t
 template <int DT>
 static hipError_t launch_dt(const VerifyParams& p, hipStream_t stream) {
     const dim3 grid((uint32_t)p.batch * (uint32_t)p.slices), block(VT);
-    // only a drawn token's rejected sibling makes the walk wait for a sum
+    // a drawn token's rejected siblings make the walk wait for a sum each
     if (!p.draft_probs || !p.parents || p.draft == 1 || p.slices == 1) {
         hipLaunchKernelGGL((verify_kernel<DT>), grid, block, 0, stream, p);
         return hipGetLastError();
