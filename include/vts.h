@@ -498,7 +498,9 @@ int vts_evict_cache(const vts_paged_cache* cache, const float* weights,
  * At most 64 drafted tokens, 2^21 requests and 2^31 - 2^16 - 1 tokens of vocabulary.
  * Probabilities are used as they are given; NaN and negative values count as
  * 0.  A token outside [0, vocab) or a parent outside [-1, t) makes a node that
- * is never accepted.  Sums and comparisons are in 64 bits.
+ * is not there: it is neither accepted nor rejected, and takes nothing from r (a
+ * request with fewer drafts is padded with tokens of -1).  Sums and comparisons
+ * are in 64 bits.
  *
  * path       device int32[batch, draft]: the accepted nodes in order, then -1.
  * count      device int32[batch]: how many.

@@ -1,6 +1,6 @@
 """verify_draft against the rule as include/vts.h states it, residuals formed one
-after the other and normalised by their own sums in 64 bits: chosen siblings
-over rows whose sum is not 1."""
+after the other and normalised by their own sums in 64 bits: nodes without a
+draft, chosen siblings over rows whose sum is not 1."""
 import numpy as np
 import pytest
 import torch
@@ -62,6 +62,83 @@ def check(target, tokens, u, drafts=None, parents=None):
 
 def softmax(gen, *shape, scale=1.0, dtype=torch.float32):
     return torch.softmax(scale * torch.randn(*shape, generator=gen), -1).to(dtype)
+
+
+# ---- nodes without a draft
+
+
+@pytest.mark.parametrize("none", [-1, 2, 2 ** 31 - 1])
+def test_no_draft_takes_nothing_from_the_target(none):
+    """Nothing was drawn from q, so the next token is drawn from p itself."""
+    u = torch.tensor([[0.5, x] for x in (0.0, 0.2, 0.49, 0.51, 0.9)])
+    n = len(u)
+    target = torch.tensor([0.5, 0.5]).expand(n, 2, 2).contiguous()
+    drafts = torch.tensor([0.9, 0.1]).expand(n, 1, 2).contiguous()
+    tokens = torch.full((n, 1), none, dtype=torch.int32)
+    for parents in (None, torch.full((n, 1), -1, dtype=torch.int32)):
+        paths, nexts = check(target, tokens, u, drafts, parents)
+        assert nexts == [0, 0, 0, 1, 1] and paths == [[-1]] * n
+
+
+@pytest.mark.parametrize("vocab", [50, 9001, 40000])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_requests_with_fewer_drafts(vocab, dtype):
+    """Chains cut short, and trees with holes among the siblings."""
+    gen = torch.Generator().manual_seed(60 + vocab)
+    batch, draft = 12, 6
+    target = softmax(gen, batch, draft + 1, vocab, dtype=dtype)
+    drafts = softmax(gen, batch, draft, vocab, dtype=dtype)
+    for parents in (None, torch.tensor([-1, -1, -1, 0, 1, 1], dtype=torch.int32).repeat(batch, 1)):
+        rows = torch.arange(draft).expand(batch, -1) if parents is None else parents.long() + 1
+        dist = drafts.float().gather(1, rows[..., None].expand(-1, -1, vocab)).reshape(-1, vocab)
+        tokens = torch.multinomial(dist, 1, generator=gen).view(batch, draft).int()
+        for b in range(batch):
+            if parents is None:
+                tokens[b, b % (draft + 1):] = -1
+            else:
+                tokens[b, [0, 1, 2, 4][b % 4]] = -1
+                tokens[b, b % draft] = vocab
+        for _ in range(4):
+            u = torch.rand(batch, draft + 1, generator=gen)
+            check(target, tokens, u, drafts, parents)
+            check(target, tokens, u, None, parents)
+
+
+def test_nodes_that_are_not_there():
+    """Tokens outside the vocabulary and parents that are no earlier node."""
+    gen = torch.Generator().manual_seed(52)
+    target = torch.softmax(torch.randn(2, 7, 50, generator=gen), -1)
+    drafts = torch.softmax(torch.randn(2, 6, 50, generator=gen), -1)
+    tokens = torch.tensor([[-1, 50, 3, 2 ** 31 - 1, 4, 5], [1, 2, 3, 4, 5, 6]], dtype=torch.int32)
+    parents = torch.tensor([[-1, -1, -1, 2, 2, 4], [-2, 5, 2 ** 31 - 1, -2 ** 31, -1, 4]],
+                           dtype=torch.int32)
+    for u in (0.0, 0.1, 0.3, 0.7, 0.99):
+        x = torch.full((2, 7), u)
+        check(target, tokens, x, drafts, parents)
+        check(target, tokens, x, None, parents)
+
+
+@pytest.mark.parametrize("drawn", [True, False])
+def test_distribution_with_holes(drawn):
+    """The outcome's first token is distributed as the target, holes or not."""
+    gen = torch.Generator().manual_seed(61)
+    batch, vocab = 40000, 4
+    p = torch.tensor([0.4, 0.3, 0.2, 0.1])
+    q = torch.tensor([0.1, 0.2, 0.3, 0.4])
+    parents = torch.full((batch, 4), -1, dtype=torch.int32)
+    tokens = torch.multinomial(q.expand(batch * 4, vocab), 1, generator=gen).view(batch, 4).int()
+    tokens[:, 0] = -1
+    tokens[::2, 2] = vocab
+    u = torch.rand(batch, 5, generator=gen)
+    path, count, token = vts.verify_draft(p.expand(batch, 5, vocab).contiguous().to(DEV), tokens.to(DEV),
+                                          u.to(DEV), parents=parents.to(DEV),
+                                          draft_probs=q.expand(batch, 4, vocab).contiguous().to(DEV)
+                                          if drawn else None)
+    at = path.cpu()[:, :1].clamp(min=0).long()
+    first = torch.where(count.cpu() > 0, tokens.gather(1, at)[:, 0], token.cpu())
+    share = torch.bincount(first.long(), minlength=vocab).double() / batch
+    # five standard deviations of a share
+    assert ((share - p.double()).abs() <= 5 * (p.double() * (1 - p.double()) / batch).sqrt()).all()
 
 
 # ---- chosen siblings

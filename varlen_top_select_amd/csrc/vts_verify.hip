@@ -115,7 +115,8 @@ struct Verify {
     // walk ends.
     __device__ __forceinline__ bool advance(Walk& k) const {
         for (int32_t t = k.next; t < p.draft; ++t) {
-            if (sm.parent[t] != k.cur) continue;
+            // (where there is no token none was drawn, so nothing leaves the residual)
+            if (sm.parent[t] != k.cur || sm.token[t] < 0) continue;
             const double pt = sm.p[t];
             bool yes;
             if (drafts) {
@@ -142,7 +143,7 @@ struct Verify {
             }
             if (k.gone) continue;
             for (int32_t c = t; c < p.draft; ++c)
-                if (sm.parent[c] == k.cur) k.gone |= 1ull << c;
+                if (sm.parent[c] == k.cur && sm.token[c] >= 0) k.gone |= 1ull << c;
             k.next = t + 1;
             return true;
         }
