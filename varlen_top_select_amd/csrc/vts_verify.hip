@@ -21,8 +21,8 @@
 // the same state, and every wave sums one segment of the vocabulary; the last
 // workgroup to arrive joins the sums in order, finishes the walk, and scans the
 // one segment that the token lies in.  A chain needs no other sum, and a tree of
-// chosen tokens one for each node where a child was rejected, the later ones by
-// the last workgroup alone.  In a tree of drawn tokens a rejection's sum decides
+// chosen tokens one for each node where a child was rejected and another follows,
+// the later ones by the last workgroup alone (16 trees of 24: 42 us).  In a tree of drawn tokens a rejection's sum decides
 // over the next sibling, so there the walk goes in ROUNDS launches that each end
 // with a sum by all workgroups, and a last one of one workgroup per request that
 // takes what sums are left alone, a sixteenth of the row to a wave (10 us for
@@ -70,7 +70,10 @@ struct Walk {
     uint64_t gone;
 };
 
-template <int DT>
+// DRAWN: with draft probabilities.  The two walks have kernels of their own: code
+// that runs once waits for its own instructions (in one kernel a single chosen
+// token takes 17.0 us for 14.9, a drawn tree of 24 57.7 for 48.6).
+template <int DT, bool DRAWN>
 struct Verify {
     static constexpr int VE = DT == F32 ? 4 : 8;  // elements of a 16-byte vector
     const VerifyParams& p;
@@ -83,7 +86,7 @@ struct Verify {
         : p(p_), sm(s_), b(b_) {
         constexpr int64_t E = DT == F32 ? 4 : 2;
         target = (const char*)p.target + b * p.target_batch * E;
-        drafts = p.draft_probs ? (const char*)p.draft_probs + b * p.draft_batch * E : nullptr;
+        drafts = DRAWN ? (const char*)p.draft_probs + b * p.draft_batch * E : nullptr;
     }
     __device__ __forceinline__ const void* target_row(int32_t cur) const {
         return target + (cur + 1) * p.target_row * (DT == F32 ? 4 : 2);
@@ -104,7 +107,7 @@ struct Verify {
             sm.token[t] = ok ? x : -1;
             sm.parent[t] = parent;
             sm.p[t] = ok ? load_prob<DT>(target_row(parent), x) : 0.0f;
-            sm.q[t] = !drafts ? 1.0f : ok ? load_prob<DT>(draft_row(parent), x) : 0.0f;
+            sm.q[t] = !DRAWN ? 1.0f : ok ? load_prob<DT>(draft_row(parent), x) : 0.0f;
             sm.u[t] = gload(p.uniforms + (int64_t)b * (p.draft + 1) + t);
         }
         __syncthreads();
@@ -119,7 +122,7 @@ struct Verify {
             if (sm.parent[t] != k.cur || sm.token[t] < 0) continue;
             const double pt = sm.p[t];
             bool yes;
-            if (drafts) {
+            if constexpr (DRAWN) {
                 const double r = fmax(pt - k.a * (double)sm.q[t], 0.0);
                 yes = r > 0 && (double)sm.u[t] * (double)sm.q[t] * k.mass < r;
             } else {
@@ -135,17 +138,19 @@ struct Verify {
                 k.gone = 0;
                 continue;
             }
-            if (drafts) {
+            if constexpr (DRAWN) {
                 k.a += k.mass;
                 // the sum matters to a later sibling, or to the draw at the end
                 k.next = t + 1;
                 return true;
+            } else {
+                if (k.gone) continue;
+                for (int32_t c = t; c < p.draft; ++c)
+                    if (sm.parent[c] == k.cur && sm.token[c] >= 0) k.gone |= 1ull << c;
+                if (k.gone == 1ull << t) break;  // there is no later sibling
+                k.next = t + 1;
+                return true;
             }
-            if (k.gone) continue;
-            for (int32_t c = t; c < p.draft; ++c)
-                if (sm.parent[c] == k.cur && sm.token[c] >= 0) k.gone |= 1ull << c;
-            k.next = t + 1;
-            return true;
         }
         k.next = p.draft;
         return false;
@@ -199,19 +204,19 @@ struct Verify {
                                           int32_t v) const {
         Pair f;
         load(pr, v, f.x);
-        if (k.a > 0) load(qr, v, f.y);
+        if (DRAWN && k.a > 0) load(qr, v, f.y);
         return f;
     }
     __device__ __forceinline__ void residual(const Walk& k, const Pair& f, int32_t v,
                                              double (&r)[VE]) const {
-        if (k.a > 0) {
+        if (DRAWN && k.a > 0) {
 #pragma unroll
             for (int i = 0; i < VE; ++i)
                 r[i] = fmax((double)f.x[i] - k.a * (double)prob(f.y[i]), 0.0);  // NaN: 0
         } else {
 #pragma unroll
             for (int i = 0; i < VE; ++i) r[i] = prob(f.x[i]);
-            if (k.gone)
+            if constexpr (!DRAWN)
                 for (uint64_t g = k.gone; g; g &= g - 1) {
                     const int32_t x = sm.token[__builtin_ctzll(g)] - v;
 #pragma unroll
@@ -224,7 +229,7 @@ struct Verify {
     __device__ __forceinline__ double wave_sum(const Walk& k, int32_t v0, int32_t v1) const {
         constexpr int U = DT == F32 ? 4 : 2;  // vectors in flight per lane and row
         const void* pr = target_row(k.cur);
-        const void* qr = k.a > 0 ? draft_row(k.cur) : nullptr;
+        const void* qr = DRAWN && k.a > 0 ? draft_row(k.cur) : nullptr;
         double s = 0;
         for (int32_t v = v0 + (int32_t)lane_id() * VE; v < v1; v += 64 * VE * U) {
             Pair f[U];
@@ -290,7 +295,7 @@ struct Verify {
     __device__ __forceinline__ int32_t search(const Walk& k, int32_t v0, int32_t v1, double start,
                                               double bar) {
         const void* pr = target_row(k.cur);
-        const void* qr = k.a > 0 ? draft_row(k.cur) : nullptr;
+        const void* qr = DRAWN && k.a > 0 ? draft_row(k.cur) : nullptr;
         int32_t tail = -1;
         for (int32_t x0 = v0; x0 < v1; x0 += VT * VE) {
             const int32_t v = x0 + (int32_t)threadIdx.x * VE;
@@ -506,11 +511,11 @@ struct Verify {
     }
 };
 
-template <int DT>
+template <int DT, bool DRAWN>
 __global__ __launch_bounds__(VT) void verify_kernel(VerifyParams p) {
     __shared__ VerifyShared sm;
     const int32_t b = (int32_t)(blockIdx.x / p.slices), slice = (int32_t)(blockIdx.x % p.slices);
-    Verify<DT> v(p, sm, b);
+    Verify<DT, DRAWN> v(p, sm, b);
     v.run(slice);
 }
 
@@ -518,14 +523,14 @@ template <int DT>
 __global__ __launch_bounds__(VT) void verify_round_kernel(VerifyParams p, int32_t r) {
     __shared__ VerifyShared sm;
     const int32_t b = (int32_t)(blockIdx.x / p.slices), slice = (int32_t)(blockIdx.x % p.slices);
-    Verify<DT> v(p, sm, b);
+    Verify<DT, true> v(p, sm, b);
     v.round(slice, r);
 }
 
 template <int DT>
 __global__ __launch_bounds__(VT) void verify_last_kernel(VerifyParams p, int32_t rounds) {
     __shared__ VerifyShared sm;
-    Verify<DT> v(p, sm, (int32_t)blockIdx.x);
+    Verify<DT, true> v(p, sm, (int32_t)blockIdx.x);
     v.last_round(rounds);
 }
 
@@ -534,7 +539,10 @@ static hipError_t launch_dt(const VerifyParams& p, hipStream_t stream) {
     const dim3 grid((uint32_t)p.batch * (uint32_t)p.slices), block(VT);
     // a drawn token's rejected siblings make the walk wait for a sum each
     if (!p.draft_probs || !p.parents || p.draft == 1 || p.slices == 1) {
-        hipLaunchKernelGGL((verify_kernel<DT>), grid, block, 0, stream, p);
+        if (p.draft_probs)
+            hipLaunchKernelGGL((verify_kernel<DT, true>), grid, block, 0, stream, p);
+        else
+            hipLaunchKernelGGL((verify_kernel<DT, false>), grid, block, 0, stream, p);
         return hipGetLastError();
     }
     for (int32_t r = 0; r < ROUNDS; ++r)

@@ -278,8 +278,9 @@ def verify_draft(target_probs: torch.Tensor, draft_tokens: torch.Tensor, uniform
     """Verifies draft_tokens[batch, draft] (a chain, or a tree given by
     ``parents``) against target_probs[batch, draft + 1, vocab] with the random
     numbers uniforms[batch, draft + 1] in [0, 1) (vts_verify_draft in
-    include/vts.h).  Tokens of -1 pad a request that has fewer.  Returns the accepted nodes [batch, draft] (-1 past them),
-    their number [batch] and the next token [batch], all int32."""
+    include/vts.h).  Tokens of -1 pad a request that has fewer.  Returns the
+    accepted nodes [batch, draft] (-1 past them), their number [batch] and the
+    next token [batch], all int32."""
     if not isinstance(target_probs, torch.Tensor) or target_probs.dim() != 3:
         raise ValueError("target_probs must be a 3-D tensor [batch, draft + 1, vocab]")
     if target_probs.dtype not in _DTYPE:
