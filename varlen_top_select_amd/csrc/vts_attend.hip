@@ -9,12 +9,18 @@
 //
 // One pass: each wave walks its 32-place tiles with a running maximum m, sum l
 // and output O per query row (32-bit), and the waves, then the workgroups that
-// share a list, join theirs: O = sum_w 2^(m_w - m) O_w and the same for l.  The
-// maximum is only raised when a score passes it by more than 2^8, so that most
-// tiles need no exchange between lanes; p stays below 2^8 in either 16-bit
-// type and its relative rounding does not change.  p is rounded to the cache's
-// type for the second product (half a step, 2^-9 of bf16's p on average out
-// over the places); l sums the unrounded p.
+// share a list, join theirs: O = sum_w 2^(m_w - m) O_w and the same for l.  m is
+// only raised when a score passes it by a margin, so that most tiles need no
+// exchange between lanes.  p is rounded to the cache's type for the second product
+// (at most half a step, 2^-8 of a bf16 p and 2^-11 of an fp16 one, which average
+// out over the places); l sums the unrounded p.  In bf16 m is the maximum and the
+// margin 2^8: p has its full precision down to 2^-126.  fp16 loses it below 2^-14,
+// so there m lies 2^SHIFT below the maximum and the margin ends at 2^15, next to
+// fp16's largest value: p is rounded to 2^-11 of itself down to 2^-(14 + SHIFT) of
+// the row's greatest and to 2^-(25 + SHIFT) of that below, so that many light
+// places next to a heavy one keep their sum.  (SHIFT 11: 8 trees of 16 up to 65536
+// in fp16 take 375 us, for 361 with none and a margin of 2^8, 365 with 7 and 385
+// with 14; 64 chains up to 16384 453 with any.)
 #include "vts_paged.hpp"
 
 namespace vts {
@@ -76,6 +82,8 @@ struct Attend {
     // 128 lists of 2048 slots, 64 heads: 112 us without, 104 with.
     static constexpr bool ONCE = HEAD || (SLOTS && !WIDE);
     static constexpr int ROWS = S::ROWS;
+    // of m, see above: how far below the maximum it is put, and when it is raised
+    static constexpr float SHIFT = DT == F16 ? 11 : 0, RAISE = DT == F16 ? 15 : 8;
     using VRow = typename std::conditional<D == 128, u32x4, u32x2>::type;
 
     const AttendParams& p;
@@ -408,7 +416,7 @@ struct Attend {
 #pragma unroll
             for (int e = 0; e < 8; ++e) top[mt] = fmaxf(top[mt], s[mt][e >> 2][e & 3]);
             top[mt] *= c;
-            past = past || top[mt] > m[mt] + 8.0f;
+            past = past || top[mt] > m[mt] + RAISE;
         }
         if (ballot(past)) {
 #pragma unroll
@@ -416,7 +424,7 @@ struct Attend {
                 float up = fmaxf(top[mt], __shfl_xor(top[mt], 16));
                 up = fmaxf(up, __shfl_xor(up, 32));
                 // (a row that is not past its maximum keeps it)
-                up = up > m[mt] + 8.0f ? up : m[mt];
+                up = up > m[mt] + RAISE ? up - SHIFT : m[mt];
                 const float f = up == NEG_INF ? 1.0f : __builtin_amdgcn_exp2f(m[mt] - up);
                 m[mt] = up;
                 l[mt] *= f;
@@ -597,7 +605,9 @@ struct Attend {
         w[1] = pack2<DT>(x[2] * inv, x[3] * inv);
         gstore((u32x2*)((char*)p.out + 2 * (at * D + d)), w);
         if (d == 0 && p.lse)
-            gstore(p.lse + at, sum == 0.0f ? NEG_INF : (top + log2f(sum)) * 0.6931471805599453f);
+            gstore(p.lse + at, sum == 0.0f ? NEG_INF
+                                           : (top + SHIFT + log2f(sum * __builtin_exp2f(-SHIFT))) *
+                                                 0.6931471805599453f);
     }
     // this lane's outputs 4 * i .. of row mt * 16 + col, and where they begin
     __device__ __forceinline__ f32x4 four(int mt, int i) const {
