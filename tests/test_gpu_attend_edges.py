@@ -1,4 +1,4 @@
-"""tree_attention where weights differ by many orders of magnitude."""
+"""tree_attention where weights differ by many orders of magnitude, or are zero."""
 import math
 
 import pytest
@@ -87,3 +87,25 @@ def test_climbing_scores(dtype):
         q[..., 0] = 1
         lens = torch.full((batch,), length, dtype=torch.int32, device=DEV)
         check_attend(q, k, v, table, lens, scale=0.5)
+
+
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("batch,kv,heads", FORMS)
+def test_nothing_of_weight(bad, batch, kv, heads):
+    """Rows whose every score is -inf get zeros whatever V holds, the others what they see."""
+    gen = torch.Generator().manual_seed(71)
+    dim, page, length, dtype = 64, 16, 3000, torch.bfloat16
+    width = -(-length // page)
+    k, v = (torch.randn(batch * width, page, kv, dim, generator=gen).to(dtype).to(DEV) for _ in range(2))
+    table = torch.arange(batch * width, dtype=torch.int32, device=DEV).view(batch, width)
+    lens = torch.full((batch,), length, dtype=torch.int32, device=DEV)
+    k[..., 0] = -math.inf
+    v[..., 5] = bad
+    q = torch.zeros(batch, 1, heads, dim, dtype=dtype, device=DEV)
+    q[..., 0] = 1
+    out, lse = vts.tree_attention(q, k, v, table, lens, return_lse=True)
+    torch.cuda.synchronize()
+    assert (lse == -math.inf).all()
+    assert (out == 0).all()
+    o64, l64, _, _ = ref.attend(q[:, :, :1], k[:, :, :1], v[:, :, :1], table, lens)
+    assert (l64 == -math.inf).all() and (o64 == 0).all()

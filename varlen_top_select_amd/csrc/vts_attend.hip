@@ -598,14 +598,15 @@ struct Attend {
                                               float sum) const {
         int32_t t, head;
         if (!row_of(sub, r, t, head)) return;
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const bool none = sum == 0.0f;  // (then x is NaN where V is no finite number)
+        const float inv = 1.0f / sum;
         const int64_t at = ((int64_t)req * p.c.draft + t) * p.c.heads + head;
         u32x2 w;
-        w[0] = pack2<DT>(x[0] * inv, x[1] * inv);
-        w[1] = pack2<DT>(x[2] * inv, x[3] * inv);
+        w[0] = none ? 0 : pack2<DT>(x[0] * inv, x[1] * inv);
+        w[1] = none ? 0 : pack2<DT>(x[2] * inv, x[3] * inv);
         gstore((u32x2*)((char*)p.out + 2 * (at * D + d)), w);
         if (d == 0 && p.lse)
-            gstore(p.lse + at, sum == 0.0f ? NEG_INF
+            gstore(p.lse + at, none ? NEG_INF
                                            : (top + SHIFT + log2f(sum * __builtin_exp2f(-SHIFT))) *
                                                  0.6931471805599453f);
     }
