@@ -64,3 +64,12 @@ def test_weights_rows_that_coincide(lib, batch, kv, wb, wh, width, apart):
     got = lib.vts_attention_weight_add(cache(batch, kv), A, STRIDES, 2, 4 * kv, None, A, None, 0.1, A, wb,
                                        wh, width, None)
     assert (got != INVALID) == apart
+
+
+def test_empty_batch_with_slots(lib):
+    """The slots of no request: an address that is null and a top_k that is not 0."""
+    def call(slots, top_k):
+        return lib.vts_tree_attention(cache(batch=0), A, STRIDES, 2, 16, None, slots, top_k, 0.1, 2 * A,
+                                      None, A, 1 << 40, None)
+    assert call(None, 5) == call(None, 0) == call(A, 5) == OK
+    assert call(A, 0) == INVALID and call(None, -1) == INVALID and call(A, -1) == INVALID

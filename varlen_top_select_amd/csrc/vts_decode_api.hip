@@ -213,7 +213,9 @@ int vts_tree_attention(const vts_paged_cache* cache, const void* q, const int64_
     memset(&p, 0, sizeof(p));
     int st = paged(cache, draft, heads, true, &p.c);
     if (st != VTS_OK) return st;
-    if (slots != nullptr ? top_k < 1 : top_k != 0) return VTS_ERR_INVALID;
+    // (an empty batch's slots may have no address)
+    if (slots != nullptr ? top_k < 1 : top_k < 0 || (top_k > 0 && p.c.batch > 0))
+        return VTS_ERR_INVALID;
     if (top_k > INT32_MAX - MARGIN) return VTS_ERR_UNSUPPORTED;
     if (isnan(scale)) return VTS_ERR_INVALID;
     if (p.c.batch == 0) return VTS_OK;
