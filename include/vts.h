@@ -361,9 +361,9 @@ int topk_page_table_transform(const void* scores, int32_t dtype, int64_t num_row
  *            pages of page_size positions of kv_heads rows of head_dim (64 or
  *            128) consecutive elements.
  * k_strides, v_strides  elements between pages, positions of a page, and
- *            heads, multiples of 8: any order of the three dimensions is
- *            possible.  A cache spans at most 2^32 16-byte vectors and
- *            2^31 - 1 positions.
+ *            heads, multiples of 8 (ignored for a dimension of one): any order
+ *            of the three dimensions is possible.  A cache spans at most 2^32
+ *            16-byte vectors and 2^31 - 1 positions.
  * page_table device int32[batch, page_table_width], rows page_table_stride
  *            entries apart.
  * seq_lens   device int32[batch].

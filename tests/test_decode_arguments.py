@@ -73,3 +73,47 @@ def test_empty_batch_with_slots(lib):
                                       None, A, 1 << 40, None)
     assert call(None, 5) == call(None, 0) == call(A, 5) == OK
     assert call(A, 0) == INVALID and call(None, -1) == INVALID and call(A, -1) == INVALID
+
+
+def strided(batch=3, kv=4, dim=64, page=16, pages=50, ks=None, vs=None):
+    own = (page * kv * dim, kv * dim, dim)
+    return decode._CACHE.pack(A, A, *(ks or own), *(vs or own), A, 100, 100, A, pages, page, kv, dim, batch, 1)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the calls would run, on addresses that are none")
+def test_strides_of_one_element_do_not_count(lib):
+    """A dimension of one has no step: its stride may be anything."""
+    big = 1 << 50
+
+    def attend(c, q):
+        return lib.vts_tree_attention(c, A, decode._STRIDES.pack(*q), 1 if q[1] == 3 else 2, 16, None, None,
+                                      0, 0.1, 1 << 40, None, A, 1 << 40, None)
+    plain = (2048, 1024, 64)
+    own = (16 * 4 * 64, 4 * 64, 64)
+    assert attend(strided(), plain) != INVALID
+    assert attend(strided(kv=1, ks=(1024, 64, 1), vs=(1024, 64, big)), plain) != INVALID
+    assert attend(strided(page=1, ks=(256, 7, 64), vs=(256, big, 64)), plain) != INVALID
+    assert attend(strided(pages=1, ks=(3, 256, 64), vs=(big, 256, 64)), plain) != INVALID
+    assert attend(strided(batch=1), (1, 1024, 64)) != INVALID
+    assert attend(strided(), (2048, 3, 64)) != INVALID  # one drafted token
+    # of two and more they do
+    assert attend(strided(ks=(own[0], own[1], 4)), plain) == INVALID
+    assert attend(strided(), (2044, 1024, 64)) == INVALID
+    assert attend(strided(kv=1, ks=(1024, 60, 64)), plain) == INVALID
+    assert attend(strided(), (2048, 1024, 4)) == INVALID
+
+
+def test_binding_strides_of_one_element():
+    t = torch.zeros(5, 3, 4, 64)
+    assert decode._steps(t) == t.stride()[:3] == (768, 256, 64)
+    one = torch.as_strided(t, (5, 3, 1, 64), (256, 64, 1, 1))
+    assert decode._steps(one) == (256, 64, 0)
+    assert decode._steps(torch.as_strided(t, (1, 3, 4, 64), (7, 256, 64, 1))) == (0, 256, 64)
+    assert decode._steps(torch.as_strided(t, (1, 1, 1, 64), (3, 5, 1, 1))) == (0, 0, 0)
+    for size, stride in (((5, 3, 4, 64), (768, 256, 60, 1)), ((5, 3, 1, 64), (256, 60, 64, 1))):
+        assert decode._steps(torch.as_strided(t, size, stride)) is None
+    column = torch.zeros(4, 6, dtype=torch.int32).t()[:, :1]  # one column of rows 1 apart
+    assert column.stride() == (1, 6) and decode._row_step(column, 6) == 1
+    assert decode._row_step(torch.zeros(6, 4).t(), 4) is None
+    assert decode._row_step(torch.zeros(6, 4), 6) == 4
+    assert decode._row_step(torch.zeros(1, 4), 1) == 4

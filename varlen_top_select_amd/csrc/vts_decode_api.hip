@@ -27,16 +27,21 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
     return a0 < b0 + nb && b0 < a0 + na;
 }
 
-// A cache's strides in 16-byte vectors, which must reach its last row in 32 bits.
+// A cache's strides in 16-byte vectors, which must reach its last row in 32 bits
+// (0 for a dimension of one, whose stride means nothing).
 int cache_view(const void* base, const int64_t* strides, int64_t pages, int32_t page_size,
                int32_t kv_heads, int32_t head_dim, CacheView* out) {
     if (base == nullptr || !aligned(base, 16)) return VTS_ERR_INVALID;
+    const int64_t sizes[3] = {pages, page_size, kv_heads};
+    uint64_t s[3];
     for (int i = 0; i < 3; ++i) {
+        s[i] = 0;
+        if (sizes[i] == 1) continue;
         if (strides[i] < 0 || strides[i] % 8 != 0) return VTS_ERR_INVALID;
         if (strides[i] / 8 > UINT32_MAX) return VTS_ERR_UNSUPPORTED;
+        s[i] = (uint64_t)strides[i] / 8;
     }
-    const uint64_t s0 = (uint64_t)strides[0] / 8, s1 = (uint64_t)strides[1] / 8,
-                   s2 = (uint64_t)strides[2] / 8;
+    const uint64_t s0 = s[0], s1 = s[1], s2 = s[2];
     // each factor is below 2^32, so no product wraps; the sums stay below 2^66 / 4
     const uint64_t a = (uint64_t)(pages - 1) * s0, b = (uint64_t)(page_size - 1) * s1,
                    c = (uint64_t)(kv_heads - 1) * s2 + (uint64_t)head_dim / 8;
@@ -98,10 +103,11 @@ int paged(const vts_paged_cache* c, int32_t draft, int32_t heads, bool with_v, P
     return VTS_OK;
 }
 
-int check_q(const void* q, const int64_t* strides) {
+int check_q(const void* q, const int64_t* strides, const PagedParams& c) {
     if (q == nullptr || strides == nullptr || !aligned(q, 16)) return VTS_ERR_INVALID;
-    for (int i = 0; i < 3; ++i)
-        if (strides[i] < 0 || strides[i] % 8 != 0) return VTS_ERR_INVALID;
+    const int32_t sizes[3] = {c.batch, c.draft, c.heads};
+    for (int i = 0; i < 3; ++i)  // (a dimension of one has no step, and none is taken)
+        if (sizes[i] > 1 && (strides[i] < 0 || strides[i] % 8 != 0)) return VTS_ERR_INVALID;
     return VTS_OK;
 }
 
@@ -219,7 +225,7 @@ int vts_tree_attention(const vts_paged_cache* cache, const void* q, const int64_
     if (top_k > INT32_MAX - MARGIN) return VTS_ERR_UNSUPPORTED;
     if (isnan(scale)) return VTS_ERR_INVALID;
     if (p.c.batch == 0) return VTS_OK;
-    st = check_q(q, q_strides);
+    st = check_q(q, q_strides, p.c);
     if (st != VTS_OK) return st;
     const size_t rows = (size_t)p.c.batch * draft * heads;
     const size_t out_bytes = rows * cache->head_dim * 2;
@@ -273,7 +279,7 @@ int vts_attention_weight_add(const vts_paged_cache* cache, const void* q,
     if (p.c.batch == 0 || width == 0) return VTS_OK;
     if (!rows_apart(p.c.batch, weights_batch_stride, p.c.kv_heads, weights_head_stride, width))
         return VTS_ERR_INVALID;
-    st = check_q(q, q_strides);
+    st = check_q(q, q_strides, p.c);
     if (st != VTS_OK) return st;
     if (lse == nullptr || weights == nullptr || !aligned(lse, 4) || !aligned(weights, 4))
         return VTS_ERR_INVALID;

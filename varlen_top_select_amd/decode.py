@@ -82,6 +82,25 @@ def verify_draft_workspace_bytes(batch, vocab):
     return library().vts_verify_draft_workspace_bytes(batch, vocab)
 
 
+def _steps(t):
+    """The strides of a 4-D tensor's first three dimensions (0 where a dimension has one
+    element, whose stride means nothing), or None where its rows are no aligned vectors."""
+    a, b, c, d = t.stride()
+    if (a | b | c) & 7 or d != 1:
+        n = t.shape
+        a, b, c = a if n[0] > 1 else 0, b if n[1] > 1 else 0, c if n[2] > 1 else 0
+        if (a | b | c) & 7 or d != 1:
+            return None
+    return a, b, c
+
+
+def _row_step(t, rows):
+    """The stride between a table's contiguous rows, or None."""
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        return None
+    return t.stride(0) if rows > 1 else t.shape[1]
+
+
 def _cache(name, t, like=None):
     if not isinstance(t, torch.Tensor) or t.dim() != 4:
         raise ValueError(f"{name} must be a 4-D tensor [pages, page_size, kv_heads, head_dim]")
@@ -91,11 +110,11 @@ def _cache(name, t, like=None):
         raise ValueError(f"{name} must be on the GPU")
     if like is not None and (t.dtype is not like.dtype or t.get_device() != like.get_device()):
         raise ValueError(f"{name} must have the other cache's dtype and device")
-    sp, ss, sh, sd = t.stride()
-    if sd != 1 or (sp | ss | sh) & 7 or t.data_ptr() & 15:
+    steps = _steps(t)
+    if steps is None or t.data_ptr() & 15:
         raise ValueError(f"{name} rows must be contiguous, 16-byte aligned, with strides that "
                          "are multiples of 8 elements")
-    return sp, ss, sh
+    return steps
 
 
 def _tensor(name, t, dtype, shape, index):
@@ -108,9 +127,10 @@ def _tensor(name, t, dtype, shape, index):
 
 def _table(name, t, batch, index):
     if (not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.get_device() != index
-            or t.dim() != 2 or t.shape[0] != batch or t.shape[1] < 1 or t.stride(1) != 1):
+            or t.dim() != 2 or t.shape[0] != batch or t.shape[1] < 1
+            or (step := _row_step(t, batch)) is None):
         raise ValueError(f"{name} must be an int32 tensor of {batch} contiguous rows on cuda:{index}")
-    return t.stride(0) if batch > 1 else t.shape[1]
+    return step
 
 
 def _paged(k_cache, v_cache, page_table, seq_lens):
@@ -146,11 +166,11 @@ def _query(q, k_cache, batch, kv_heads, head_dim, index):
         raise ValueError(f"q must have 1..{MAX_DRAFT} drafted tokens a request")
     if heads < kv_heads or heads % kv_heads:
         raise ValueError("the query heads must be a multiple of the KV heads")
-    sb, st, sh, sd = q.stride()
-    if sd != 1 or (sb | st | sh) & 7 or q.data_ptr() & 15:
+    steps = _steps(q)
+    if steps is None or q.data_ptr() & 15:
         raise ValueError("q rows must be contiguous, 16-byte aligned, with strides that are "
                          "multiples of 8 elements")
-    return draft, heads, _STRIDES.pack(sb, st, sh)
+    return draft, heads, _STRIDES.pack(*steps)
 
 
 def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -197,7 +217,8 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
 
 def _weights(name, w, batch, kv_heads, index):
     if (not isinstance(w, torch.Tensor) or w.dtype is not torch.float32 or w.get_device() != index
-            or w.dim() != 3 or w.shape[0] != batch or w.shape[1] != kv_heads or w.stride(2) != 1):
+            or w.dim() != 3 or w.shape[0] != batch or w.shape[1] != kv_heads
+            or (w.stride(2) != 1 and w.shape[2] > 1)):
         raise ValueError(f"{name} must be a float32 tensor [{batch}, {kv_heads}, width] with "
                          f"contiguous rows on cuda:{index}")
     return w.stride(0), w.stride(1), w.shape[2]
