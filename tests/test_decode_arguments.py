@@ -117,3 +117,27 @@ def test_binding_strides_of_one_element():
     assert decode._row_step(torch.zeros(6, 4).t(), 4) is None
     assert decode._row_step(torch.zeros(6, 4), 6) == 4
     assert decode._row_step(torch.zeros(1, 4), 1) == 4
+
+
+def test_rows_that_meet_an_output():
+    """Exactly the tensors with an element in the output's memory."""
+    space = torch.zeros(6000, dtype=torch.bfloat16)
+    gen = torch.Generator().manual_seed(5)
+
+    def pick(*a):
+        return a[int(torch.randint(len(a), (1,), generator=gen))]
+    seen = [0, 0]
+    for _ in range(6000):
+        size = (pick(1, 2, 5), pick(1, 3), pick(1, 2, 4), pick(8, 16))
+        stride = (pick(0, 8, 64, 200, 512), pick(8, 24, 64, 128, 300), pick(0, 8, 16, 40, 256), 1)
+        t = space.as_strided(size, stride, pick(0, 8, 900, 2000))
+        at = int(torch.randint(0, 5000, (1,), generator=gen))
+        out = space[at:at + pick(1, 8, 64, 300)]
+        mark = torch.zeros_like(space)
+        mark.as_strided(size, stride, t.storage_offset()).fill_(1)
+        want = bool(mark[at:at + out.numel()].any())
+        assert decode._meets(out, t) == want, (size, stride, t.storage_offset(), at, out.numel())
+        seen[want] += 1
+    assert min(seen) > 300
+    assert not decode._meets(space[:0], space.view(2, 3, 10, 100))
+    assert not decode._meets(space, space.view(2, 3, 10, 100)[:0])

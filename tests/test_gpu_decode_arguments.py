@@ -76,3 +76,33 @@ def test_empty_batch():
                                           torch.zeros(0, 3, dtype=torch.int32, device=DEV),
                                           torch.zeros(0, 4, device=DEV))
     assert path.shape == (0, 3) and count.shape == token.shape == (0,)
+
+
+def test_out_over_its_inputs():
+    """Rows are written while others are still read: such an output is refused."""
+    gen = torch.Generator().manual_seed(83)
+    q, k, v, table, lens = step(gen, kv=2)
+    want = vts.tree_attention(q, k, v, table, lens)[0]
+    for t in (q, k, v):
+        near = t.flatten()[: q.numel()].view(q.shape)
+        with pytest.raises(ValueError, match="overlap"):
+            vts.tree_attention(q, k, v, table, lens, out=near)
+    # beside its inputs in one allocation it is none of them
+    both = torch.zeros(2, *q.shape, dtype=q.dtype, device=DEV)
+    both[0] = q
+    out, _ = vts.tree_attention(both[0], k, v, table, lens, out=both[1])
+    assert out.data_ptr() == both[1].data_ptr() and torch.equal(out, want) and torch.equal(both[0], q)
+
+
+def test_weights_rows_that_coincide():
+    gen = torch.Generator().manual_seed(84)
+    q, k, v, table, lens = step(gen, kv=2)
+    lse = vts.tree_attention(q, k, v, table, lens, return_lse=True)[1]
+    for stride in ((80, 80, 1), (40, 160, 1), (0, 80, 1), (80, 0, 1)):
+        w = torch.zeros(1000, device=DEV).as_strided((2, 2, 80), stride)
+        with pytest.raises((ValueError, vts.VtsError)):
+            vts.attention_weight_add(w, q, k, table, lens, lse)
+    apart = [torch.zeros(1000, device=DEV).as_strided((2, 2, 80), s) for s in ((160, 80, 1), (80, 160, 1), (200, 90, 1))]
+    for w in apart:
+        vts.attention_weight_add(w, q, k, table, lens, lse)
+    assert all(torch.equal(apart[0], w) for w in apart) and apart[0].any()

@@ -155,6 +155,29 @@ def _paged(k_cache, v_cache, page_table, seq_lens):
     return packed, index, batch, kv_heads, head_dim
 
 
+def _meets(out, t):
+    """Whether the contiguous `out` has memory in common with the rows of the 4-D t."""
+    if not out.numel() or not t.numel():
+        return False
+    e = t.element_size()
+    lo, hi = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
+    row = t.shape[3] * e
+    dims = sorted(((n, s * e) for n, s in zip(t.shape[:3], t.stride()) if n > 1 and s), key=lambda d: -d[1])
+
+    def within(at, i):  # some row of t's last dimensions i.. that begin at `at`
+        if i == len(dims):
+            return at < hi and at + row > lo
+        n, s = dims[i]
+        reach = row + sum((m - 1) * d for m, d in dims[i + 1:])
+        first = max(0, (lo - at - reach) // s + 1)  # the steps that end past lo
+        last = min(n - 1, (hi - at - 1) // s)       # those that begin before hi
+        if first <= last and at + last * s >= lo:
+            return True  # a row begins in there
+        return any(within(at + j * s, i + 1) for j in range(first, last + 1))
+
+    return within(t.data_ptr(), 0)
+
+
 def _query(q, k_cache, batch, kv_heads, head_dim, index):
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be a 4-D tensor [batch, draft, heads, head_dim]")
@@ -180,7 +203,8 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
                    return_lse: bool = False, workspace: torch.Tensor | None = None, stream=None):
     """Attention of q[batch, draft, heads, head_dim] over each request's cached
     prefix (or the listed ``slots``) and the drafted tokens that ``tree_mask``
-    names (vts_tree_attention in include/vts.h)."""
+    names (vts_tree_attention in include/vts.h).  Returns the outputs, in ``out`` if
+    given, which must not overlap q or the caches, and the rows' log-sum-exp or None."""
     cache, index, batch, kv_heads, head_dim = _paged(k_cache, v_cache, page_table, seq_lens)
     draft, heads, q_strides = _query(q, k_cache, batch, kv_heads, head_dim, index)
     mask_ptr = slots_ptr = None
@@ -195,6 +219,8 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         slots_ptr = _tensor("slots", slots, torch.int32, shape, index).data_ptr()
     if out is not None:
         _tensor("out", out, q.dtype, (batch, draft, heads, head_dim), index)
+        if _meets(out, q) or _meets(out, k_cache) or _meets(out, v_cache):
+            raise ValueError("out must not overlap q or the caches")
     if scale is None:
         scale = 1.0 / math.sqrt(head_dim)
     lib, device = library(), q.device
