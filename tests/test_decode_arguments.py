@@ -141,3 +141,18 @@ def test_rows_that_meet_an_output():
     assert min(seen) > 300
     assert not decode._meets(space[:0], space.view(2, 3, 10, 100))
     assert not decode._meets(space, space.view(2, 3, 10, 100)[:0])
+
+
+def test_no_kernel_that_no_call_reaches():
+    """With a head to each wave there are at most 64 rows, which lie in registers or LDS."""
+    if not os.path.exists(vts.LIB_PATH):
+        from varlen_top_select_amd import build
+        build.build()
+    with open(vts.LIB_PATH, "rb") as f:
+        names = f.read()
+    for dtype in (1, 2):
+        for dim in (64, 128):
+            for heads in (0, 1):
+                for rows in range(3):
+                    name = f"weigh_kernelILi{dtype}ELi{dim}ELb{heads}ELi{rows}EE".encode()
+                    assert (name in names) == (not (heads and rows == 2)), name

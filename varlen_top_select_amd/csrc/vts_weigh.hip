@@ -219,11 +219,12 @@ __global__ __launch_bounds__(NT, ROWS == ROWS_LDS && D == 128 ? 1 : 2) void weig
 template <int DT, int D, bool HEADS>
 static hipError_t launch_rows(const WeighParams& p, hipStream_t stream) {
     const dim3 grid((uint32_t)p.workers), block(NT);
+    // (with a head to each wave there are at most 64 rows)
     if (p.rows <= 16)
         hipLaunchKernelGGL((weigh_kernel<DT, D, HEADS, ROWS_REG>), grid, block, 0, stream, p);
-    else if (p.rows <= (HEADS ? 64 : 256))
+    else if (HEADS || p.rows <= 256)
         hipLaunchKernelGGL((weigh_kernel<DT, D, HEADS, ROWS_LDS>), grid, block, 0, stream, p);
-    else
+    else if constexpr (!HEADS)
         hipLaunchKernelGGL((weigh_kernel<DT, D, HEADS, ROWS_FAR>), grid, block, 0, stream, p);
     return hipGetLastError();
 }
