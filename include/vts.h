@@ -416,8 +416,9 @@ typedef struct {
  *            other, of any shape, but not for the selections.
  *
  * Sums are 32-bit; the probabilities are rounded to dtype for the product with
- * V.  The result depends on the shape and the lengths but not on timing.
- * Work is shared in units of 128 places over the batch's real lengths, so
+ * V, fp16's in a range that keeps their precision down to 2^-25 of the row's
+ * greatest.  The result depends on the shape and the lengths but not on timing.
+ * Work is shared in units of 32 to 128 places over the batch's real lengths, so
  * ragged batches cost what their lengths say.
  */
 size_t vts_tree_attention_workspace_bytes(int32_t batch, int32_t draft, int32_t heads,

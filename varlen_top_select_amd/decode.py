@@ -10,7 +10,9 @@
 A cache is a 4-D tensor ``[num_pages, page_size, kv_heads, head_dim]`` of any
 strides that are multiples of 8 elements (so a cache laid out heads first is
 passed as a permuted view), bfloat16 or float16.  Lengths count the drafted
-tokens, as ``next_n`` does in ``topk_varlen``.
+tokens, as ``next_n`` does in ``topk_varlen``.  The operators serve decoding and
+have no derivatives: their outputs carry no gradient, also of inputs that require
+one.
 
 Without ``workspace`` the calls share one per device and stream, made at the first
 eager call and held until the process ends, also where a larger shape has
