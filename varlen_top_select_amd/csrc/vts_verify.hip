@@ -33,8 +33,9 @@ namespace vts {
 
 constexpr int VT = 1024;  // threads
 constexpr int VW = VT / 64;
-// launches of a tree's walk that end with a sum by all (16 trees of 24 over 100003
-// bf16: 66 us with 2, 61 with 3, 51 with 5, 55 with 7)
+// launches of a tree's walk that end with a sum by all (16 trees over 100003 bf16:
+// of 24 tokens 56 us with 2, 51 with 3, 49 with 5, 52 with 7; of 4 tokens, whose
+// walk seldom needs so many, 27, 30, 34 and 37)
 constexpr int ROUNDS = 5;
 
 // a 16-byte load from any element's address
