@@ -17,6 +17,14 @@
  *   vts_evict_cache                 eviction by that weight
  *   vts_verify_draft                acceptance of drafted tokens
  *
+ * and what brings a request that far:
+ *
+ *   vts_write_cache                 head norms, positions, keys and values into
+ *                                   the cache, in 16, 8 or 4 bits
+ *   vts_read_cache                  cached rows of listed slots
+ *   vts_prompt_attention            attention of packed prompts
+ *   vts_tree_attention_microscaled  vts_tree_attention over 8- or 4-bit caches
+ *
  * The unprefixed names topk_varlen and topk_page_table_transform are exported
  * as aliases of the two entry points.
  *
@@ -516,6 +524,170 @@ int vts_verify_draft(const void* target_probs, int32_t dtype, int64_t target_bat
                      const int32_t* draft_tokens, const int32_t* parents, const float* uniforms,
                      int64_t batch, int32_t draft, int64_t vocab, int32_t* path, int32_t* count,
                      int32_t* next_token, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Filling a paged cache, microscaled caches, and prompts.
+ *
+ * A microscaled cache holds its rows in 8 or 4 bits to an element and one power
+ * of two to 32 consecutive ones.  Its vts_paged_cache has the dtype of the queries
+ * and outputs; k and v point to bytes, rows of head_dim (bits 8) or head_dim / 2
+ * (bits 4) of them, 16-byte aligned, k_strides and v_strides in bytes, multiples of
+ * 16.  Elements are E4M3 numbers (bits 8: sign, 4 bits of exponent with bias 7, 3 of
+ * mantissa; 0x7F and 0xFF are NaN) or E2M1 (bits 4: 0, 0.5, 1, 1.5, 2, 3, 4, 6 with a
+ * sign, the first of two in a byte's low half).  A scale is one byte, E8M0: 2^(x - 127), NaN
+ * for 255.  Values are rounded to the queries' dtype where they are used: bf16 holds
+ * every number of the format down to 2^-133, fp16 those of its own range.
+ *
+ * k, v       device: head_dim / 32 bytes per row, aligned to that.
+ * k_strides, v_strides  bytes between pages, positions of a page, and heads,
+ *            multiples of head_dim / 32 (ignored for a dimension of one).
+ */
+typedef struct {
+    const uint8_t* k;
+    const uint8_t* v;
+    int64_t k_strides[3];
+    int64_t v_strides[3];
+    int32_t bits;
+} vts_microscales;
+
+/*
+ * vts_tree_attention_microscaled -- vts_tree_attention over a microscaled cache,
+ * with the same arguments, masks and guarantees; the workspace serves caches of
+ * 8 and of 4 bits.
+ */
+size_t vts_tree_attention_microscaled_workspace_bytes(int32_t batch, int32_t draft, int32_t heads,
+                                                      int32_t kv_heads, int32_t head_dim, int32_t top_k);
+int vts_tree_attention_microscaled(const vts_paged_cache* cache, const vts_microscales* scales, const void* q,
+                                   const int64_t* q_strides, int32_t draft, int32_t heads,
+                                   const int64_t* tree_mask, const int32_t* slots, int32_t top_k, float scale,
+                                   void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/*
+ * vts_write_cache -- new tokens' queries made ready and their keys and values put
+ * into the cache:
+ *
+ *   x'    = x / sqrt(mean(x^2) + eps) * norm          (q and k, per head; norm NULL:
+ *                                                      x' = x)
+ *   (a, b) -> (a c - b s, b c + a s)                  (q and k, per pair of x';
+ *                                                      rotary NULL: not turned)
+ *
+ * where pair i of a row is elements i and i + rot / 2 (interleaved: 2 i and 2 i + 1),
+ * i < rot / 2, and c = rotary[position][i], s = rotary[position][rot / 2 + i];
+ * elements from rot on are not turned.  q goes to q_out, k (and to k_out, if given) and
+ * v to the slot's rows of the cache.  Rows are computed in 32 bits and rounded once.
+ * For a microscaled cache k is computed in 64: each block of 32 elements gets the least
+ * power of two (from 2^-127) with which its largest magnitude rounds to a number of the
+ * format, and its elements, divided by that, are rounded to nearest, ties to even; a block
+ * that holds an infinity or NaN gets the scale NaN.
+ *
+ * A slot outside the cache (-1 for padding) is not written; the token's q_out and
+ * k_out are.  A token whose position is outside [0, max_position) gets zeros in q_out
+ * and k_out and is not written.  The slots inside the cache have to be distinct: the
+ * entry of one named twice holds parts of either token.  Nothing else of the cache
+ * changes.  page_table, seq_lens and batch of `cache` are not looked at.
+ *
+ * q, k, v    device, the cache's dtype, 16-byte aligned rows of head_dim elements;
+ *            strides: elements between tokens and heads, multiples of 8.
+ * q_norm, k_norm  device [head_dim], 16-byte aligned, of norm_dtype (VTS_F32 or the
+ *            cache's dtype), or NULL.
+ * rotary     device float[max_position, rot], 16-byte aligned, or NULL (then rot is
+ *            0); rot: a multiple of 16, at most head_dim.
+ * positions  device int32[tokens] (not read without rotary).
+ * slots      device int32[tokens].
+ * q_out      device, dtype[tokens, heads, head_dim], 16-byte aligned; k_out: the same
+ *            with kv_heads, or NULL.  They must not overlap each other, the inputs
+ *            or the caches.
+ * At most 2^25 tokens.
+ */
+typedef struct {
+    const void* q;
+    const void* k;
+    const void* v;
+    int64_t q_strides[2];
+    int64_t k_strides[2];
+    int64_t v_strides[2];
+    const void* q_norm;
+    const void* k_norm;
+    double eps;
+    const float* rotary;
+    int64_t max_position;
+    const int32_t* positions;
+    const int32_t* slots;
+    int64_t tokens;
+    void* q_out;
+    void* k_out;
+    int32_t heads;
+    int32_t norm_dtype;
+    int32_t rot;
+    int32_t interleaved;
+} vts_new_tokens;
+int vts_write_cache(const vts_paged_cache* cache, const vts_microscales* scales, const vts_new_tokens* tokens,
+                    void* stream);
+
+/*
+ * vts_read_cache -- the cached rows of listed slots, as rows of the cache's dtype:
+ * k_out[i], v_out[i] = rows of all KV heads of slots[i], zeros for a slot outside the
+ * cache.  A slot may be listed more than once.
+ *
+ * scales     of a microscaled cache, or NULL.
+ * slots      device int32[count].
+ * k_out, v_out  device, dtype[count, kv_heads, head_dim], 16-byte aligned; they must
+ *            not overlap each other or the caches.
+ * At most 2^33 / (kv_heads * head_dim / 8) slots.  page_table, seq_lens and batch of
+ * `cache` are not looked at.
+ */
+int vts_read_cache(const vts_paged_cache* cache, const vts_microscales* scales, const int32_t* slots,
+                   int64_t count, void* k_out, void* v_out, void* stream);
+
+/*
+ * vts_prompt_attention -- attention of packed prompts.
+ *
+ *   out[i, h] = sum_j p_j v_j,   p = softmax_j(scale * q[i, h] . k_j)
+ *   lse[i, h] = log sum_j exp(scale * q . k_j)
+ *
+ * Sequence b has query rows [cu_q[b], cu_q[b + 1]) and key rows [cu_k[b], cu_k[b + 1]);
+ * query head h uses KV head h / (heads / kv_heads).  causal: its queries are the last of
+ * its keys, so of nq queries and nk keys query i sees the keys j <= i + nk - nq; else
+ * all.  A row that sees nothing, or nothing of weight, gets zeros and an lse of
+ * -inf.  Values of keys that a row does not see never reach it, infinities and NaN
+ * among them.  Rows of no sequence (before cu_q[0], from cu_q[batch] on) are left as
+ * they were, or with `clear` get zeros and -inf.
+ *
+ * Entries of cu_q and cu_k are clamped to the rows there are; one below its
+ * predecessor makes an empty sequence, after which what later sequences' rows get is
+ * not defined (nothing outside the outputs is touched).
+ *
+ * q, k, v    device, dtype (VTS_BF16 or VTS_F16), 16-byte aligned rows of head_dim
+ *            (64 or 128) elements, total_q of heads, total_k of kv_heads; strides:
+ *            elements between tokens and heads, multiples of 8.
+ * cu_q, cu_k device int32[batch + 1], ascending.
+ * out        device, dtype[total_q, heads, head_dim], 16-byte aligned; must not
+ *            overlap the inputs.
+ * lse        device float[total_q, heads] or NULL.
+ *
+ * total_q * heads, total_k and batch are below 2^31 - 1024, and kv_heads *
+ * (total_q * (heads / kv_heads) / 128 + batch) is at most 2^24 - 64.
+ */
+typedef struct {
+    const void* q;
+    const void* k;
+    const void* v;
+    int64_t q_strides[2];
+    int64_t k_strides[2];
+    int64_t v_strides[2];
+    const int32_t* cu_q;
+    const int32_t* cu_k;
+    int64_t batch;
+    int64_t total_q;
+    int64_t total_k;
+    int32_t heads;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t dtype;
+} vts_prompts;
+int vts_prompt_attention(const vts_prompts* prompts, int32_t causal, float scale, void* out, float* lse,
+                         int32_t clear, void* stream);
 
 /* Human-readable text of a vts_status. */
 const char* vts_status_string(int status);

@@ -16,7 +16,8 @@ transforms): a unique selection, in canonical order unless ``sort=False``.
 
 The operators of the rest of the decode step (attention of drafted tokens over a
 paged cache, accumulated attention weight, eviction, draft verification) are in
-``varlen_top_select_amd.decode`` and exported here too.
+``varlen_top_select_amd.decode``, those that fill the cache and attend a prompt in
+``varlen_top_select_amd.cache``; all are exported here too.
 
 The C entry points, their argument contracts and the page citations are in
 ``include/vts.h``.
@@ -34,7 +35,8 @@ __all__ = ["topk_varlen", "topk_varlen_noalloc", "topk_varlen_ordered", "topk_pa
            "workspace_bytes", "make_workspace",
            "set_tuning", "workspace_stats", "VtsError", "library", "LIB_PATH",
            "tree_attention", "attention_weight_add", "evict_cache", "verify_draft",
-           "tree_mask_from_parents"]
+           "tree_mask_from_parents",
+           "write_cache", "read_cache", "prompt_attention", "rotary_table", "page_slots"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libvts.so")
@@ -102,6 +104,7 @@ def library():
     lib.vts_set_tuning.restype = ctypes.c_int
     lib.vts_set_tuning.argtypes = [i32, i64]
     decode.declare(lib)
+    cache.declare(lib)
     _lib = lib
     return lib
 
@@ -416,6 +419,8 @@ def workspace_stats(workspace: torch.Tensor, stream=None) -> list[int]:
     return list(out)
 
 
-from . import decode  # noqa: E402  (uses the helpers above)
+from . import cache, decode  # noqa: E402  (use the helpers above)
+from .cache import (page_slots, prompt_attention, read_cache, rotary_table,  # noqa: E402
+                    write_cache)
 from .decode import (attention_weight_add, evict_cache, tree_attention,  # noqa: E402
                      tree_mask_from_parents, verify_draft)

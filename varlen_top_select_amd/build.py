@@ -9,10 +9,13 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libvts.so")
 # compiled separately and in parallel, linked in this order (first the
 # kernels' code objects: any-order selection, the deterministic mode, top_k
-# above 2048, the hint rung, the decode-step operators)
+# above 2048, the hint rung, the decode-step operators, microscaled caches, the cache's
+# filling and prompts)
 SOURCES = ["vts_kernels.hip", "vts_kernels_ordered.hip", "vts_kernels_wide.hip",
            "vts_kernels_hint.hip", "vts_attend.hip", "vts_weigh.hip", "vts_evict.hip",
-           "vts_verify.hip", "vts_api.hip", "vts_decode_api.hip"]
+           "vts_verify.hip", "vts_attend_micro_bf16.hip", "vts_attend_micro_f16.hip",
+           "vts_cache.hip", "vts_prompt.hip", "vts_api.hip", "vts_decode_api.hip",
+           "vts_cache_api.hip"]
 PROBE_LIB = os.path.join(HERE, "libvts_probe.so")
 PROBE_SOURCES = ["vts_probe.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -32,7 +35,8 @@ FLAGS = [
 MIN_WAVES_PER_SIMD = 4
 # The decode-step kernels must not spill either: a spill's load waits for every
 # cache row on its way.
-NO_SCRATCH = ("topk_kernel", "attend_kernel", "weigh_kernel", "evict_", "verify_")
+NO_SCRATCH = ("topk_kernel", "attend_kernel", "weigh_kernel", "evict_", "verify_", "write_kernel",
+              "read_kernel", "prompt_kernel")
 
 
 def _check_resources(remarks: str, out: str) -> None:

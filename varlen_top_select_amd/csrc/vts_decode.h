@@ -24,6 +24,12 @@ struct CacheView {
     uint32_t page_stride, pos_stride, head_stride;
 };
 
+// A microscaled cache's scales: head_dim / 32 bytes to a row, strides in such rows.
+struct ScaleView {
+    const uint8_t* base;
+    uint32_t page_stride, pos_stride, head_stride;
+};
+
 struct PagedParams {
     CacheView k, v;
     const int32_t* table;
@@ -59,6 +65,7 @@ struct AttendParams {
     // [..][D], maximum and sum [..][2]
     float* part_o;
     float* part_ml;
+    ScaleView k_scale, v_scale;  // of a microscaled cache
 };
 
 struct WeighParams {
@@ -122,6 +129,9 @@ struct VerifyParams {
 };
 
 hipError_t launch_attend(int dtype, int head_dim, const AttendParams& p, hipStream_t stream);
+// the same over a microscaled cache, bf16 or fp16 queries and outputs
+hipError_t launch_attend_micro_bf16(int head_dim, int bits, const AttendParams& p, hipStream_t stream);
+hipError_t launch_attend_micro_f16(int head_dim, int bits, const AttendParams& p, hipStream_t stream);
 hipError_t launch_weigh(int dtype, int head_dim, const WeighParams& p, hipStream_t stream);
 hipError_t launch_evict(const EvictParams& p, hipStream_t stream);
 hipError_t launch_verify(int dtype, const VerifyParams& p, hipStream_t stream);

@@ -52,6 +52,31 @@ __device__ __forceinline__ float to_float(uint32_t raw16) {
         return (float)__builtin_bit_cast(_Float16, (uint16_t)raw16);
 }
 
+// ---- microscaled rows: one power of two (E8M0) per 32 elements of 8 bits (E4M3) or
+// 4 (E2M1, the first of two in the low half of a byte)
+
+// The scale as the conversions take it: a float's exponent.  They read 0 as 2^-127 and
+// the infinity that 255 gives as NaN.
+__device__ __forceinline__ float scale_of(uint32_t code) {
+    return __builtin_bit_cast(float, code << 23);
+}
+// the two numbers in byte I of x
+template <int DT, int I>
+__device__ __forceinline__ uint32_t widen4(uint32_t x, float scale) {
+    if constexpr (DT == BF16)
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, scale, I));
+    else
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(x, scale, I));
+}
+// the two numbers in the low or high half of x
+template <int DT, bool HI>
+__device__ __forceinline__ uint32_t widen8(uint32_t x, float scale) {
+    if constexpr (DT == BF16)
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, scale, HI));
+    else
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x, scale, HI));
+}
+
 template <int DT>
 __device__ __forceinline__ bool not_finite(uint32_t pair) {
     constexpr uint32_t E = DT == BF16 ? 0x7F80u : 0x7C00u;

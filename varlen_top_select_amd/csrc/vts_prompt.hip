@@ -1,0 +1,395 @@
+// vts_prompt.hip -- attention of whole prompts, packed one after the other.
+//
+//   o_i = sum_j p_ij v_j,  p_i = softmax_j(scale * q_i . k_j)
+//
+// over the keys j of i's sequence, up to i's own (its queries are the last of its
+// keys).  One pass with a running maximum and sum per row, as in vts_attend.hpp.
+//
+// The rows of a workgroup are tokens times the query heads of one KV head, so that K
+// and V are read once for a whole group and a tile of 128 rows spans few tokens: its
+// masked corner is small, and a sequence of one token still fills `group` rows.  A wave
+// has 32 rows; K and V tiles of 64 keys go through LDS for all waves.  With K rows
+// as A and query rows as B of the 32x32x16 product, lane l gets scores of row l % 32
+// at keys 8 * (e / 4) + 4 * (l / 32) + e % 4: its sixteen probabilities are already
+// its B operands of the second product, with V's keys taken in the same order by
+// transposing LDS loads.  m is raised only when a score passes it by a margin.
+#include "vts_cache.h"
+#include "vts_paged.hpp"
+
+namespace vts {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+template <int DT>
+__device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+    if constexpr (DT == BF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+                                                      __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+constexpr int PROMPT_WAVES = PROMPT_ROWS / 32;
+constexpr int PROMPT_NT = PROMPT_WAVES * 64;
+constexpr int PROMPT_KEYS = 64;  // of a tile
+
+template <int D>
+struct PromptShared {
+    u32x4 k[2][PROMPT_KEYS * (D / 8)], v[2][PROMPT_KEYS * (D / 8)];
+};
+
+// A workgroup's tile: its sequence, the first of its rows, and the lengths.
+struct PromptTile {
+    int32_t q0, k0, lq, lk, row0;
+    bool found;
+};
+
+__device__ __forceinline__ int32_t cu_at(const int32_t* cu, int32_t i, int32_t total) {
+    const int32_t n = gload(cu + i);
+    return n < 0 ? 0 : n > total ? total : n;
+}
+
+// Tile t of all sequences' tiles.  Every wave finds it by itself, 64 sequences at a time.
+__device__ __forceinline__ PromptTile find_tile(const PromptParams& p, int32_t t) {
+    PromptTile r;
+    r.found = false;
+    const int lane = lane_id();
+    int32_t base = 0;
+    for (int32_t b0 = 0; b0 < p.batch; b0 += 64) {
+        const int32_t b = b0 + lane;
+        int32_t q0 = 0, len = 0;
+        if (b < p.batch) {
+            q0 = cu_at(p.cu_q, b, p.total_q);
+            len = cu_at(p.cu_q, b + 1, p.total_q) - q0;
+            if (len < 0) len = 0;
+        }
+        const int32_t mine = (len * p.group + PROMPT_ROWS - 1) / PROMPT_ROWS;
+        int32_t inc = mine;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int32_t o = __shfl_up(inc, d);
+            if (lane >= d) inc += o;
+        }
+        const uint64_t past = ballot(t < base + inc);
+        if (past) {
+            const int at = __builtin_ctzll(past);
+            r.found = true;
+            r.q0 = __builtin_amdgcn_readlane(q0, at);
+            r.lq = __builtin_amdgcn_readlane(len, at);
+            const int32_t tiles = __builtin_amdgcn_readlane(mine, at);
+            const int32_t first = base + __builtin_amdgcn_readlane(inc, at) - tiles;
+            // the sequence's last tile, which sees the most, comes first
+            r.row0 = (tiles - 1 - (t - first)) * PROMPT_ROWS;
+            r.k0 = __builtin_amdgcn_readfirstlane(cu_at(p.cu_k, b0 + at, p.total_k));
+            r.lk = __builtin_amdgcn_readfirstlane(cu_at(p.cu_k, b0 + at + 1, p.total_k)) - r.k0;
+            if (r.lk < 0) r.lk = 0;
+            return r;
+        }
+        base += __builtin_amdgcn_readlane(inc, 63);
+    }
+    return r;
+}
+
+template <int DT, int D>
+struct Prompt {
+    static constexpr int CH = D / 8;     // 16-byte chunks of a row
+    static constexpr int KS = D / 16;    // steps of the first product
+    static constexpr int MT = D / 32;    // tiles of the second
+    static constexpr int LOADS = PROMPT_KEYS * CH / PROMPT_NT;
+    static constexpr float SHIFT = DT == F16 ? 11 : 0, RAISE = DT == F16 ? 15 : 8;
+
+    const PromptParams& p;
+    PromptShared<D>& sm;
+    PromptTile t;
+    int32_t kv;
+    int tid, lane, wave, col, half;
+    int32_t limit;  // the last key that the lane's row sees, -1: none
+    bool valid;
+    int64_t row_out;  // the row's place in lse, and out
+    u32x4 q[KS];
+    f32x16 o[MT];
+    float m, l;
+    u32x4 kr[LOADS], vr[LOADS];  // the tile on its way
+
+    __device__ __forceinline__ Prompt(const PromptParams& p_, PromptShared<D>& s_, const PromptTile& t_, int32_t kv_)
+        : p(p_), sm(s_), t(t_), kv(kv_) {
+        tid = threadIdx.x;
+        lane = tid & 63;
+        wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        col = lane & 31;
+        half = lane >> 5;
+        const int32_t row = t.row0 + wave * 32 + col;
+        const int32_t token = row / p.group, head = kv * p.group + (row - token * p.group);
+        valid = token < t.lq;
+        limit = !valid ? -1 : p.causal ? token + t.lk - t.lq : t.lk - 1;
+        row_out = (int64_t)(t.q0 + token) * p.heads + head;
+        const char* at = (const char*)p.q +
+                         2 * (valid ? (int64_t)(t.q0 + token) * p.q_token + head * p.q_head : 0);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            u32x4 x = {0, 0, 0, 0};
+            if (valid) x = gload((const u32x4*)at + s * 2 + half);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] ^= p.q_sign;
+            q[s] = x;
+        }
+        m = NEG_INF;
+        l = 0;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[i][e] = 0;
+    }
+
+    static __device__ __forceinline__ int k_at(int r, int c) {
+        return r * CH + (c ^ (D == 128 ? r & 15 : (r >> 1) & 7));
+    }
+    // V's chunks are moved by 64 bytes from row to row, so that the four rows that a
+    // transposing load takes lie in different banks
+    static __device__ __forceinline__ int v_at(int r, int c) {
+        return r * CH + (c ^ ((D == 128 ? r & 3 : (r >> 1) & 1) << 2));
+    }
+
+    __device__ __forceinline__ void load(int32_t j0) {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int x = i * PROMPT_NT + tid, c = x % CH;
+            int32_t j = j0 + x / CH;
+            if (j >= t.lk) j = t.lk - 1;
+            const int64_t row = t.k0 + j;
+            kr[i] = gload((const u32x4*)((const char*)p.k + 2 * (row * p.k_token + kv * p.k_head)) + c);
+            vr[i] = gload((const u32x4*)((const char*)p.v + 2 * (row * p.v_token + kv * p.v_head)) + c);
+        }
+    }
+    __device__ __forceinline__ void stage(int buf) {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int x = i * PROMPT_NT + tid, r = x / CH, c = x % CH;
+            sm.k[buf][k_at(r, c)] = kr[i];
+            sm.v[buf][v_at(r, c)] = vr[i];
+        }
+    }
+    __device__ __forceinline__ static int key_of(int e) { return 8 * (e >> 2) + (e & 3); }
+
+    // V's operand of keys 16 * step .. and elements 32 * i ..: eight keys in the order
+    // of the lane's probabilities
+    __device__ __forceinline__ u32x4 operand_v(int buf, int step, int i) const {
+        const int g = lane >> 4, n = lane & 15;
+        u32x4 x;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const int r = 16 * step + 8 * w + 4 * (g >> 1) + (n >> 2);
+            const int c = 4 * i + 2 * (g & 1) + ((n & 3) >> 1);
+            const char* at = (const char*)&sm.v[buf][v_at(r, c)] + 8 * (n & 1);
+            const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4*)at);
+            const u32x2 z = __builtin_bit_cast(u32x2, y);
+            x[2 * w] = z[0];
+            x[2 * w + 1] = z[1];
+        }
+        return x;
+    }
+
+    template <bool MASKED>
+    __device__ __forceinline__ void tile(int32_t j0, int buf) {
+        const float c = p.scale_log2e;
+        f32x16 s[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[b][e] = 0;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+                s[b] = mfma32<DT>(sm.k[buf][k_at(32 * b + col, 2 * ks + half)], q[ks], s[b]);
+        if constexpr (MASKED) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    s[b][e] = j0 + 32 * b + key_of(e) + 4 * half <= limit ? s[b][e] : NEG_INF;
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) top = fmaxf(top, s[b][e]);
+        top *= c;
+        if (ballot(top > m + RAISE)) {
+            float up = fmaxf(top, __shfl_xor(top, 32));
+            up = up > m + RAISE ? up - SHIFT : m;
+            const float f = up == NEG_INF ? 1.0f : __builtin_amdgcn_exp2f(m - up);
+            m = up;
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[i][e] *= f;
+        }
+        const float base = m == NEG_INF ? 0.0f : m;
+        u32x4 pv[4];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+                const float x = __builtin_amdgcn_exp2f(fmaf(s[b][e], c, -base));
+                const float y = __builtin_amdgcn_exp2f(fmaf(s[b][e + 1], c, -base));
+                l += x + y;
+                pv[2 * b + (e >> 3)][(e >> 1) & 3] = pack2<DT>(x, y);
+            }
+        if constexpr (MASKED) {
+            if (any_not_finite(buf)) {
+                product_not_finite(j0, buf, pv);
+                return;
+            }
+        }
+#pragma unroll
+        for (int step = 0; step < 4; ++step)
+#pragma unroll
+            for (int i = 0; i < MT; ++i) o[i] = mfma32<DT>(operand_v(buf, step, i), pv[step], o[i]);
+    }
+
+    // Where not every row sees every key, an infinity or NaN in V would reach rows that
+    // do not see it (0 * inf).  Such a tile's finite elements go through the product
+    // and the others are added to the rows that see them.
+    __device__ __forceinline__ bool any_not_finite(int buf) const {
+        bool bad = false;
+#pragma unroll 4
+        for (int x = lane; x < PROMPT_KEYS * CH; x += 64) {
+            const u32x4 w = sm.v[buf][x];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) bad = bad || not_finite<DT>(w[e]);
+        }
+        return ballot(bad) != 0;
+    }
+    __device__ __forceinline__ void product_not_finite(int32_t j0, int buf, const u32x4 (&pv)[4]) {
+    #pragma unroll
+        for (int step = 0; step < 4; ++step)
+    #pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                u32x4 x = operand_v(buf, step, i);
+    #pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (not_finite<DT>(x[e] & 0xFFFFu)) x[e] &= 0xFFFF0000u;
+                    if (not_finite<DT>(x[e] >> 16)) x[e] &= 0xFFFFu;
+                }
+                o[i] = mfma32<DT>(x, pv[step], o[i]);
+            }
+    #pragma unroll 1
+        for (int key = 0; key < PROMPT_KEYS; ++key) {
+            // the key's weight for this lane's row lies in the lane of one half
+            uint32_t pair = 0;
+    #pragma unroll
+            for (int step = 0; step < 4; ++step)
+    #pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    // word e of a step holds keys 16 step + 8 (e / 2) + 4 half + 2 (e % 2) + {0, 1}
+                    pair = (key >> 4) == step && ((key >> 3) & 1) * 2 + ((key >> 1) & 1) == e ? pv[step][e] : pair;
+            pair = from_lane(pair, ((key >> 2) & 1) * 32 + col);
+            const float w = to_float<DT>((pair >> (16 * (key & 1))) & 0xFFFFu);
+            const bool see = j0 + key <= limit;
+    #pragma unroll
+            for (int i = 0; i < MT; ++i)
+    #pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int d = 32 * i + key_of(e) + 4 * half;
+                    const uint32_t raw = ((const uint16_t*)&sm.v[buf][v_at(key, d / 8)])[d % 8];
+                    const float y = o[i][e] + w * to_float<DT>(raw);
+                    o[i][e] = see && not_finite<DT>(raw) ? y : o[i][e];
+                }
+        }
+    }
+
+    __device__ __forceinline__ void write() {
+        l += __shfl_xor(l, 32);
+        if (!valid) return;
+        const bool none = l == 0.0f;  // (then o is NaN where V is no finite number)
+        const float inv = 1.0f / l;
+        char* at = (char*)p.out + 2 * row_out * D;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                u32x2 w;
+                w[0] = none ? 0 : pack2<DT>(o[i][e] * inv, o[i][e + 1] * inv);
+                w[1] = none ? 0 : pack2<DT>(o[i][e + 2] * inv, o[i][e + 3] * inv);
+                gstore((u32x2*)(at + 2 * (32 * i + key_of(e) + 4 * half)), w);
+            }
+        if (half == 0 && p.lse)
+            gstore(p.lse + row_out, none ? NEG_INF
+                                         : (m + SHIFT + log2f(l * __builtin_exp2f(-SHIFT))) *
+                                               0.6931471805599453f);
+    }
+
+    // the tile at j0 to LDS, and the next one on its way
+    __device__ __forceinline__ void next(int32_t j0, int32_t end, int buf) {
+        // the other half may still be read; this one was done with before the last barrier
+        stage(buf);
+        if (j0 + PROMPT_KEYS < end) load(j0 + PROMPT_KEYS);
+        __syncthreads();
+    }
+    __device__ __forceinline__ void run() {
+        // the keys that the last token of the tile sees, and those that all rows see
+        const int32_t rows = t.lq * p.group;
+        const int32_t last_row = t.row0 + PROMPT_ROWS < rows ? t.row0 + PROMPT_ROWS - 1 : rows - 1;
+        const int32_t end = !p.causal ? t.lk : last_row / p.group + 1 + t.lk - t.lq;
+        const int32_t all = !p.causal ? t.lk : t.row0 / p.group + 1 + t.lk - t.lq;
+        if (end > 0) {
+            load(0);
+            int32_t j0 = 0;
+            int buf = 0;
+#pragma unroll 1
+            for (; j0 + PROMPT_KEYS <= all; j0 += PROMPT_KEYS, buf ^= 1) {
+                next(j0, end, buf);
+                tile<false>(j0, buf);
+            }
+#pragma unroll 1
+            for (; j0 < end; j0 += PROMPT_KEYS, buf ^= 1) {
+                next(j0, end, buf);
+                tile<true>(j0, buf);
+            }
+        }
+        write();
+    }
+};
+
+template <int DT, int D>
+__global__ __launch_bounds__(PROMPT_NT, 1) void prompt_kernel(PromptParams p) {
+    __shared__ PromptShared<D> sm;
+    const int32_t work = p.tiles * p.kv_heads;
+    if ((int32_t)blockIdx.x >= work) {
+        // rows of no sequence, before the first and behind the last
+        const int32_t a = p.batch > 0 ? cu_at(p.cu_q, 0, p.total_q) : 0;
+        const int32_t b = p.batch > 0 ? cu_at(p.cu_q, p.batch, p.total_q) : 0;
+        const int64_t per = (int64_t)p.heads * (D / 8), all = ((int64_t)a + p.total_q - b) * per;
+        const int64_t step = (int64_t)(gridDim.x - work) * PROMPT_NT;
+        for (int64_t x = (int64_t)(blockIdx.x - work) * PROMPT_NT + threadIdx.x; x < all; x += step) {
+            const int64_t y = x < a * per ? x : x + (int64_t)(b - a) * per;
+            gstore((u32x4*)p.out + y, u32x4{0, 0, 0, 0});
+            if (p.lse && y % (D / 8) == 0) gstore(p.lse + y / (D / 8), NEG_INF);
+        }
+        return;
+    }
+    const int32_t kv = (int32_t)blockIdx.x % p.kv_heads;
+    const PromptTile t = find_tile(p, (int32_t)blockIdx.x / p.kv_heads);
+    if (!t.found) return;
+    Prompt<DT, D> a(p, sm, t, kv);
+    a.run();
+}
+
+template <int DT, int D>
+static hipError_t start(const PromptParams& p, hipStream_t stream) {
+    const uint32_t grid = (uint32_t)(p.tiles * p.kv_heads + (p.clear ? 64 : 0));
+    hipLaunchKernelGGL((prompt_kernel<DT, D>), dim3(grid), dim3(PROMPT_NT), 0, stream, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_prompt(int dtype, int head_dim, const PromptParams& p, hipStream_t stream) {
+    if (dtype == BF16) return head_dim == 64 ? start<BF16, 64>(p, stream) : start<BF16, 128>(p, stream);
+    return head_dim == 64 ? start<F16, 64>(p, stream) : start<F16, 128>(p, stream);
+}
+
+}  // namespace vts

@@ -9,10 +9,11 @@
 
 A cache is a 4-D tensor ``[num_pages, page_size, kv_heads, head_dim]`` of any
 strides that are multiples of 8 elements (so a cache laid out heads first is
-passed as a permuted view), bfloat16 or float16.  Lengths count the drafted
-tokens, as ``next_n`` does in ``topk_varlen``.  The operators serve decoding and
-have no derivatives: their outputs carry no gradient, also of inputs that require
-one.
+passed as a permuted view), bfloat16 or float16; ``tree_attention`` also takes
+microscaled caches of uint8 rows with their scales (``varlen_top_select_amd.cache``).
+Lengths count the drafted tokens, as ``next_n`` does in ``topk_varlen``.  The operators
+serve decoding and have no derivatives: their outputs carry no gradient, also of
+inputs that require one.
 
 Without ``workspace`` the calls share one per device and stream, made at the first
 eager call and held until the process ends, also where a larger shape has
@@ -37,6 +38,7 @@ __all__ = ["tree_attention", "attention_weight_add", "evict_cache", "verify_draf
 
 _CACHE = struct.Struct("@QQqqqqqqQqqQqiiiii4x")  # vts_paged_cache
 _STRIDES = struct.Struct("@qqq")
+_SCALES = struct.Struct("@QQqqqqqqi4x")  # vts_microscales
 MAX_DRAFT = 64
 
 
@@ -73,9 +75,13 @@ def _workspace(workspace, need, device, sp):
 
 
 @functools.lru_cache(maxsize=256)
-def tree_attention_workspace_bytes(batch, draft, heads, kv_heads, head_dim, top_k=0):
-    """Bytes of a workspace (zeroed once) for tree_attention calls of this shape."""
-    return library().vts_tree_attention_workspace_bytes(batch, draft, heads, kv_heads, head_dim, top_k)
+def tree_attention_workspace_bytes(batch, draft, heads, kv_heads, head_dim, top_k=0, microscaled=False):
+    """Bytes of a workspace (zeroed once) for tree_attention calls of this shape, over
+    16-bit or (8 and 4 bits) microscaled caches."""
+    lib = library()
+    f = (lib.vts_tree_attention_microscaled_workspace_bytes if microscaled
+         else lib.vts_tree_attention_workspace_bytes)
+    return f(batch, draft, heads, kv_heads, head_dim, top_k)
 
 
 @functools.lru_cache(maxsize=256)
@@ -84,14 +90,15 @@ def verify_draft_workspace_bytes(batch, vocab):
     return library().vts_verify_draft_workspace_bytes(batch, vocab)
 
 
-def _steps(t):
+def _steps(t, low=7):
     """The strides of a 4-D tensor's first three dimensions (0 where a dimension has one
-    element, whose stride means nothing), or None where its rows are no aligned vectors."""
+    element, whose stride means nothing), or None where its rows are no aligned vectors
+    of low + 1 elements."""
     a, b, c, d = t.stride()
-    if (a | b | c) & 7 or d != 1:
+    if (a | b | c) & low or d != 1:
         n = t.shape
         a, b, c = a if n[0] > 1 else 0, b if n[1] > 1 else 0, c if n[2] > 1 else 0
-        if (a | b | c) & 7 or d != 1:
+        if (a | b | c) & low or d != 1:
             return None
     return a, b, c
 
@@ -133,6 +140,58 @@ def _table(name, t, batch, index):
             or (step := _row_step(t, batch)) is None):
         raise ValueError(f"{name} must be an int32 tensor of {batch} contiguous rows on cuda:{index}")
     return step
+
+
+def _rows(name, t, low, index):
+    """The strides of a microscaled cache's tensor, or of its scales."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 4 or t.dtype is not torch.uint8 or t.get_device() != index:
+        raise ValueError(f"{name} must be a 4-D uint8 tensor on cuda:{index}")
+    steps = _steps(t, low)
+    if steps is None or t.data_ptr() & low:
+        raise ValueError(f"{name} rows must be contiguous, with an address and strides that are multiples "
+                         f"of {low + 1} bytes")
+    return steps
+
+
+def _micro(k_cache, v_cache, k_scales, v_scales):
+    """(the caches' strides, vts_microscales as bytes, device index, head_dim)"""
+    if k_scales is None or v_scales is None:
+        raise ValueError("k_scales and v_scales must be given together")
+    if not isinstance(k_cache, torch.Tensor) or not k_cache.is_cuda:
+        raise ValueError("k_cache must be on the GPU")
+    index = k_cache.get_device()
+    ks, vs = _rows("k_cache", k_cache, 15, index), _rows("v_cache", v_cache, 15, index)
+    if not isinstance(k_scales, torch.Tensor) or k_scales.dim() != 4 or k_scales.shape[3] not in (2, 4):
+        raise ValueError("k_scales must be a 4-D tensor [pages, page_size, kv_heads, head_dim / 32] of "
+                         "head_dim 64 or 128")
+    head_dim = 32 * k_scales.shape[3]
+    kss = _rows("k_scales", k_scales, head_dim // 32 - 1, index)
+    vss = _rows("v_scales", v_scales, head_dim // 32 - 1, index)
+    if v_cache.shape != k_cache.shape or v_scales.shape != k_scales.shape:
+        raise ValueError("v_cache and v_scales must have the shapes of k_cache and k_scales")
+    if k_cache.shape[:3] != k_scales.shape[:3] or k_cache.shape[3] not in (head_dim, head_dim // 2):
+        raise ValueError("a microscaled cache's rows must be head_dim (8 bits) or head_dim / 2 (4 bits) bytes, "
+                         "and its scales [pages, page_size, kv_heads, head_dim / 32]")
+    bits = 8 * k_cache.shape[3] // head_dim
+    packed = _SCALES.pack(k_scales.data_ptr(), v_scales.data_ptr(), *kss, *vss, bits)
+    return ks, vs, packed, index, head_dim
+
+
+def _paged_micro(k_cache, v_cache, k_scales, v_scales, page_table, seq_lens, dtype):
+    """_paged of a microscaled cache, and its vts_microscales as bytes"""
+    ks, vs, scales, index, head_dim = _micro(k_cache, v_cache, k_scales, v_scales)
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise ValueError("q dtype must be bfloat16 or float16")
+    pages, page_size, kv_heads, _ = k_cache.shape
+    if not isinstance(seq_lens, torch.Tensor) or seq_lens.dim() != 1:
+        raise ValueError("seq_lens must be a 1-D tensor")
+    batch = seq_lens.shape[0]
+    _tensor("seq_lens", seq_lens, torch.int32, (batch,), index)
+    stride = _table("page_table", page_table, batch, index)
+    packed = _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), *ks, *vs, page_table.data_ptr(), stride,
+                         page_table.shape[1], seq_lens.data_ptr(), pages, page_size, kv_heads,
+                         head_dim, batch, _DTYPE[dtype])
+    return packed, scales, index, batch, kv_heads, head_dim
 
 
 def _paged(k_cache, v_cache, page_table, seq_lens):
@@ -180,11 +239,11 @@ def _meets(out, t):
     return within(t.data_ptr(), 0)
 
 
-def _query(q, k_cache, batch, kv_heads, head_dim, index):
+def _query(q, dtype, batch, kv_heads, head_dim, index):
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be a 4-D tensor [batch, draft, heads, head_dim]")
     n, draft, heads, dim = q.shape
-    if q.dtype is not k_cache.dtype or q.get_device() != index or n != batch or dim != head_dim:
+    if q.dtype is not dtype or q.get_device() != index or n != batch or dim != head_dim:
         raise ValueError("q must have the cache's dtype, device and head_dim, and the batch of "
                          "seq_lens")
     if not 1 <= draft <= MAX_DRAFT:
@@ -202,13 +261,24 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
                    page_table: torch.Tensor, seq_lens: torch.Tensor, *,
                    tree_mask: torch.Tensor | None = None, slots: torch.Tensor | None = None,
                    scale: float | None = None, out: torch.Tensor | None = None,
-                   return_lse: bool = False, workspace: torch.Tensor | None = None, stream=None):
+                   return_lse: bool = False, workspace: torch.Tensor | None = None, stream=None,
+                   k_scales: torch.Tensor | None = None, v_scales: torch.Tensor | None = None):
     """Attention of q[batch, draft, heads, head_dim] over each request's cached
     prefix (or the listed ``slots``) and the drafted tokens that ``tree_mask``
     names (vts_tree_attention in include/vts.h).  Returns the outputs, in ``out`` if
-    given, which must not overlap q or the caches, and the rows' log-sum-exp or None."""
-    cache, index, batch, kv_heads, head_dim = _paged(k_cache, v_cache, page_table, seq_lens)
-    draft, heads, q_strides = _query(q, k_cache, batch, kv_heads, head_dim, index)
+    given, which must not overlap q or the caches, and the rows' log-sum-exp or None.
+    With ``k_scales`` and ``v_scales`` the caches are microscaled: uint8 rows of
+    head_dim (8 bits) or head_dim / 2 bytes (4 bits), and uint8 scales [pages, page_size,
+    kv_heads, head_dim / 32]; q is then bfloat16 or float16."""
+    micro = k_scales is not None or v_scales is not None
+    if micro:
+        if not isinstance(q, torch.Tensor):
+            raise ValueError("q must be a 4-D tensor [batch, draft, heads, head_dim]")
+        cache, scales, index, batch, kv_heads, head_dim = _paged_micro(
+            k_cache, v_cache, k_scales, v_scales, page_table, seq_lens, q.dtype)
+    else:
+        cache, index, batch, kv_heads, head_dim = _paged(k_cache, v_cache, page_table, seq_lens)
+    draft, heads, q_strides = _query(q, q.dtype if micro else k_cache.dtype, batch, kv_heads, head_dim, index)
     mask_ptr = slots_ptr = None
     top_k = 0
     if tree_mask is not None:
@@ -221,7 +291,7 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         slots_ptr = _tensor("slots", slots, torch.int32, shape, index).data_ptr()
     if out is not None:
         _tensor("out", out, q.dtype, (batch, draft, heads, head_dim), index)
-        if _meets(out, q) or _meets(out, k_cache) or _meets(out, v_cache):
+        if any(_meets(out, t) for t in (q, k_cache, v_cache, k_scales, v_scales) if t is not None):
             raise ValueError("out must not overlap q or the caches")
     if scale is None:
         scale = 1.0 / math.sqrt(head_dim)
@@ -232,8 +302,14 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
                         device=device) if out is None else out
         lse = torch.empty((batch, draft, heads), dtype=torch.float32,
                           device=device) if return_lse else None
-        ws = _workspace(workspace, tree_attention_workspace_bytes(batch, draft, heads, kv_heads, head_dim, top_k),
-                        device, sp)
+        ws = _workspace(workspace, tree_attention_workspace_bytes(batch, draft, heads, kv_heads, head_dim,
+                                                                  top_k, micro), device, sp)
+        if micro:
+            _check("vts_tree_attention_microscaled", lib.vts_tree_attention_microscaled(
+                cache, scales, q.data_ptr(), q_strides, draft, heads, mask_ptr, slots_ptr, top_k, scale,
+                o.data_ptr(), lse.data_ptr() if return_lse else None, ws.data_ptr(),
+                ws.numel() * ws.element_size(), sp))
+            return o, lse
         _check("vts_tree_attention", lib.vts_tree_attention(
             cache, q.data_ptr(), q_strides, draft, heads, mask_ptr, slots_ptr, top_k, scale,
             o.data_ptr(), lse.data_ptr() if return_lse else None, ws.data_ptr(),
@@ -261,7 +337,7 @@ def attention_weight_add(weights: torch.Tensor, q: torch.Tensor, k_cache: torch.
     entry got from the rows of q that ``row_keep`` counts; lse as
     tree_attention returned it (vts_attention_weight_add in include/vts.h)."""
     cache, index, batch, kv_heads, head_dim = _paged(k_cache, None, page_table, seq_lens)
-    draft, heads, q_strides = _query(q, k_cache, batch, kv_heads, head_dim, index)
+    draft, heads, q_strides = _query(q, k_cache.dtype, batch, kv_heads, head_dim, index)
     wb, wh, width = _weights("weights", weights, batch, kv_heads, index)
     if (batch > 1 and wb < width) or (kv_heads > 1 and wh < width):
         raise ValueError("weights rows must not overlap")
@@ -401,6 +477,11 @@ def declare(lib):
     lib.vts_tree_attention_workspace_bytes.argtypes = [i32] * 6
     lib.vts_tree_attention.restype = ctypes.c_int
     lib.vts_tree_attention.argtypes = [vp, vp, vp, i32, i32, vp, vp, i32, f32, vp, vp, vp, sz, vp]
+    lib.vts_tree_attention_microscaled_workspace_bytes.restype = sz
+    lib.vts_tree_attention_microscaled_workspace_bytes.argtypes = [i32] * 6
+    lib.vts_tree_attention_microscaled.restype = ctypes.c_int
+    lib.vts_tree_attention_microscaled.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, i32, f32, vp, vp, vp,
+                                                   sz, vp]
     lib.vts_attention_weight_add.restype = ctypes.c_int
     lib.vts_attention_weight_add.argtypes = [vp, vp, vp, i32, i32, vp, vp, vp, f32, vp, i64, i64,
                                              i64, vp]
