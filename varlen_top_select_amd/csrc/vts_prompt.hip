@@ -38,6 +38,7 @@ constexpr int PROMPT_KEYS = 64;  // of a tile
 template <int D>
 struct PromptShared {
     u32x4 k[2][PROMPT_KEYS * (D / 8)], v[2][PROMPT_KEYS * (D / 8)];
+    uint32_t bad;  // a masked tile's V holds something that is not finite
 };
 
 // A workgroup's tile: its sequence, the first of its rows, and the lengths.
@@ -240,12 +241,6 @@ struct Prompt {
                 l += x + y;
                 pv[2 * b + (e >> 3)][(e >> 1) & 3] = pack2<DT>(x, y);
             }
-        if constexpr (MASKED) {
-            if (any_not_finite(buf)) {
-                product_not_finite(j0, buf, pv);
-                return;
-            }
-        }
 #pragma unroll
         for (int step = 0; step < 4; ++step)
 #pragma unroll
@@ -253,52 +248,38 @@ struct Prompt {
     }
 
     // Where not every row sees every key, an infinity or NaN in V would reach rows that
-    // do not see it (0 * inf).  Such a tile's finite elements go through the product
-    // and the others are added to the rows that see them.
-    __device__ __forceinline__ bool any_not_finite(int buf) const {
-        bool bad = false;
-#pragma unroll 4
-        for (int x = lane; x < PROMPT_KEYS * CH; x += 64) {
-            const u32x4 w = sm.v[buf][x];
+    // do not see it (0 * inf).  Such a tile's are cleared on the way to LDS, and what rows
+    // see of them is added at the end, from memory: rare, and kept apart from the loops,
+    // whose registers it would take (45 spilled).
+    __device__ __forceinline__ void clear_not_finite() {
+        bool f = false;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) bad = bad || not_finite<DT>(w[e]);
-        }
-        return ballot(bad) != 0;
-    }
-    __device__ __forceinline__ void product_not_finite(int32_t j0, int buf, const u32x4 (&pv)[4]) {
-    #pragma unroll
-        for (int step = 0; step < 4; ++step)
-    #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                u32x4 x = operand_v(buf, step, i);
-    #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (not_finite<DT>(x[e] & 0xFFFFu)) x[e] &= 0xFFFF0000u;
-                    if (not_finite<DT>(x[e] >> 16)) x[e] &= 0xFFFFu;
-                }
-                o[i] = mfma32<DT>(x, pv[step], o[i]);
+        for (int i = 0; i < LOADS; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t w = vr[i][e];
+                f = f || not_finite<DT>(w);
+                vr[i][e] = (not_finite<DT>(w & 0xFFFFu) ? 0 : w & 0xFFFFu) |
+                           (not_finite<DT>(w >> 16) ? 0 : w & 0xFFFF0000u);
             }
-    #pragma unroll 1
-        for (int key = 0; key < PROMPT_KEYS; ++key) {
-            // the key's weight for this lane's row lies in the lane of one half
-            uint32_t pair = 0;
-    #pragma unroll
-            for (int step = 0; step < 4; ++step)
-    #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    // word e of a step holds keys 16 step + 8 (e / 2) + 4 half + 2 (e % 2) + {0, 1}
-                    pair = (key >> 4) == step && ((key >> 3) & 1) * 2 + ((key >> 1) & 1) == e ? pv[step][e] : pair;
-            pair = from_lane(pair, ((key >> 2) & 1) * 32 + col);
-            const float w = to_float<DT>((pair >> (16 * (key & 1))) & 0xFFFFu);
-            const bool see = j0 + key <= limit;
-    #pragma unroll
+        if (f) sm.bad = 1;
+    }
+    __device__ __forceinline__ void add_not_finite(int32_t j0, int32_t end) {
+#pragma unroll 1
+        for (int32_t j = j0; j < end; ++j) {
+            const char* at = (const char*)p.v + 2 * ((int64_t)(t.k0 + j) * p.v_token + kv * p.v_head);
+            const bool see = j <= limit;
+#pragma unroll
             for (int i = 0; i < MT; ++i)
-    #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int d = 32 * i + key_of(e) + 4 * half;
-                    const uint32_t raw = ((const uint16_t*)&sm.v[buf][v_at(key, d / 8)])[d % 8];
-                    const float y = o[i][e] + w * to_float<DT>(raw);
-                    o[i][e] = see && not_finite<DT>(raw) ? y : o[i][e];
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    const u32x2 four = gload((const u32x2*)(at + 2 * (32 * i + key_of(e) + 4 * half)));
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const uint32_t raw = (four[x >> 1] >> (16 * (x & 1))) & 0xFFFFu;
+                        const float y = o[i][e + x] + to_float<DT>(raw);
+                        o[i][e + x] = see && not_finite<DT>(raw) ? y : o[i][e + x];
+                    }
                 }
         }
     }
@@ -325,7 +306,9 @@ struct Prompt {
     }
 
     // the tile at j0 to LDS, and the next one on its way
+    template <bool MASKED>
     __device__ __forceinline__ void next(int32_t j0, int32_t end, int buf) {
+        if constexpr (MASKED) clear_not_finite();
         // the other half may still be read; this one was done with before the last barrier
         stage(buf);
         if (j0 + PROMPT_KEYS < end) load(j0 + PROMPT_KEYS);
@@ -339,25 +322,30 @@ struct Prompt {
         const int32_t all = !p.causal ? t.lk : t.row0 / p.group + 1 + t.lk - t.lq;
         if (end > 0) {
             load(0);
+            if (tid == 0) sm.bad = 0;
+            __syncthreads();
             int32_t j0 = 0;
             int buf = 0;
 #pragma unroll 1
             for (; j0 + PROMPT_KEYS <= all; j0 += PROMPT_KEYS, buf ^= 1) {
-                next(j0, end, buf);
+                next<false>(j0, end, buf);
                 tile<false>(j0, buf);
             }
+            const int32_t first = j0;
 #pragma unroll 1
             for (; j0 < end; j0 += PROMPT_KEYS, buf ^= 1) {
-                next(j0, end, buf);
+                next<true>(j0, end, buf);
                 tile<true>(j0, buf);
             }
+            __syncthreads();
+            if (sm.bad) add_not_finite(first, end);
         }
         write();
     }
 };
 
 template <int DT, int D>
-__global__ __launch_bounds__(PROMPT_NT, 1) void prompt_kernel(PromptParams p) {
+__global__ __launch_bounds__(PROMPT_NT, 2) void prompt_kernel(PromptParams p) {
     __shared__ PromptShared<D> sm;
     const int32_t work = p.tiles * p.kv_heads;
     if ((int32_t)blockIdx.x >= work) {
