@@ -29,6 +29,9 @@
 // an order of their own (lane group g takes the g-th quarter of a row in all steps),
 // so that a lane's quarter is one LDS load and, at head size 128, one scale.
 #pragma once
+#ifndef VTS_AHEAD
+#define VTS_AHEAD 2
+#endif
 
 #include "vts_paged.hpp"
 
@@ -80,6 +83,9 @@ struct AttendShared : AttendShape<D, MT, MODE, F> {
         // outputs of waves to be joined, padded: the 16 rows of a store fall on all banks
         float o[MODE == HEADS ? 1 : S::WIDE ? S::KG - 1 : 2][MODE == HEADS ? 1 : S::ROWS][D + 4];
     };
+    // 16 rows of a wave on their way to whole rows of a part (waves do not wait for each
+    // other, so it is no wave's tile; from 32 rows on, where its query rows were)
+    f32x4 turn[F != 16 && MODE == HEADS && MT == 1 ? WAVES : 1][16 * D / 4];
     float ml[S::KG][S::ROWS][2];
     uint32_t last;
 };
@@ -99,8 +105,9 @@ struct Attend {
     static constexpr int T = S::NW * 64;    // threads
     // whether a cache row is read once by the whole call, as far as it is known
     // (the slots of two rows may be the same): such loads leave the caches alone.
-    // 128 lists of 2048 slots, 64 heads: 112 us without, 104 with.
-    static constexpr bool ONCE = HEAD || (SLOTS && !WIDE);
+    // 128 lists of 2048 slots, 64 heads: 112 us without, 104 with.  (Microscaled rows
+    // that are no whole cache line share one with another head's.)
+    static constexpr bool ONCE = (HEAD || (SLOTS && !WIDE)) && S::RB >= 128;
     static constexpr int ROWS = S::ROWS;
     // of m, see above: how far below the maximum it is put, and when it is raised
     static constexpr float SHIFT = DT == F16 ? 11 : 0, RAISE = DT == F16 ? 15 : 8;
@@ -124,24 +131,28 @@ struct Attend {
     static constexpr int BLOCKS = D / 32;  // scales of a row
     static constexpr int HALF = S::KG * 32 * CHF;  // (wide) chunks of K in a unit, and of V
     static constexpr int LOADSF = !WIDE ? CHF / 2 : HALF >= T ? 2 * HALF / T : 1;
+    // Microscaled tiles on their way to a wave: with one of 4 KB a wave waits for memory most
+    // of the time; more do not fit the registers.
+    static constexpr int AHEAD = !MICRO || WIDE ? 1 : MT == 1 || D == 64 ? VTS_AHEAD : 1;
     using Scales = typename std::conditional<D == 128, uint32_t, uint16_t>::type;
     u32x4 q[QL ? 1 : KS];
     uint64_t bits[MT];
     f32x4 o[MT][NTILE];
     float m[MT], l[MT];
     // the tile on its way: 32 places to a wave, or the wave's rows of the unit
-    u32x4 k[MICRO ? LOADSF : WIDE ? LOADS : 2 * KS];
+    u32x4 k[MICRO ? LOADSF * AHEAD : WIDE ? LOADS : 2 * KS];
     VRow v[8];
-    u32x4 vw[MICRO ? LOADSF : LOADS];
+    u32x4 vw[MICRO ? LOADSF * AHEAD : LOADS];
     const void* kbase;
     const void* vbase;
     // Microscaled: the scales on their way (K's of place l in lane l, V's in lane
     // 32 + l; wide: of the thread's chunks) and of the tile at hand
-    uint32_t sc_next[WIDE ? LOADSF : 1], sc;
+    uint32_t sc_next[WIDE ? LOADSF : AHEAD], sc;
     bool here[WIDE ? LOADSF : 1];  // (wide) whether the chunks' places are there
     // of the scales: K's in lanes 0..31, V's above
     const char* sbase;
     uint32_t scale_page, scale_pos;
+    bool cleared;  // something that is not finite was taken out of a tile's V
 
     __device__ Attend(const AttendParams& p_, AttendShared<D, MT, MODE, F>& s_, int32_t mb_)
         : p(p_), sm(s_), mb(mb_) {
@@ -327,28 +338,28 @@ struct Attend {
     }
     // The rows of a wave's tile, as they lie in memory, and their scales: K's of
     // place l in lane l, V's in lane 32 + l, one load for both.
-    __device__ __forceinline__ void load_micro(uint32_t off, uint32_t soff) {
+    __device__ __forceinline__ void load_micro(int to, uint32_t off, uint32_t soff) {
         const uint32_t safe = off == NO_PLACE ? 0 : off;
 #pragma unroll
         for (int i = 0; i < LOADSF; ++i) {
             const int r = i * (64 / CHF) + lane / CHF;
-            k[i] = row_load<u32x4, ONCE>(kbase, from_lane(safe, r), (lane % CHF) * 16);
-            vw[i] = row_load<u32x4, ONCE>(vbase, from_lane(safe, 32 + r), (lane % CHF) * 16);
+            k[to * LOADSF + i] = row_load<u32x4, ONCE>(kbase, from_lane(safe, r), (lane % CHF) * 16);
+            vw[to * LOADSF + i] = row_load<u32x4, ONCE>(vbase, from_lane(safe, 32 + r), (lane % CHF) * 16);
         }
-        sc_next[0] = *(const VTS_GLOBAL Scales*)((const VTS_GLOBAL char*)sbase +
+        sc_next[to] = *(const VTS_GLOBAL Scales*)((const VTS_GLOBAL char*)sbase +
                                                  (uint64_t)(soff == NO_PLACE ? 0 : soff) * BLOCKS);
     }
     __device__ __forceinline__ char* packed_row(int which, int r) const {
         return (char*)sm.packed[wave] + (which * 32 + r) * PAD;
     }
-    __device__ __forceinline__ void stage_micro() {
+    __device__ __forceinline__ void stage_micro(int from) {
 #pragma unroll
         for (int i = 0; i < LOADSF; ++i) {
             const int r = i * (64 / CHF) + lane / CHF;
-            *(u32x4*)(packed_row(0, r) + (lane % CHF) * 16) = k[i];
-            *(u32x4*)(packed_row(1, r) + (lane % CHF) * 16) = vw[i];
+            *(u32x4*)(packed_row(0, r) + (lane % CHF) * 16) = k[from * LOADSF + i];
+            *(u32x4*)(packed_row(1, r) + (lane % CHF) * 16) = vw[from * LOADSF + i];
         }
-        sc = sc_next[0];
+        sc = sc_next[from];
         // the wave's own stores come before its loads; the compiler has to know
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
@@ -364,26 +375,115 @@ struct Attend {
         for (int s = 0; s < KS; ++s)
             x[s] = F == 4 ? widen(w[s], 0, scale) : widen(w[(2 * s) % WORDS], w[(2 * s + 1) % WORDS], scale);
     }
-    // the lane's part `part` of V's row `place`
-    __device__ __forceinline__ VRow micro_v(int place, int part) const {
-        constexpr int B = RB / 16;  // bytes of a part
-        const char* at = packed_row(1, place) + part * B;
-        const float scale = scale_at(from_lane(sc, 32 + place), part / (16 / BLOCKS));
-        VRow y;
-        if constexpr (D == 128) {
-            uint32_t w[2] = {0, 0};
-            __builtin_memcpy(w, __builtin_assume_aligned(at, B), B);
-            y = widen(w[0], w[1], scale);
-        } else if constexpr (F == 4) {
-            const uint32_t w = *(const uint16_t*)at;
-            y[0] = widen4<DT, 0>(w, scale);
-            y[1] = widen4<DT, 1>(w, scale);
-        } else {
-            const uint32_t w = *(const uint32_t*)at;
-            y[0] = widen8<DT, false>(w, scale);
-            y[1] = widen8<DT, true>(w, scale);
+    // second_product over V as it is stored: word by word of the lane's elements, so that
+    // few converted ones are held at a time.
+    __device__ __forceinline__ void micro_product(uint32_t have, bool masked, bool drafted,
+                                                  const u32x4 (&pv)[MT]) {
+        constexpr int B = RB / 16;  // bytes of the lane's part of a row
+        uint32_t raw[8][B == 8 ? 2 : 1];
+        float scale[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const char* at = packed_row(1, v_place(j)) + col * B;
+            if constexpr (B == 2)
+                raw[j][0] = *(const uint16_t*)at;
+            else
+                __builtin_memcpy(raw[j], __builtin_assume_aligned(at, B), B);
+            scale[j] = scale_at(from_lane(sc, 32 + v_place(j)), col / (16 / BLOCKS));
         }
-        return y;
+        if (masked) {
+            int g = grp;
+            asm volatile("" : "+v"(g));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t there = (have >> ((j >> 2) * 16 + g * 4 + (j & 3))) & 1u;
+#pragma unroll
+                for (int w = 0; w < (B == 8 ? 2 : 1); ++w) raw[j][w] = there ? raw[j][w] : 0;
+                scale[j] = there ? scale[j] : 1.0f;
+            }
+        }
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+            uint32_t x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if constexpr (F == 4)
+                    x[j] = w == 0   ? widen4<DT, 0>(raw[j][0], scale[j])
+                           : w == 1 ? widen4<DT, 1>(raw[j][0], scale[j])
+                           : w == 2 ? widen4<DT, 2>(raw[j][0], scale[j])
+                                    : widen4<DT, 3>(raw[j][0], scale[j]);
+                else
+                    x[j] = w & 1 ? widen8<DT, true>(raw[j][w / 2], scale[j])
+                                 : widen8<DT, false>(raw[j][w / 2], scale[j]);
+            }
+            if (drafted) {  // see clear_not_finite
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (ballot(not_finite<DT>(x[j])) == 0) continue;
+                    cleared = true;
+                    if (not_finite<DT>(x[j] & 0xFFFFu)) x[j] &= 0xFFFF0000u;
+                    if (not_finite<DT>(x[j] >> 16)) x[j] &= 0xFFFFu;
+                }
+            }
+            u32x4 lo, hi;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                lo[j] = __builtin_amdgcn_perm(x[2 * j + 1], x[2 * j], 0x05040100u);
+                hi[j] = __builtin_amdgcn_perm(x[2 * j + 1], x[2 * j], 0x07060302u);
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                o[mt][2 * w] = mfma<DT>(lo, pv[mt], o[mt][2 * w]);
+                o[mt][2 * w + 1] = mfma<DT>(hi, pv[mt], o[mt][2 * w + 1]);
+            }
+        }
+    }
+    // What micro_product cleared in this wave's tiles of units [u0, u1), from memory to the
+    // rows that see it: rare, and apart from the walk, whose registers it would take.
+    __device__ __forceinline__ void add_cleared(int32_t u0, int32_t u1) {
+        fresh();
+#pragma unroll 1
+        for (int32_t u = u0; u < u1; ++u) {
+            if (first_place(u) + 31 < pl.first) continue;
+#pragma unroll 1
+            for (int kk = 0; kk < 32; ++kk) {
+                const int32_t i = first_place(u) + kk - pl.first;
+                if (i < 0) continue;
+                const Entry e = issue_entry<SLOTS>(p.c, pl, first_place(u) + kk);
+                const uint32_t off = resolve_entry<SLOTS>(p.c, p.c.v.page_stride, p.c.v.pos_stride, e);
+                if (off == NO_PLACE) continue;
+                const uint32_t soff = resolve_entry<SLOTS>(p.c, p.v_scale.page_stride, p.v_scale.pos_stride, e);
+                const int32_t h = HEAD ? head_unit * WAVES + wave : head_unit;
+                const uint8_t* codes = p.v_scale.base + ((uint64_t)soff + (uint64_t)h * p.v_scale.head_stride) * BLOCKS;
+#pragma unroll
+                for (int e4 = 0; e4 < 4; ++e4) {
+                    constexpr int B = RB / 16;
+                    const int part = grp * 4 + e4;
+                    const float scale = scale_of(gload(codes + part / (16 / BLOCKS)));
+                    uint32_t w[2] = {0, 0};
+                    const VTS_GLOBAL char* at =
+                        (const VTS_GLOBAL char*)vbase + ((uint64_t)off << 4) + part * B;
+                    if constexpr (B == 2) {
+                        w[0] = *(const VTS_GLOBAL uint16_t*)at;
+                    } else {
+                        w[0] = *(const VTS_GLOBAL uint32_t*)at;
+                        if constexpr (B == 8) w[1] = *(const VTS_GLOBAL uint32_t*)(at + 4);
+                    }
+                    const u32x4 x = widen(w[0], w[1], scale);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const bool see = (bits[mt] >> (i & 63)) & 1;
+#pragma unroll
+                        for (int n = 0; n < NTILE; ++n) {
+                            const uint32_t half = (x[n >> 1] >> (16 * (n & 1))) & 0xFFFFu;
+                            const float y = o[mt][n][e4] + to_float<DT>(half);
+                            o[mt][n][e4] = see && not_finite<DT>(half) ? y : o[mt][n][e4];
+                        }
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        }
     }
     // Wide: the thread's chunks of a unit.  PAIRS of the same place and number of K and of V,
     // or, where the unit's K has fewer chunks than there are threads, one of K or of V.
@@ -510,14 +610,12 @@ struct Attend {
         while (bad) {
             const int kk = __builtin_ctz(bad);
             bad &= bad - 1;
-            const uint32_t r = WIDE || MICRO ? 0 : from_lane(off, 32 + kk);
+            const uint32_t r = WIDE ? 0 : from_lane(off, 32 + kk);
             VRow x[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 if constexpr (WIDE)
                     x[e] = wide_v(buf, kk, grp * 4 + e);
-                else if constexpr (MICRO)
-                    x[e] = micro_v(kk, grp * 4 + e);
                 else
                     x[e] = row_load<VRow>(vbase, r, (grp * 4 + e) * VB);
             }
@@ -549,13 +647,10 @@ struct Attend {
     // as soon as this tile's are used up, and its V rows after the second
     // product, so one of the two is always on its way.
     __device__ __forceinline__ void tile(uint32_t have, bool drafted, uint32_t off, int32_t j0,
-                                         bool more, uint32_t off_next, uint32_t soff_next, int buf) {
+                                         bool more, uint32_t off_next, int buf) {
         const float c = p.scale_log2e;
         const bool masked = have != ~0u || drafted;
-        if constexpr (MICRO && !WIDE) {
-            stage_micro();
-            if (more) load_micro(off_next, soff_next);
-        } else if constexpr (!WIDE) {
+        if constexpr (!MICRO && !WIDE) {
             stage_k();
             if (more) load_k(off_next);
         }
@@ -564,23 +659,23 @@ struct Attend {
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) s[mt][h] = f32x4{0, 0, 0, 0};
-        u32x4 kx[MICRO && !WIDE ? 2 : 1][KS];
-        if constexpr (MICRO && !WIDE) {
-            micro_k(0, kx[0]);
-            micro_k(1, kx[1]);
+        if constexpr (PERMUTED) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                u32x4 kx[KS];
+                micro_k(h, kx);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+                        s[mt][h] = mfma<DT>(kx[ks], QL ? sm.q[q_at(mt, ks)][lane] : q[QL ? 0 : ks], s[mt][h]);
+            }
         }
         // step by step over all rows, so that independent products stand between
         // dependent ones
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            u32x4 k0, k1;
-            if constexpr (MICRO && !WIDE) {
-                k0 = kx[0][ks];
-                k1 = kx[1][ks];
-            } else {
-                k0 = operand_k(0, ks, buf);
-                k1 = operand_k(1, ks, buf);
-            }
+        for (int ks = 0; ks < (PERMUTED ? 0 : KS); ++ks) {
+            const u32x4 k0 = operand_k(0, ks, buf), k1 = operand_k(1, ks, buf);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 const u32x4 qq = QL ? sm.q[q_at(mt, ks)][lane] : q[QL ? 0 : ks];
@@ -646,11 +741,10 @@ struct Attend {
         if constexpr (WIDE)
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = wide_v(buf, v_place(j), col);
-        else if constexpr (MICRO)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = micro_v(v_place(j), col);
         uint32_t bad = 0;
-        if (masked) {
+        if constexpr (PERMUTED) {
+            micro_product(have, masked, drafted, pv);
+        } else if (masked) {
             int g = grp;
             asm volatile("" : "+v"(g));
 #pragma unroll
@@ -661,8 +755,9 @@ struct Attend {
             }
             if (drafted) bad = clear_not_finite();
         }
-        second_product(pv);
-        if (bad) add_rows(bad, off, j0, buf, pv);
+        if constexpr (!PERMUTED) second_product(pv);
+        if constexpr (!PERMUTED)
+            if (bad) add_rows(bad, off, j0, buf, pv);
         if constexpr (!WIDE) {
             if constexpr (!MICRO)
                 if (more) load_v(off_next);
@@ -676,18 +771,16 @@ struct Attend {
         fresh();
         page_stride = lane < 32 ? p.c.k.page_stride : p.c.v.page_stride;
         pos_stride = lane < 32 ? p.c.k.pos_stride : p.c.v.pos_stride;
-        if constexpr (MICRO && WIDE) {
-            walk_wide_micro(u0, u1);
+        if constexpr (MICRO) {
+            if constexpr (WIDE)
+                walk_wide_micro(u0, u1);
+            else
+                walk_micro(u0, u1);
             return;
         }
-        Entry first = issue(u0);
-        uint32_t off = resolve(first), soff_next = 0;
+        uint32_t off = resolve(issue(u0));
         Entry next = issue(u0 + 1);
-        if constexpr (MICRO) {
-            scale_page = lane < 32 ? p.k_scale.page_stride : p.v_scale.page_stride;
-            scale_pos = lane < 32 ? p.k_scale.pos_stride : p.v_scale.pos_stride;
-            load_micro(off, resolve_entry<SLOTS>(p.c, scale_page, scale_pos, first));
-        } else if constexpr (WIDE) {
+        if constexpr (WIDE) {
             load_wide(off);
         } else {
             load_k(off);
@@ -710,17 +803,47 @@ struct Attend {
                 have = (uint32_t)ballot(sm.w.there[buf][kg * 32 + (lane & 31)]);
             } else {
                 off_next = resolve(next);
-                if constexpr (MICRO)
-                    soff_next = resolve_entry<SLOTS>(p.c, scale_page, scale_pos, next);
                 next = issue(u + 2);
                 have = (uint32_t)ballot(off != NO_PLACE);
             }
             const bool drafted = j0 + 31 >= pl.first;
-            tile(have, drafted, off, j0, u + 1 < u1, off_next, soff_next, buf);
+            tile(have, drafted, off, j0, u + 1 < u1, off_next, buf);
             off = off_next;
         }
     }
-    // The same of a wide workgroup over a microscaled cache.
+    // The same over a microscaled cache, AHEAD tiles on their way.
+    __device__ __forceinline__ void walk_micro(int32_t u0, int32_t u1) {
+        cleared = false;
+        scale_page = lane < 32 ? p.k_scale.page_stride : p.v_scale.page_stride;
+        scale_pos = lane < 32 ? p.k_scale.pos_stride : p.v_scale.pos_stride;
+        uint32_t off[AHEAD];
+        Entry e[AHEAD + 1];
+#pragma unroll
+        for (int i = 0; i <= AHEAD; ++i) e[i] = issue(u0 + i);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            off[i] = resolve(e[i]);
+            load_micro(i, off[i], resolve_entry<SLOTS>(p.c, scale_page, scale_pos, e[i]));
+        }
+        Entry next = e[AHEAD];
+#pragma unroll 1
+        for (int32_t u = u0; u < u1; u += AHEAD) {
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                if (u + i >= u1) break;
+                const int32_t j0 = first_place(u + i);
+                const uint32_t have = (uint32_t)ballot(off[i] != NO_PLACE);
+                stage_micro(i);
+                off[i] = resolve(next);
+                if (u + i + AHEAD < u1)
+                    load_micro(i, off[i], resolve_entry<SLOTS>(p.c, scale_page, scale_pos, next));
+                next = issue(u + i + AHEAD + 1);
+                tile(have, j0 + 31 >= pl.first, 0, j0, false, 0, 0);
+            }
+        }
+        if (cleared) add_cleared(u0, u1);
+    }
+    // A wide workgroup's.
     __device__ __forceinline__ void walk_wide_micro(int32_t u0, int32_t u1) {
         load_wide_micro(u0);
 #pragma unroll 1
@@ -731,7 +854,7 @@ struct Attend {
             if (u + 1 < u1) load_wide_micro(u + 1);
             __syncthreads();
             const uint32_t have = (uint32_t)ballot(sm.w.there[buf][kg * 32 + (lane & 31)]);
-            tile(have, j0 + 31 >= pl.first, 0, j0, false, 0, 0, buf);
+            tile(have, j0 + 31 >= pl.first, 0, j0, false, 0, buf);
         }
     }
 
@@ -881,6 +1004,12 @@ struct Attend {
         }
     }
 
+    // four outputs of row r on their way, in an order that spreads a column over the banks
+    __device__ __forceinline__ f32x4& turned(int r, int c) const {
+        f32x4* base = MT == 1 ? sm.turn[MT == 1 ? wave : 0] : (f32x4*)sm.q[MT == 1 ? 0 : wave * MT * KS];
+        return base[r * (D / 4) + (c ^ r)];
+    }
+
     // Whether parts are stored through to memory.  A release fence writes all of
     // the XCD's L2 back, about 4 us in which the joiner waits: one list of 4096
     // takes 14.8 us without it for 18, 16 of 1024 25 for 32.  Parts of many rows
@@ -888,7 +1017,7 @@ struct Attend {
     // of up to 16384 with 16 rows of four heads take 486 us for 456, 8 lists
     // with 128 rows 408 for 385.
     __device__ __forceinline__ bool through() const {
-        return MODE == KEYS || (HEAD && MT == 1 && p.rows <= 8);
+        return MODE == KEYS || (HEAD && (MICRO || (MT == 1 && p.rows <= 8)));
     }
     template <typename V>
     __device__ __forceinline__ void pstore(V* a, V v) const {
@@ -916,7 +1045,28 @@ struct Attend {
                                                 bool w0_whole_start) {
         float* po = p.part_o + mine * (ROWS * D);
         float* pm = p.part_ml + mine * (ROWS * 2);
-        if constexpr (HEAD || WIDE) {
+        if constexpr (HEAD && MICRO) {
+            close();
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+                for (int i = 0; i < NTILE; ++i) turned(col, grp * NTILE + i) = four(mt, i);
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+                const int r0 = mt * 16, at = wave * 16 * MT + r0;
+                for (int x = lane * 4; x < 16 * D; x += 256)
+                    if (r0 + x / D < p.rows)
+                        pstore((f32x4*)(po + at * D + x), turned(x / D, x % D / 4));
+                if (grp == 0 && r0 + col < p.rows) {
+                    pstore(pm + (at + col) * 2, m[mt]);
+                    pstore(pm + (at + col) * 2 + 1, l[mt]);
+                }
+                // the next rows' stores come after these loads
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+            }
+        } else if constexpr (HEAD || WIDE) {
             if (own_rows())
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
@@ -1105,7 +1255,9 @@ __global__ __launch_bounds__(threads_of(MODE), MODE >= WIDE2 || F != 16 ? 2 : 1)
         sh.b = (int32_t)(sh.begin / each);
         sh.b_unit = sh.b * each;
     } else {
-        sh = dense_share<PLACES, HEAD>(p.c, p.workers, w);
+        // (four heads' parts: 64 requests up to 1024 over a 4-bit cache XX us with shares of any
+        // size, YY with these)
+        sh = dense_share<PLACES, HEAD, HEAD && F != 16 ? 12 : 1>(p.c, p.workers, w);
         if (w >= sh.workers) return;
     }
     Attend<DT, D, MT, SLOTS, MODE, F> a(p, sm, mb);

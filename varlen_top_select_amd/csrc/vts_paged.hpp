@@ -208,9 +208,10 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
     return (int64_t)(((uint64_t)hi << 32) | lo);
 }
 
-// Shares over the batch's dense lengths.  Every wave finds the same by itself,
-// four requests to a lane and 256 at a time.
-template <int PLACES, bool HEADS>
+// Shares over the batch's dense lengths; with LEAST, of that many units where this leaves
+// 256 of them or more.  Every wave finds the same by itself, four requests to a lane and 256
+// at a time.
+template <int PLACES, bool HEADS, int LEAST = 1>
 __device__ __forceinline__ Share dense_share(const PagedParams& c, int32_t workers, int32_t w) {
     constexpr int PER = 4, STEP = 64 * PER;
     const int32_t heads = head_units<HEADS>(c);
@@ -241,7 +242,9 @@ __device__ __forceinline__ Share dense_share(const PagedParams& c, int32_t worke
         inc = scan(b0, all);
         s.total += all;
     }
-    s.workers = s.total < workers ? (int32_t)s.total : workers;
+    int64_t most = s.total;
+    if (LEAST > 1 && most > 256) most = most / LEAST > 256 ? most / LEAST : 256;
+    s.workers = most < workers ? (int32_t)most : workers;
     s.begin = s.end = s.b_unit = 0;
     s.b = 0;
     if (w >= s.workers) return s;
