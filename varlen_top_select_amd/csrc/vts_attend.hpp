@@ -29,9 +29,6 @@
 // an order of their own (lane group g takes the g-th quarter of a row in all steps),
 // so that a lane's quarter is one LDS load and, at head size 128, one scale.
 #pragma once
-#ifndef VTS_AHEAD
-#define VTS_AHEAD 2
-#endif
 
 #include "vts_paged.hpp"
 
@@ -133,7 +130,7 @@ struct Attend {
     static constexpr int LOADSF = !WIDE ? CHF / 2 : HALF >= T ? 2 * HALF / T : 1;
     // Microscaled tiles on their way to a wave: with one of 4 KB a wave waits for memory most
     // of the time; more do not fit the registers.
-    static constexpr int AHEAD = !MICRO || WIDE ? 1 : MT == 1 || D == 64 ? VTS_AHEAD : 1;
+    static constexpr int AHEAD = !MICRO || WIDE ? 1 : D == 64 || (MT == 1 && !(HEAD && SLOTS && F == 8)) ? 2 : 1;
     using Scales = typename std::conditional<D == 128, uint32_t, uint16_t>::type;
     u32x4 q[QL ? 1 : KS];
     uint64_t bits[MT];
@@ -1298,7 +1295,7 @@ static hipError_t launch_one(const AttendParams& p, hipStream_t stream) {
 
 template <int DT, int D, bool SLOTS, int F>
 static hipError_t launch_mode(const AttendParams& p, hipStream_t stream) {
-    if constexpr (!SLOTS) {
+    if constexpr (!SLOTS || F != 16) {
         if (p.heads_on_waves)
             return p.rows <= 16 ? launch_one<DT, D, 1, SLOTS, HEADS, F>(p, stream)
                                 : launch_one<DT, D, 2, SLOTS, HEADS, F>(p, stream);

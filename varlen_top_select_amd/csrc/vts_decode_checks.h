@@ -175,13 +175,16 @@ inline int attend_plan(int64_t batch, int32_t draft, int32_t heads, int32_t kv_h
     if (out->workers > MAX_TICKETS / out->row_blocks) out->workers = MAX_TICKETS / out->row_blocks;
     // A workgroup that reads whole rows of the cache, four heads of them, reads
     // faster than one that reads every kv_heads-th 256 bytes (see vts_attend.hip);
-    // more rows a head do not fit, and slots lie apart in either case.
+    // more rows a head do not fit, and slots of a 16-bit cache lie apart in either case.
+    // (Those of four heads' microscaled rows, 128 lists of 2048: 52 us for 87 with 4 bits,
+    // 78 for 87 with 8.)
     // The workgroups that share a list leave four times the parts, so not where
     // many share one.  (64 requests, 16 rows to each of 8 heads: 349 us for 369 at
     // lengths of 8192, 187 for 192 at 4096; the rule knows no lengths, and below it
     // costs, 107 us for 104 at 2048 and 68 for 52 at 1024.)
     out->heads_on_waves =
-        top_k == 0 && block <= 32 && kv_heads % 4 == 0 && batch * kv_heads >= 128;
+        (top_k == 0 || bits != 16) && block <= 32 && kv_heads % 4 == 0 &&
+        batch * kv_heads * (top_k > 0 ? draft : 1) >= 128;
     const size_t parts =
         2 * (size_t)out->workers * out->row_blocks * block * (out->heads_on_waves ? 4 : 1);
     out->part_o = TICKET_BYTES;
