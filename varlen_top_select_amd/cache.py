@@ -58,22 +58,32 @@ def _slot_cache(k_cache, v_cache, k_scales, v_scales, dtype):
     return packed, scales, index, dtype, kv_heads, head_dim
 
 
-def _heads(name, t, dtype, index, head_dim=None, tokens=None, heads=None):
-    """The strides of rows [tokens, heads, head_dim] (0 for a dimension of one)."""
+def _heads(name, t, dtype, index):
+    """The shape and the strides of rows [tokens, heads, head_dim] (0 for a dimension of one)."""
     if not isinstance(t, torch.Tensor) or t.dim() != 3:
         raise ValueError(f"{name} must be a 3-D tensor [tokens, heads, head_dim]")
     if t.dtype is not dtype or t.get_device() != index:
         raise ValueError(f"{name} must be a {dtype} tensor on cuda:{index}")
-    n, h, d = t.shape
-    if (head_dim is not None and d != head_dim or tokens is not None and n != tokens
-            or heads is not None and h != heads or h < 1):
-        raise ValueError(f"{name} must have the shape [{tokens or 'tokens'}, {heads or 'heads'}, "
-                         f"{head_dim or 'head_dim'}]")
-    a, b = t.stride(0) if n > 1 else 0, t.stride(1) if h > 1 else 0
-    if (a | b) & 7 or t.stride(2) != 1 or n and t.data_ptr() & 15:
+    n, h, d = shape = t.shape
+    a, b, c = t.stride()
+    if n <= 1:
+        a = 0
+    if h <= 1:
+        b = 0
+        if h < 1:
+            raise ValueError(f"{name} must have heads")
+    if (a | b) & 7 or c != 1 or n and t.data_ptr() & 15:
         raise ValueError(f"{name} rows must be contiguous, 16-byte aligned, with strides that are "
                          "multiples of 8 elements")
-    return a, b
+    return shape, (a, b)
+
+
+def _keys(name, t, dtype, index, shape):
+    """The strides of such rows of a shape."""
+    got, steps = _heads(name, t, dtype, index)
+    if got != shape:
+        raise ValueError(f"{name} must have the shape {shape}")
+    return steps
 
 
 def _apart(name, out, *others):
@@ -98,10 +108,11 @@ def write_cache(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slots: torch.
     if not isinstance(q, torch.Tensor):
         raise ValueError("q must be a 3-D tensor [tokens, heads, head_dim]")
     cache, scales, index, dtype, kv_heads, head_dim = _slot_cache(k_cache, v_cache, k_scales, v_scales, q.dtype)
-    qs = _heads("q", q, dtype, index, head_dim)
-    tokens, heads = q.shape[:2]
-    ks = _heads("k", k, dtype, index, head_dim, tokens, kv_heads)
-    vs = _heads("v", v, dtype, index, head_dim, tokens, kv_heads)
+    (tokens, heads, dim), qs = _heads("q", q, dtype, index)
+    if dim != head_dim:
+        raise ValueError("q must have the cache's head_dim")
+    ks = _keys("k", k, dtype, index, (tokens, kv_heads, head_dim))
+    vs = _keys("v", v, dtype, index, (tokens, kv_heads, head_dim))
     _tensor("slots", slots, torch.int32, (tokens,), index)
     if (positions is None) != (rotary is None):
         raise ValueError("positions and rotary must be given together")
@@ -115,12 +126,17 @@ def write_cache(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slots: torch.
             raise ValueError("rotary must be 16-byte aligned, not empty, with a multiple of 16 columns, "
                              "at most head_dim")
         _tensor("positions", positions, torch.int32, (tokens,), index)
-    norms = [w for w in (q_norm, k_norm) if w is not None]
-    for w in norms:
-        if not isinstance(w, torch.Tensor) or w.dtype not in (torch.float32, dtype) or w.dtype is not norms[0].dtype:
+    qn = kn = norm = 0
+    if q_norm is not None or k_norm is not None:
+        kind = (k_norm if q_norm is None else q_norm).dtype
+        if kind is not dtype and kind is not torch.float32:
             raise ValueError("q_norm and k_norm must be float32 or of q's dtype, both the same")
-        _tensor("q_norm and k_norm", w, w.dtype, (head_dim,), index)
-        if w.data_ptr() & 15:
+        norm = _DTYPE[kind]
+        if q_norm is not None:
+            qn = _tensor("q_norm", q_norm, kind, (head_dim,), index).data_ptr()
+        if k_norm is not None:
+            kn = _tensor("k_norm", k_norm, kind, (head_dim,), index).data_ptr()
+        if (qn | kn) & 15:
             raise ValueError("q_norm and k_norm must be 16-byte aligned")
     if not 0 <= eps < math.inf:
         raise ValueError("eps must be a finite number, not negative")
@@ -129,18 +145,16 @@ def write_cache(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slots: torch.
         if q_out.data_ptr() & 15:
             raise ValueError("q_out must be 16-byte aligned")
         _apart("q_out", q_out, q, k, v, k_cache, v_cache, k_scales, v_scales)
-    lib, device = library(), q.device
+    lib = library()
 
     def call(sp):
-        out = torch.empty((tokens, heads, head_dim), dtype=dtype, device=device) if q_out is None else q_out
-        k_out = torch.empty((tokens, kv_heads, head_dim), dtype=dtype, device=device) if return_k else None
+        out = q.new_empty((tokens, heads, head_dim)) if q_out is None else q_out
+        k_out = q.new_empty((tokens, kv_heads, head_dim)) if return_k else None
         packed = _TOKENS.pack(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), *qs, *ks, *vs,
-            0 if q_norm is None else q_norm.data_ptr(), 0 if k_norm is None else k_norm.data_ptr(), eps,
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), *qs, *ks, *vs, qn, kn, eps,
             0 if rotary is None else rotary.data_ptr(), max_position,
             0 if positions is None else positions.data_ptr(), slots.data_ptr(), tokens, out.data_ptr(),
-            0 if k_out is None else k_out.data_ptr(), heads,
-            _DTYPE[norms[0].dtype] if norms else 0, rot, bool(interleaved))
+            0 if k_out is None else k_out.data_ptr(), heads, norm, rot, bool(interleaved))
         _check("vts_write_cache", lib.vts_write_cache(cache, scales, packed, sp))
         return out, k_out
 
@@ -157,13 +171,14 @@ def read_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, slots: torch.Tensor
     if dtype is None and micro:
         dtype = torch.bfloat16
     cache, scales, index, dtype, kv_heads, head_dim = _slot_cache(k_cache, v_cache, k_scales, v_scales, dtype)
-    if not isinstance(slots, torch.Tensor):
-        raise ValueError("slots must be an int32 tensor")
-    _tensor("slots", slots, torch.int32, slots.shape, index)
-    lib, device = library(), k_cache.device
+    if (not isinstance(slots, torch.Tensor) or slots.dtype is not torch.int32 or slots.get_device() != index
+            or not slots.is_contiguous()):
+        raise ValueError(f"slots must be a contiguous int32 tensor on cuda:{index}")
+    lib = library()
+    shape = (*slots.shape, kv_heads, head_dim)
 
     def call(sp):
-        k, v = (torch.empty((*slots.shape, kv_heads, head_dim), dtype=dtype, device=device) for _ in "kv")
+        k, v = k_cache.new_empty(shape, dtype=dtype), k_cache.new_empty(shape, dtype=dtype)
         _check("vts_read_cache", lib.vts_read_cache(cache, scales, slots.data_ptr(), slots.numel(),
                                                     k.data_ptr(), v.data_ptr(), sp))
         return k, v
@@ -187,13 +202,13 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     dtype, index = q.dtype, q.get_device()
     if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise ValueError("q dtype must be bfloat16 or float16")
-    qs = _heads("q", q, dtype, index)
-    total_q, heads, head_dim = q.shape
-    if head_dim not in (64, 128):
+    (total_q, heads, head_dim), qs = _heads("q", q, dtype, index)
+    if head_dim != 64 and head_dim != 128:
         raise ValueError("head_dim must be 64 or 128")
-    ks = _heads("k", k, dtype, index, head_dim)
-    total_k, kv_heads = k.shape[:2]
-    vs = _heads("v", v, dtype, index, head_dim, total_k, kv_heads)
+    (total_k, kv_heads, dim), ks = _heads("k", k, dtype, index)
+    if dim != head_dim:
+        raise ValueError("k must have q's head_dim")
+    vs = _keys("v", v, dtype, index, (total_k, kv_heads, dim))
     if heads % kv_heads:
         raise ValueError("the query heads must be a multiple of the KV heads")
     if cu_seqlens_k is None:
@@ -210,14 +225,14 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
         _apart("out", out, q, k, v)
     if scale is None:
         scale = 1.0 / math.sqrt(head_dim)
-    lib, device = library(), q.device
+    lib = library()
     packed = _PROMPTS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), *qs, *ks, *vs, cu_seqlens.data_ptr(),
                            cu_seqlens_k.data_ptr(), batch, total_q, total_k, heads, kv_heads, head_dim,
                            _DTYPE[dtype])
 
     def call(sp):
-        o = torch.empty((total_q, heads, head_dim), dtype=dtype, device=device) if out is None else out
-        lse = torch.empty((total_q, heads), dtype=torch.float32, device=device) if return_lse else None
+        o = q.new_empty((total_q, heads, head_dim)) if out is None else out
+        lse = q.new_empty((total_q, heads), dtype=torch.float32) if return_lse else None
         _check("vts_prompt_attention", lib.vts_prompt_attention(
             packed, bool(causal), scale, o.data_ptr(), lse.data_ptr() if return_lse else None,
             out is None, sp))

@@ -144,8 +144,11 @@ def _table(name, t, batch, index):
 
 def _rows(name, t, low, index):
     """The strides of a microscaled cache's tensor, or of its scales."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 4 or t.dtype is not torch.uint8 or t.get_device() != index:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.uint8 or t.get_device() != index or t.dim() != 4:
         raise ValueError(f"{name} must be a 4-D uint8 tensor on cuda:{index}")
+    a, b, c, d = t.stride()
+    if ((a | b | c | t.data_ptr()) & low) == 0 and d == 1:
+        return a, b, c
     steps = _steps(t, low)
     if steps is None or t.data_ptr() & low:
         raise ValueError(f"{name} rows must be contiguous, with an address and strides that are multiples "
@@ -161,20 +164,21 @@ def _micro(k_cache, v_cache, k_scales, v_scales):
         raise ValueError("k_cache must be on the GPU")
     index = k_cache.get_device()
     ks, vs = _rows("k_cache", k_cache, 15, index), _rows("v_cache", v_cache, 15, index)
-    if not isinstance(k_scales, torch.Tensor) or k_scales.dim() != 4 or k_scales.shape[3] not in (2, 4):
-        raise ValueError("k_scales must be a 4-D tensor [pages, page_size, kv_heads, head_dim / 32] of "
-                         "head_dim 64 or 128")
-    head_dim = 32 * k_scales.shape[3]
-    kss = _rows("k_scales", k_scales, head_dim // 32 - 1, index)
-    vss = _rows("v_scales", v_scales, head_dim // 32 - 1, index)
-    if v_cache.shape != k_cache.shape or v_scales.shape != k_scales.shape:
-        raise ValueError("v_cache and v_scales must have the shapes of k_cache and k_scales")
-    if k_cache.shape[:3] != k_scales.shape[:3] or k_cache.shape[3] not in (head_dim, head_dim // 2):
-        raise ValueError("a microscaled cache's rows must be head_dim (8 bits) or head_dim / 2 (4 bits) bytes, "
-                         "and its scales [pages, page_size, kv_heads, head_dim / 32]")
-    bits = 8 * k_cache.shape[3] // head_dim
-    packed = _SCALES.pack(k_scales.data_ptr(), v_scales.data_ptr(), *kss, *vss, bits)
-    return ks, vs, packed, index, head_dim
+    if not isinstance(k_scales, torch.Tensor) or k_scales.dim() != 4:
+        raise ValueError("k_scales must be a 4-D tensor [pages, page_size, kv_heads, head_dim / 32]")
+    pages, page_size, kv_heads, row = shape = k_cache.shape
+    blocks = k_scales.shape[3]
+    if blocks != 4 and blocks != 2:
+        raise ValueError("k_scales must be of head_dim 64 or 128, a scale to 32 elements")
+    kss, vss = _rows("k_scales", k_scales, blocks - 1, index), _rows("v_scales", v_scales, blocks - 1, index)
+    scales = (pages, page_size, kv_heads, blocks)
+    if v_cache.shape != shape or k_scales.shape != scales or v_scales.shape != scales or row not in (
+            32 * blocks, 16 * blocks):
+        raise ValueError("a microscaled cache's rows must be head_dim (8 bits) or head_dim / 2 (4 bits) bytes, its "
+                         "scales [pages, page_size, kv_heads, head_dim / 32], and V's tensors must have the shapes "
+                         "of K's")
+    packed = _SCALES.pack(k_scales.data_ptr(), v_scales.data_ptr(), *kss, *vss, row // (4 * blocks))
+    return ks, vs, packed, index, 32 * blocks
 
 
 def _paged_micro(k_cache, v_cache, k_scales, v_scales, page_table, seq_lens, dtype):
