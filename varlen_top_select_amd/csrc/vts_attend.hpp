@@ -42,14 +42,17 @@ enum Mode : int {
     WIDE4 = 4,  // eight waves: four groups of 32 rows, twice 32 places
 };
 
-constexpr int threads_of(int mode) { return mode >= WIDE2 ? 512 : NT; }
+// (over a microscaled cache wide workgroups have four waves, and two of them share a
+// compute unit: eight that wait for each other have all their products at the same time)
+constexpr int threads_of(int mode, int f) { return mode >= WIDE2 && f == 16 ? 512 : NT; }
 
 template <int D, int MT, int MODE, int F>
 struct AttendShape {
     static constexpr bool WIDE = MODE >= WIDE2;
-    static constexpr int NW = threads_of(MODE) / 64;       // waves
+    static constexpr int NW = threads_of(MODE, F) / 64;    // waves
     static constexpr int RG = WIDE ? MODE : 1;             // groups of rows
     static constexpr int KG = WIDE ? NW / RG : MODE == HEADS ? 1 : NW;  // groups of places
+    static constexpr int PLACES = WIDE && F != 16 ? 64 : KG * 32;  // of a unit
     static constexpr int SUBS = MODE == HEADS ? NW : RG;   // blocks of 16 * MT rows
     static constexpr int ROWS = SUBS * 16 * MT;
     // a cache row in memory
@@ -70,15 +73,16 @@ struct WideTiles {
 template <int D, int MT, int MODE, int F>
 struct AttendShared : AttendShape<D, MT, MODE, F> {
     using S = AttendShape<D, MT, MODE, F>;
-    u32x4 q[MT > 1 ? S::SUBS * MT * (D / 32) : 1][64];  // query rows as operands, from 32 rows on
+    // query rows as operands, from 32 rows on
+    u32x4 q[MT > 1 && !(S::WIDE && F != 16) ? S::SUBS * MT * (D / 32) : 1][64];
     union {
         // a wave's K rows on their way from the order of whole rows to operands
         u32x4 k[S::WIDE || F != 16 ? 1 : WAVES][S::WIDE || F != 16 ? 1 : 32 * (D / 8)];
         // the same of a microscaled cache, K and V
         u32x4 packed[S::WIDE || F == 16 ? 1 : WAVES][S::WIDE || F == 16 ? 1 : 2 * 32 * S::PAD / 16];
-        WideTiles<D, S::WIDE ? S::KG * 32 : 1> w;
+        WideTiles<D, S::WIDE ? S::PLACES : 1> w;
         // outputs of waves to be joined, padded: the 16 rows of a store fall on all banks
-        float o[MODE == HEADS ? 1 : S::WIDE ? S::KG - 1 : 2][MODE == HEADS ? 1 : S::ROWS][D + 4];
+        float o[MODE == HEADS || S::KG == 1 ? 1 : S::WIDE ? S::KG - 1 : 2][MODE == HEADS ? 1 : S::ROWS][D + 4];
     };
     // 16 rows of a wave on their way to whole rows of a part (waves do not wait for each
     // other, so it is no wave's tile; from 32 rows on, where its query rows were)
@@ -98,6 +102,12 @@ struct Attend {
     static constexpr bool MICRO = F != 16;
     // a lane multiplies the elements of its quarter of a row, and not its eight of each 32
     static constexpr bool PERMUTED = MICRO && !S::WIDE;
+    // A wide workgroup over a microscaled cache: a wave's 32 rows are one block of the 32x32x16
+    // product.  It takes two thirds of the LDS loads that two blocks of the 16x16x32 one take,
+    // and two workgroups of four waves to a compute unit have products and softmax at the
+    // same time (8 trees of 16 up to 65536: XX us for 433).
+    static constexpr bool BLOCK = MICRO && S::WIDE;
+    static constexpr int KB = D / 16, OB = D / 32;  // steps and tiles of its products
     static constexpr bool HEAD = MODE == HEADS, WIDE = S::WIDE;
     static constexpr int T = S::NW * 64;    // threads
     // whether a cache row is read once by the whole call, as far as it is known
@@ -113,6 +123,7 @@ struct Attend {
     const AttendParams& p;
     AttendShared<D, MT, MODE, F>& sm;
     int tid, lane, wave, col, grp;
+    int bcol, half;  // (BLOCK) the lane's row, and its half of a product's places
     int rg, kg;  // the wave's group of rows and of places
     uint32_t page_stride, pos_stride;  // of K in lanes 0..31, of V above
     int32_t req, head_unit, mb, t0;  // t0: the row of a slot list
@@ -126,16 +137,24 @@ struct Attend {
     // Microscaled: a wave's loads of each of K and V, or (wide) a thread's chunks of both
     static constexpr int CHF = S::CHF, RB = S::RB, PAD = S::PAD;
     static constexpr int BLOCKS = D / 32;  // scales of a row
-    static constexpr int HALF = S::KG * 32 * CHF;  // (wide) chunks of K in a unit, and of V
+    static constexpr int HALF = S::PLACES * CHF;  // (wide) chunks of K in a unit, and of V
     static constexpr int LOADSF = !WIDE ? CHF / 2 : HALF >= T ? 2 * HALF / T : 1;
-    // Microscaled tiles on their way to a wave: with one of 4 KB a wave waits for memory most
-    // of the time; more do not fit the registers.
-    static constexpr int AHEAD = !MICRO || WIDE ? 1 : D == 64 || (MT == 1 && !(HEAD && SLOTS && F == 8)) ? 2 : 1;
+    // Microscaled tiles (wide: units) on their way, as many as the registers hold beside
+    // two waves of a SIMD: with one of 4 KB a wave waits for memory most of the time (64
+    // requests up to 16384 over a 4-bit cache 224 us with one and 187 with two).
+    static constexpr int AHEAD = !MICRO          ? 1
+                                 : WIDE          ? (D == 64 || F == 4 ? 2 : 1)
+                                 : D == 64       ? 3
+                                 : MT > 1        ? 1
+                                 : F == 4        ? 2
+                                 : HEAD && SLOTS ? 1
+                                                 : 2;
     using Scales = typename std::conditional<D == 128, uint32_t, uint16_t>::type;
-    u32x4 q[QL ? 1 : KS];
+    u32x4 q[BLOCK ? KB : QL ? 1 : KS];
     uint64_t bits[MT];
-    f32x4 o[MT][NTILE];
+    f32x4 o[BLOCK ? 1 : MT][NTILE];
     float m[MT], l[MT];
+    f32x16 ob[BLOCK ? OB : 1];
     // the tile on its way: 32 places to a wave, or the wave's rows of the unit
     u32x4 k[MICRO ? LOADSF * AHEAD : WIDE ? LOADS : 2 * KS];
     VRow v[8];
@@ -144,8 +163,8 @@ struct Attend {
     const void* vbase;
     // Microscaled: the scales on their way (K's of place l in lane l, V's in lane
     // 32 + l; wide: of the thread's chunks) and of the tile at hand
-    uint32_t sc_next[WIDE ? LOADSF : AHEAD], sc;
-    bool here[WIDE ? LOADSF : 1];  // (wide) whether the chunks' places are there
+    uint32_t sc_next[WIDE ? LOADSF * AHEAD : AHEAD], sc;
+    bool here[WIDE ? LOADSF * AHEAD : 1];  // (wide) whether the chunks' places are there
     // of the scales: K's in lanes 0..31, V's above
     const char* sbase;
     uint32_t scale_page, scale_pos;
@@ -165,6 +184,8 @@ struct Attend {
         wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         col = lane & 15;
         grp = lane >> 4;
+        bcol = lane & 31;
+        half = lane >> 5;
         rg = WIDE ? wave % S::RG : 0;
         kg = WIDE ? wave / S::RG : HEAD ? 0 : wave;
     }
@@ -214,8 +235,12 @@ struct Attend {
             const ScaleView& s = lane < 32 ? p.k_scale : p.v_scale;
             sbase = (const char*)s.base + (uint64_t)h * s.head_stride * BLOCKS;
         }
+        if constexpr (BLOCK) {
+            begin_block();
+            return;
+        }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+        for (int mt = 0; mt < (BLOCK ? 0 : MT); ++mt) {
             int32_t t, head;
             const bool ok = row_of(sub(), mt * 16 + col, t, head);
             const char* at = (const char*)p.q +
@@ -247,12 +272,36 @@ struct Attend {
         }
         if constexpr (QL && !HEAD) __syncthreads();
     }
+    __device__ __forceinline__ void begin_block() {
+        int32_t t, head;
+        const bool ok = row_of(sub(), bcol, t, head);
+        const char* at = (const char*)p.q + 2 * (req * p.q_batch + (ok ? t * p.q_row + head * p.q_head : 0));
+#pragma unroll
+        for (int s = 0; s < KB; ++s) {
+            u32x4 x = {0, 0, 0, 0};
+            if (ok) x = gload((const u32x4*)at + s * 2 + half);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] ^= p.q_sign;
+            q[s] = x;
+        }
+        bits[0] = !ok           ? 0
+                  : p.tree_mask ? (uint64_t)gload(p.tree_mask + (int64_t)req * p.c.draft + t)
+                  : t >= 63     ? ~0ull
+                                : (2ull << t) - 1;
+        m[0] = NEG_INF;
+        l[0] = 0;
+#pragma unroll
+        for (int i = 0; i < OB; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ob[i][e] = 0;
+        cleared = false;
+    }
     __device__ __forceinline__ int q_at(int mt, int s) const {
         return (sub() * MT + mt) * KS + s;
     }
 
     __device__ __forceinline__ int32_t first_place(int32_t u) const {
-        return (u * S::KG + kg) * 32;
+        return BLOCK ? u * S::PLACES + kg * 32 : (u * S::KG + kg) * 32;
     }
     // the place that lane l of a wave looks up: of its own 32, or (wide) of its
     // rows of the unit
@@ -335,16 +384,19 @@ struct Attend {
     }
     // The rows of a wave's tile, as they lie in memory, and their scales: K's of
     // place l in lane l, V's in lane 32 + l, one load for both.
-    __device__ __forceinline__ void load_micro(int to, uint32_t off, uint32_t soff) {
-        const uint32_t safe = off == NO_PLACE ? 0 : off;
+    // Returns whether the lane's place is there.
+    __device__ __forceinline__ bool load_micro(int to, const Lookup& e) {
+        const Spot at = resolve_lookup<SLOTS>(p.c, e);
+        const uint32_t off = spot_offset(at, page_stride, pos_stride);
 #pragma unroll
         for (int i = 0; i < LOADSF; ++i) {
             const int r = i * (64 / CHF) + lane / CHF;
-            k[to * LOADSF + i] = row_load<u32x4, ONCE>(kbase, from_lane(safe, r), (lane % CHF) * 16);
-            vw[to * LOADSF + i] = row_load<u32x4, ONCE>(vbase, from_lane(safe, 32 + r), (lane % CHF) * 16);
+            k[to * LOADSF + i] = row_load<u32x4, ONCE>(kbase, from_lane(off, r), (lane % CHF) * 16);
+            vw[to * LOADSF + i] = row_load<u32x4, ONCE>(vbase, from_lane(off, 32 + r), (lane % CHF) * 16);
         }
         sc_next[to] = *(const VTS_GLOBAL Scales*)((const VTS_GLOBAL char*)sbase +
-                                                 (uint64_t)(soff == NO_PLACE ? 0 : soff) * BLOCKS);
+                                                  (uint64_t)spot_offset(at, scale_page, scale_pos) * BLOCKS);
+        return at.there;
     }
     __device__ __forceinline__ char* packed_row(int which, int r) const {
         return (char*)sm.packed[wave] + (which * 32 + r) * PAD;
@@ -435,36 +487,43 @@ struct Attend {
             }
         }
     }
-    // What micro_product cleared in this wave's tiles of units [u0, u1), from memory to the
-    // rows that see it: rare, and apart from the walk, whose registers it would take.
+    // What was cleared of V in units [u0, u1), in the wave's tiles or (BLOCK) in all, from
+    // memory to the rows that see it: rare, and apart from the walk, whose registers it
+    // would take.
     __device__ __forceinline__ void add_cleared(int32_t u0, int32_t u1) {
         fresh();
+        constexpr int SPAN = BLOCK ? S::PLACES : 32;
 #pragma unroll 1
         for (int32_t u = u0; u < u1; ++u) {
-            if (first_place(u) + 31 < pl.first) continue;
+            const int32_t j0 = BLOCK ? u * SPAN : first_place(u);
+            if (j0 + SPAN - 1 < pl.first) continue;
 #pragma unroll 1
-            for (int kk = 0; kk < 32; ++kk) {
-                const int32_t i = first_place(u) + kk - pl.first;
+            for (int kk = 0; kk < SPAN; ++kk) {
+                const int32_t i = j0 + kk - pl.first;
                 if (i < 0) continue;
-                const Entry e = issue_entry<SLOTS>(p.c, pl, first_place(u) + kk);
-                const uint32_t off = resolve_entry<SLOTS>(p.c, p.c.v.page_stride, p.c.v.pos_stride, e);
-                if (off == NO_PLACE) continue;
-                const uint32_t soff = resolve_entry<SLOTS>(p.c, p.v_scale.page_stride, p.v_scale.pos_stride, e);
+                const Spot at = resolve_lookup<SLOTS>(p.c, issue_lookup<SLOTS>(p.c, pl, j0 + kk));
+                if (!at.there) continue;
+                const uint32_t off = spot_offset(at, p.c.v.page_stride, p.c.v.pos_stride);
+                const uint32_t soff = spot_offset(at, p.v_scale.page_stride, p.v_scale.pos_stride);
                 const int32_t h = HEAD ? head_unit * WAVES + wave : head_unit;
                 const uint8_t* codes = p.v_scale.base + ((uint64_t)soff + (uint64_t)h * p.v_scale.head_stride) * BLOCKS;
+                const VTS_GLOBAL char* row = (const VTS_GLOBAL char*)vbase + ((uint64_t)off << 4);
+                if constexpr (BLOCK) {
+                    add_to_block(codes, row, i);
+                    continue;
+                }
 #pragma unroll
-                for (int e4 = 0; e4 < 4; ++e4) {
+                for (int e4 = 0; e4 < (BLOCK ? 0 : 4); ++e4) {
                     constexpr int B = RB / 16;
                     const int part = grp * 4 + e4;
                     const float scale = scale_of(gload(codes + part / (16 / BLOCKS)));
                     uint32_t w[2] = {0, 0};
-                    const VTS_GLOBAL char* at =
-                        (const VTS_GLOBAL char*)vbase + ((uint64_t)off << 4) + part * B;
+                    const VTS_GLOBAL char* x4 = row + part * B;
                     if constexpr (B == 2) {
-                        w[0] = *(const VTS_GLOBAL uint16_t*)at;
+                        w[0] = *(const VTS_GLOBAL uint16_t*)x4;
                     } else {
-                        w[0] = *(const VTS_GLOBAL uint32_t*)at;
-                        if constexpr (B == 8) w[1] = *(const VTS_GLOBAL uint32_t*)(at + 4);
+                        w[0] = *(const VTS_GLOBAL uint32_t*)x4;
+                        if constexpr (B == 8) w[1] = *(const VTS_GLOBAL uint32_t*)(x4 + 4);
                     }
                     const u32x4 x = widen(w[0], w[1], scale);
 #pragma unroll
@@ -482,59 +541,161 @@ struct Attend {
             }
         }
     }
+    // The same of one place's row, to the lane's elements 32 i + 8 n + 4 half ..
+    __device__ __forceinline__ void add_to_block(const uint8_t* codes, const VTS_GLOBAL char* row, int32_t place) {
+        const bool see = (bits[0] >> (place & 63)) & 1;
+#pragma unroll
+        for (int i = 0; i < OB; ++i) {
+            const float scale = scale_of(gload(codes + i));
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const VTS_GLOBAL char* at = row + (32 * i + 8 * n + 4 * half) * F / 8;
+                u32x4 x;
+                if constexpr (F == 4)
+                    x = widen(*(const VTS_GLOBAL uint16_t*)at, 0, scale);
+                else
+                    x = widen(*(const VTS_GLOBAL uint32_t*)at, 0, scale);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t one = (x[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+                    const float y = ob[i][4 * n + e] + to_float<DT>(one);
+                    ob[i][4 * n + e] = see && not_finite<DT>(one) ? y : ob[i][4 * n + e];
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    }
+
+    // A wave's 32 rows and its places of a unit, 32 or all 64: as tile(), in blocks.
+    static constexpr int PB = BLOCK ? S::PLACES / 32 / S::KG : 1;
+    __device__ __forceinline__ void tile_block(const uint32_t (&have)[PB], bool masked, int32_t j0, int buf) {
+        const float c = p.scale_log2e;
+        f32x16 s[PB];
+#pragma unroll
+        for (int b = 0; b < PB; ++b)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[b][e] = 0;
+#pragma unroll
+        for (int ks = 0; ks < KB; ++ks)
+#pragma unroll
+            for (int b = 0; b < PB; ++b) {
+                const int r = (kg + b) * 32 + bcol;
+                s[b] = mfma32<DT>(sm.w.k[buf][r * CH + ((2 * ks + half) ^ swizzled<D>(r))], q[ks], s[b]);
+            }
+        if (masked) {
+            int h = half;  // opaque: nothing of this is kept in registers between tiles
+            asm volatile("" : "+v"(h));
+#pragma unroll
+            for (int b = 0; b < PB; ++b)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int kk = key_of(e) + 4 * h;
+                    const int32_t i = j0 + b * 32 + kk - pl.first;
+                    const uint32_t see =
+                        (have[b] >> kk) & (((uint32_t)i >> 31) | (uint32_t)(bits[0] >> (i & 63)));
+                    s[b][e] = (see & 1u) ? s[b][e] : NEG_INF;
+                }
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int b = 0; b < PB; ++b)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) top = fmaxf(top, s[b][e]);
+        top *= c;
+        if (ballot(top > m[0] + RAISE)) {
+            float up = fmaxf(top, __shfl_xor(top, 32));
+            up = up > m[0] + RAISE ? up - SHIFT : m[0];
+            const float f = up == NEG_INF ? 1.0f : __builtin_amdgcn_exp2f(m[0] - up);
+            m[0] = up;
+            l[0] *= f;
+#pragma unroll
+            for (int i = 0; i < OB; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) ob[i][e] *= f;
+        }
+        const float base = m[0] == NEG_INF ? 0.0f : m[0];
+        u32x4 pv[2 * PB];
+#pragma unroll
+        for (int b = 0; b < PB; ++b)
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+                const float x = __builtin_amdgcn_exp2f(fmaf(s[b][e], c, -base));
+                const float y = __builtin_amdgcn_exp2f(fmaf(s[b][e + 1], c, -base));
+                l[0] += x + y;
+                pv[2 * b + (e >> 3)][(e >> 1) & 3] = pack2<DT>(x, y);
+            }
+#pragma unroll
+        for (int step = 0; step < 2 * PB; ++step)
+#pragma unroll
+            for (int i = 0; i < OB; ++i)
+                ob[i] = mfma32<DT>(turned_v<D>(sm.w.v[buf], lane, kg * 32 + 16 * step, i), pv[step], ob[i]);
+    }
     // Wide: the thread's chunks of a unit.  PAIRS of the same place and number of K and of V,
     // or, where the unit's K has fewer chunks than there are threads, one of K or of V.
     static constexpr int PAIRS = HALF >= T ? HALF / T : 0;
     static constexpr bool RAGGED = 2 * HALF < T;  // (then only the first threads have one)
     __device__ __forceinline__ int place_of(int i) const { return (i * T + tid) % HALF / CHF; }
     __device__ __forceinline__ bool thread_v() const { return PAIRS == 0 && tid >= HALF; }
-    __device__ __forceinline__ void load_chunk(int to, const Entry& e, bool is_v, bool mine) {
+    __device__ __forceinline__ void load_chunk(int to, const Spot& at, bool is_v, bool mine) {
         const CacheView& view = is_v ? p.c.v : p.c.k;
         const ScaleView& s = is_v ? p.v_scale : p.k_scale;
         const int chunk = mine ? tid % CHF : 0;
-        const uint32_t off = resolve_entry<SLOTS>(p.c, view.page_stride, view.pos_stride, e);
-        const uint32_t soff = resolve_entry<SLOTS>(p.c, s.page_stride, s.pos_stride, e);
-        const bool there = mine && off != NO_PLACE;
-        here[to] = there;
-        k[to] = row_load<u32x4>(is_v ? vbase : kbase, there ? off : 0, chunk * 16);
+        here[to] = mine && at.there;
+        k[to] = row_load<u32x4>(is_v ? vbase : kbase, spot_offset(at, view.page_stride, view.pos_stride), chunk * 16);
         sc_next[to] = ((const VTS_GLOBAL uint8_t*)s.base)
-            [((uint64_t)(there ? soff : 0) + (uint64_t)head_unit * s.head_stride) * BLOCKS + chunk * BLOCKS / CHF];
+            [((uint64_t)spot_offset(at, s.page_stride, s.pos_stride) + (uint64_t)head_unit * s.head_stride) * BLOCKS +
+             chunk * BLOCKS / CHF];
     }
-    __device__ __forceinline__ void load_wide_micro(int32_t u) {
-        static_assert(T % CHF == 0 && (PAIRS == 0 ? 2 * HALF <= T : HALF % T == 0), "chunks of a thread");
+    static_assert(!BLOCK || (T % CHF == 0 && (PAIRS == 0 ? 2 * HALF <= T : HALF % T == 0)), "chunks of a thread");
+    static constexpr int LOOKUPS = PAIRS ? PAIRS : 1;  // places of a thread's chunks
+    __device__ __forceinline__ void issue_wide(Lookup (&e)[LOOKUPS], int32_t u) const {
 #pragma unroll
-        for (int i = 0; i < (PAIRS ? PAIRS : 1); ++i) {
-            const bool mine = !RAGGED || tid < 2 * HALF;
-            const Entry e = issue_entry<SLOTS>(p.c, pl, mine ? u * S::KG * 32 + place_of(i) : -1);
+        for (int i = 0; i < LOOKUPS; ++i)
+            e[i] = issue_lookup<SLOTS>(p.c, pl, !RAGGED || tid < 2 * HALF ? u * S::PLACES + place_of(i) : -1);
+    }
+    __device__ __forceinline__ void load_wide_micro(int to, const Lookup (&e)[LOOKUPS]) {
+#pragma unroll
+        for (int i = 0; i < LOOKUPS; ++i) {
+            const Spot at = resolve_lookup<SLOTS>(p.c, e[i]);
             if constexpr (PAIRS) {
-                load_chunk(2 * i, e, false, true);
-                load_chunk(2 * i + 1, e, true, true);
+                load_chunk(to * LOADSF + 2 * i, at, false, true);
+                load_chunk(to * LOADSF + 2 * i + 1, at, true, true);
             } else {
-                load_chunk(0, e, thread_v(), mine);
+                load_chunk(to, at, thread_v(), !RAGGED || tid < 2 * HALF);
             }
         }
     }
-    __device__ __forceinline__ void stage_wide_micro(int buf) {
+    // clear: some rows of the unit do not see some places; what is not finite in V goes to
+    // them by add_cleared
+    __device__ __forceinline__ void stage_wide_micro(int from, int buf, bool clear) {
         constexpr int OUT = CH / CHF;  // 16-byte chunks of operands from one
 #pragma unroll
         for (int i = 0; i < LOADSF; ++i) {
             if (RAGGED && tid >= 2 * HALF) continue;
             const bool is_v = PAIRS ? i & 1 : thread_v();
             const int r = place_of(PAIRS ? i / 2 : 0), chunk = tid % CHF;
-            const float scale = scale_of(sc_next[i]);
+            const float scale = scale_of(sc_next[from * LOADSF + i]);
 #pragma unroll
             for (int e = 0; e < OUT; ++e) {
-                const u32x4 y = F == 4 ? widen(k[i][e % 4], 0, scale)
-                                       : widen(k[i][2 * e % 4], k[i][(2 * e + 1) % 4], scale);
+                u32x4 y = F == 4 ? widen(k[from * LOADSF + i][e % 4], 0, scale)
+                                 : widen(k[from * LOADSF + i][2 * e % 4], k[from * LOADSF + i][(2 * e + 1) % 4], scale);
                 const int c = chunk * OUT + e;
                 if (is_v) {
                     const u32x4 z = {0, 0, 0, 0};
-                    sm.w.v[buf][r * CH + c] = here[i] ? y : z;
+                    if (!here[from * LOADSF + i]) y = z;
+                    if (clear) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            cleared = cleared || not_finite<DT>(y[x]);
+                            y[x] = finite_part<DT>(y[x]);
+                        }
+                    }
+                    sm.w.v[buf][v_chunk<D>(r, c)] = y;
                 } else {
                     sm.w.k[buf][r * CH + (c ^ swizzled<D>(r))] = y;
                 }
             }
-            if (!is_v && chunk == 0) sm.w.there[buf][r] = here[i];
+            if (!is_v && chunk == 0) sm.w.there[buf][r] = here[from * LOADSF + i];
         }
     }
 
@@ -813,28 +974,26 @@ struct Attend {
         cleared = false;
         scale_page = lane < 32 ? p.k_scale.page_stride : p.v_scale.page_stride;
         scale_pos = lane < 32 ? p.k_scale.pos_stride : p.v_scale.pos_stride;
-        uint32_t off[AHEAD];
-        Entry e[AHEAD + 1];
+        const auto look = [&](int32_t u) { return issue_lookup<SLOTS>(p.c, pl, first_place(u) + (lane & 31)); };
+        bool there[AHEAD];
+        Lookup e[AHEAD + 1];
 #pragma unroll
-        for (int i = 0; i <= AHEAD; ++i) e[i] = issue(u0 + i);
+        for (int i = 0; i <= AHEAD; ++i) e[i] = look(u0 + i);
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            off[i] = resolve(e[i]);
-            load_micro(i, off[i], resolve_entry<SLOTS>(p.c, scale_page, scale_pos, e[i]));
-        }
-        Entry next = e[AHEAD];
+        for (int i = 0; i < AHEAD; ++i) there[i] = load_micro(i, e[i]);
+        Lookup next = e[AHEAD];
 #pragma unroll 1
         for (int32_t u = u0; u < u1; u += AHEAD) {
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) {
                 if (u + i >= u1) break;
                 const int32_t j0 = first_place(u + i);
-                const uint32_t have = (uint32_t)ballot(off[i] != NO_PLACE);
+                const uint32_t have = (uint32_t)ballot(there[i]);
                 stage_micro(i);
-                off[i] = resolve(next);
-                if (u + i + AHEAD < u1)
-                    load_micro(i, off[i], resolve_entry<SLOTS>(p.c, scale_page, scale_pos, next));
-                next = issue(u + i + AHEAD + 1);
+                const Lookup now = next;
+                // (before the rows: waiting for it waits for all loads before it)
+                next = look(u + i + AHEAD + 1);
+                there[i] = load_micro(i, now);
                 tile(have, j0 + 31 >= pl.first, 0, j0, false, 0, 0);
             }
         }
@@ -842,23 +1001,98 @@ struct Attend {
     }
     // A wide workgroup's.
     __device__ __forceinline__ void walk_wide_micro(int32_t u0, int32_t u1) {
-        load_wide_micro(u0);
+        Lookup e[AHEAD + 1][LOOKUPS];
+#pragma unroll
+        for (int i = 0; i <= AHEAD; ++i) issue_wide(e[i], u0 + i);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) load_wide_micro(i, e[i]);
+        Lookup next[LOOKUPS];
+#pragma unroll
+        for (int i = 0; i < LOOKUPS; ++i) next[i] = e[AHEAD][i];
 #pragma unroll 1
-        for (int32_t u = u0; u < u1; ++u) {
-            const int32_t j0 = first_place(u);
-            const int buf = u & 1;
-            stage_wide_micro(buf);
-            if (u + 1 < u1) load_wide_micro(u + 1);
-            __syncthreads();
-            const uint32_t have = (uint32_t)ballot(sm.w.there[buf][kg * 32 + (lane & 31)]);
-            tile(have, j0 + 31 >= pl.first, 0, j0, false, 0, buf);
+        for (int32_t u2 = u0; u2 < u1; u2 += AHEAD) {
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const int32_t u = u2 + i;
+                if (u >= u1) break;
+                const int32_t j0 = first_place(u);
+                const int buf = u & 1;
+                stage_wide_micro(i, buf, (u + 1) * S::PLACES > pl.first);
+                Lookup now[LOOKUPS];
+#pragma unroll
+                for (int x = 0; x < LOOKUPS; ++x) now[x] = next[x];
+                issue_wide(next, u + AHEAD + 1);  // (before the rows, as in walk_micro)
+                load_wide_micro(i, now);
+                __syncthreads();
+                uint32_t have[PB];
+                bool masked = j0 + PB * 32 > pl.first;
+#pragma unroll
+                for (int b = 0; b < PB; ++b) {
+                    have[b] = (uint32_t)ballot(sm.w.there[buf][(kg + b) * 32 + (lane & 31)]);
+                    masked = masked || have[b] != ~0u;
+                }
+                tile_block(have, masked, j0, buf);
+            }
         }
+        if (u1 * S::PLACES > pl.first) {  // (the same in all waves)
+            if (tid == 0) sm.last = 0;
+            __syncthreads();
+            if (cleared) sm.last = 1;
+            __syncthreads();
+            // (the groups' outputs are added up: one of them does it)
+            if (sm.last && kg == 0) add_cleared(u0, u1);
+            __syncthreads();
+        }
+    }
+
+    // (BLOCK) the lane's outputs, four by four, and where they begin
+    static constexpr int NFOUR = BLOCK ? 4 * OB : 0;
+    __device__ __forceinline__ f32x4 block_four(int i) const {
+        f32x4 x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = ob[i / 4][4 * (i % 4) + e];
+        return x;
+    }
+    __device__ __forceinline__ int block_at(int i) const { return 32 * (i / 4) + 8 * (i % 4) + 4 * half; }
+    // the same of waves of different places: left in the registers of the first group's
+    __device__ __forceinline__ void join_blocks() {
+        fresh();
+        l[0] += __shfl_xor(l[0], 32);
+        const int r = rg * 32 + bcol;
+        if (half == 0) {
+            sm.ml[kg][r][0] = m[0];
+            sm.ml[kg][r][1] = l[0];
+        }
+        __syncthreads();
+        float top = NEG_INF, sum = 0;
+#pragma unroll
+        for (int w = 0; w < S::KG; ++w) top = fmaxf(top, sm.ml[w][r][0]);
+#pragma unroll
+        for (int w = 0; w < S::KG; ++w) sum += sm.ml[w][r][1] * scale_to(sm.ml[w][r][0], top);
+        const float f = scale_to(m[0], top);
+        m[0] = top;
+        l[0] = sum;
+#pragma unroll
+        for (int i = 0; i < OB; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ob[i][e] *= f;
+        if (kg > 0) put(kg - 1);
+        __syncthreads();
+        if (kg == 0)
+#pragma unroll 1
+            for (int w = 0; w < S::KG - 1; ++w) take(w);
     }
 
     // o[.] += the rows that another wave left in LDS
     __device__ __forceinline__ void put(int slot) {
+        if constexpr (BLOCK) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+            for (int i = 0; i < NFOUR; ++i)
+                *(f32x4*)&sm.o[slot][rg * 32 + bcol][block_at(i)] = block_four(i);
+            return;
+        }
+#pragma unroll
+        for (int mt = 0; mt < (BLOCK ? 0 : MT); ++mt)
 #pragma unroll
             for (int n = 0; n < NTILE; ++n)
 #pragma unroll
@@ -866,8 +1100,17 @@ struct Attend {
                     sm.o[slot][rg * 16 * MT + mt * 16 + col][(grp * 4 + e) * NTILE + n] = o[mt][n][e];
     }
     __device__ __forceinline__ void take(int slot) {
+        if constexpr (BLOCK) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+            for (int i = 0; i < NFOUR; ++i) {
+                const f32x4 x = *(const f32x4*)&sm.o[slot][rg * 32 + bcol][block_at(i)];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) ob[i / 4][4 * (i % 4) + e] += x[e];
+            }
+            return;
+        }
+#pragma unroll
+        for (int mt = 0; mt < (BLOCK ? 0 : MT); ++mt)
 #pragma unroll
             for (int n = 0; n < NTILE; ++n)
 #pragma unroll
@@ -879,10 +1122,14 @@ struct Attend {
     // Joins the waves of different places.  Four waves: the block's rows are
     // then in sm.o[0], sm.ml[0]; wide: in the registers of the first group's.
     __device__ __forceinline__ void join_waves() {
+        if constexpr (BLOCK) {
+            join_blocks();
+            return;
+        }
         fresh();
         const int r0 = rg * 16 * MT + col;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+        for (int mt = 0; mt < (BLOCK ? 0 : MT); ++mt) {
             l[mt] += __shfl_xor(l[mt], 16);
             l[mt] += __shfl_xor(l[mt], 32);
             if (grp == 0) {
@@ -892,7 +1139,7 @@ struct Attend {
         }
         __syncthreads();
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+        for (int mt = 0; mt < (BLOCK ? 0 : MT); ++mt) {
             float top = NEG_INF, sum = 0;
 #pragma unroll
             for (int w = 0; w < S::KG; ++w) top = fmaxf(top, sm.ml[w][r0 + mt * 16][0]);
@@ -983,7 +1230,12 @@ struct Attend {
     }
 
     __device__ __forceinline__ void finish_whole() {
-        if constexpr (HEAD || WIDE) {
+        if constexpr (BLOCK) {
+            if (own_rows())
+#pragma unroll
+                for (int i = 0; i < NFOUR; ++i) write_row(sub(), bcol, block_at(i), block_four(i), m[0], l[0]);
+            __syncthreads();
+        } else if constexpr (HEAD || WIDE) {
             if (own_rows())
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
@@ -1062,6 +1314,16 @@ struct Attend {
                 // the next rows' stores come after these loads
                 __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
                 __builtin_amdgcn_wave_barrier();
+            }
+        } else if constexpr (BLOCK) {
+            if (own_rows() && row_at(sub(), bcol) < p.rows) {
+                const int at = sub() * 32 + bcol;
+#pragma unroll
+                for (int i = 0; i < NFOUR; ++i) pstore((f32x4*)(po + at * D + block_at(i)), block_four(i));
+                if (half == 0) {
+                    pstore(pm + at * 2, m[0]);
+                    pstore(pm + at * 2 + 1, l[0]);
+                }
             }
         } else if constexpr (HEAD || WIDE) {
             if (own_rows())
@@ -1232,9 +1494,9 @@ struct Attend {
 };
 
 template <int DT, int D, int MT, bool SLOTS, int MODE, int F>
-__global__ __launch_bounds__(threads_of(MODE), MODE >= WIDE2 || F != 16 ? 2 : 1) void attend_kernel(AttendParams p) {
+__global__ __launch_bounds__(threads_of(MODE, F), MODE >= WIDE2 || F != 16 ? 2 : 1) void attend_kernel(AttendParams p) {
     constexpr bool HEAD = MODE == HEADS;
-    constexpr int PLACES = AttendShape<D, MT, MODE, F>::KG * 32;
+    constexpr int PLACES = AttendShape<D, MT, MODE, F>::PLACES;
     __shared__ AttendShared<D, MT, MODE, F> sm;
     // the row blocks of one share run next to each other on one XCD
     const int32_t per = 8 * p.row_blocks;
@@ -1289,7 +1551,7 @@ template <int DT, int D, int MT, bool SLOTS, int MODE, int F>
 static hipError_t launch_one(const AttendParams& p, hipStream_t stream) {
     const uint32_t grid = (uint32_t)((p.workers + 7) / 8 * 8 * p.row_blocks);
     hipLaunchKernelGGL((attend_kernel<DT, D, MT, SLOTS, MODE, F>), dim3(grid),
-                       dim3(threads_of(MODE)), 0, stream, p);
+                       dim3(threads_of(MODE, F)), 0, stream, p);
     return hipGetLastError();
 }
 

@@ -169,7 +169,7 @@ inline int attend_plan(int64_t batch, int32_t draft, int32_t heads, int32_t kv_h
     out->block_rows = block;
     out->row_blocks = (out->rows + block - 1) / block;
     if (out->row_blocks > MAX_TICKETS) return VTS_ERR_UNSUPPORTED;
-    const bool two = bits != 16 ? block <= 32 : top_k > 0 && block == 16;
+    const bool two = bits != 16 || (top_k > 0 && block == 16);
     out->workers = CUS * (two ? 2 : 1) / out->row_blocks;
     if (out->workers < 8) out->workers = 8;
     if (out->workers > MAX_TICKETS / out->row_blocks) out->workers = MAX_TICKETS / out->row_blocks;

@@ -31,6 +31,48 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
                                                       __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
+// The 32x32x16 product, of 32 query rows: with K rows as A, lane l gets the scores of query
+// row l % 32 at places key_of(e) + 4 * (l / 32), and its probabilities are in order its B
+// operands of the second product, of sixteen places each.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+template <int DT>
+__device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+    if constexpr (DT == BF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+                                                      __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ constexpr int key_of(int e) { return 8 * (e >> 2) + (e & 3); }
+
+// V rows in LDS, whole, for transposing loads: each takes 32 bytes of four rows for 16
+// lanes, so a row's chunks (16 bytes) are moved by 64 bytes from row to row and the four
+// lie in different banks.
+template <int D>
+__device__ __forceinline__ int v_chunk(int r, int c) {
+    return r * (D / 8) + (c ^ ((D == 128 ? r & 3 : (r >> 1) & 1) << 2));
+}
+// The second product's A operand of places r0 + 16 .. and elements 32 * i ..: eight places
+// in the order of the lane's probabilities.
+template <int D>
+__device__ __forceinline__ u32x4 turned_v(const u32x4* v, int lane, int r0, int i) {
+    const int g = lane >> 4, n = lane & 15;
+    u32x4 x;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        const int r = r0 + 8 * w + 4 * (g >> 1) + (n >> 2);
+        const int c = 4 * i + 2 * (g & 1) + ((n & 3) >> 1);
+        const char* at = (const char*)&v[v_chunk<D>(r, c)] + 8 * (n & 1);
+        const u32x2 y = __builtin_bit_cast(
+            u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)at));
+        x[2 * w] = y[0];
+        x[2 * w + 1] = y[1];
+    }
+    return x;
+}
+
 // two floats rounded to nearest even, the first in the low half
 template <int DT>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -81,6 +123,12 @@ template <int DT>
 __device__ __forceinline__ bool not_finite(uint32_t pair) {
     constexpr uint32_t E = DT == BF16 ? 0x7F80u : 0x7C00u;
     return (pair & E) == E || ((pair >> 16) & E) == E;
+}
+// the pair with zeros in place of what is not finite
+template <int DT>
+__device__ __forceinline__ uint32_t finite_part(uint32_t pair) {
+    return (not_finite<DT>(pair & 0xFFFFu) ? 0 : pair & 0xFFFFu) |
+           (not_finite<DT>(pair >> 16) ? 0 : pair & 0xFFFF0000u);
 }
 
 // One request's (or, with slot lists, one row's) positions: a list of `count`
@@ -150,6 +198,54 @@ __device__ __forceinline__ uint32_t resolve_entry(const PagedParams& c, uint32_t
     if (page < 0 || page >= c.num_pages) return NO_PLACE;
     at = c.page_shift >= 0 ? at & (c.page_size - 1) : at % c.page_size;
     return (uint32_t)page * page_stride + (uint32_t)at * pos_stride;
+}
+
+// A lookup in flight that loads in any case, from the first entry where there is none to
+// look up: with loads in branches the compiler does not know how many are on their way,
+// and waits for all of them where it needs the first.
+struct Lookup {
+    int32_t slot, entry;  // as loaded
+    int32_t pos;          // of the entry, -1: none
+    bool listed;          // the slot is the place's
+};
+struct Spot {
+    uint32_t page, at;
+    bool there;
+};
+
+template <bool SLOTS>
+__device__ __forceinline__ Lookup issue_lookup(const PagedParams& c, const Places& pl, int32_t j) {
+    Lookup e;
+    e.slot = -1;
+    e.listed = false;
+    int32_t pos = j;
+    if constexpr (SLOTS) {
+        e.listed = j >= 0 && j < pl.top_k;
+        e.slot = gload(pl.slots + (e.listed ? j : 0));
+        pos = e.listed ? -1 : pl.draft_pos + (j - pl.top_k);
+    }
+    e.pos = j < pl.count && pos >= 0 && pos < c.capacity ? pos : -1;
+    const int32_t at = e.pos < 0 ? 0 : e.pos;
+    e.entry = gload(pl.table + (c.page_shift >= 0 ? at >> c.page_shift : at / c.page_size));
+    return e;
+}
+template <bool SLOTS>
+__device__ __forceinline__ Spot resolve_lookup(const PagedParams& c, const Lookup& e) {
+    int32_t page = e.pos < 0 ? -1 : e.entry, at = e.pos;
+    if constexpr (SLOTS) {
+        if (e.listed) {
+            at = e.slot;
+            page = at < 0 ? -1 : c.page_shift >= 0 ? at >> c.page_shift : at / c.page_size;
+        }
+    }
+    Spot s;
+    s.there = page >= 0 && page < c.num_pages;
+    s.page = s.there ? (uint32_t)page : 0;
+    s.at = !s.there ? 0 : (uint32_t)(c.page_shift >= 0 ? at & (c.page_size - 1) : at % c.page_size);
+    return s;
+}
+__device__ __forceinline__ uint32_t spot_offset(const Spot& s, uint32_t page_stride, uint32_t pos_stride) {
+    return s.page * page_stride + s.at * pos_stride;
 }
 
 __device__ __forceinline__ uint32_t from_lane(uint32_t v, int lane) {

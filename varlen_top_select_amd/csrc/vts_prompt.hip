@@ -18,19 +18,6 @@
 
 namespace vts {
 
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-
-template <int DT>
-__device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
-    if constexpr (DT == BF16)
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
-                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-    else
-        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
-                                                      __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-}
-
 constexpr int PROMPT_WAVES = PROMPT_ROWS / 32;
 constexpr int PROMPT_NT = PROMPT_WAVES * 64;
 constexpr int PROMPT_KEYS = 64;  // of a tile
@@ -147,12 +134,6 @@ struct Prompt {
     static __device__ __forceinline__ int k_at(int r, int c) {
         return r * CH + (c ^ (D == 128 ? r & 15 : (r >> 1) & 7));
     }
-    // V's chunks are moved by 64 bytes from row to row, so that the four rows that a
-    // transposing load takes lie in different banks
-    static __device__ __forceinline__ int v_at(int r, int c) {
-        return r * CH + (c ^ ((D == 128 ? r & 3 : (r >> 1) & 1) << 2));
-    }
-
     __device__ __forceinline__ void load(int32_t j0) {
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
@@ -169,30 +150,9 @@ struct Prompt {
         for (int i = 0; i < LOADS; ++i) {
             const int x = i * PROMPT_NT + tid, r = x / CH, c = x % CH;
             sm.k[buf][k_at(r, c)] = kr[i];
-            sm.v[buf][v_at(r, c)] = vr[i];
+            sm.v[buf][v_chunk<D>(r, c)] = vr[i];
         }
     }
-    __device__ __forceinline__ static int key_of(int e) { return 8 * (e >> 2) + (e & 3); }
-
-    // V's operand of keys 16 * step .. and elements 32 * i ..: eight keys in the order
-    // of the lane's probabilities
-    __device__ __forceinline__ u32x4 operand_v(int buf, int step, int i) const {
-        const int g = lane >> 4, n = lane & 15;
-        u32x4 x;
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            const int r = 16 * step + 8 * w + 4 * (g >> 1) + (n >> 2);
-            const int c = 4 * i + 2 * (g & 1) + ((n & 3) >> 1);
-            const char* at = (const char*)&sm.v[buf][v_at(r, c)] + 8 * (n & 1);
-            const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s16x4*)at);
-            const u32x2 z = __builtin_bit_cast(u32x2, y);
-            x[2 * w] = z[0];
-            x[2 * w + 1] = z[1];
-        }
-        return x;
-    }
-
     template <bool MASKED>
     __device__ __forceinline__ void tile(int32_t j0, int buf) {
         const float c = p.scale_log2e;
@@ -244,7 +204,7 @@ struct Prompt {
 #pragma unroll
         for (int step = 0; step < 4; ++step)
 #pragma unroll
-            for (int i = 0; i < MT; ++i) o[i] = mfma32<DT>(operand_v(buf, step, i), pv[step], o[i]);
+            for (int i = 0; i < MT; ++i) o[i] = mfma32<DT>(turned_v<D>(sm.v[buf], lane, 16 * step, i), pv[step], o[i]);
     }
 
     // Where not every row sees every key, an infinity or NaN in V would reach rows that
@@ -259,8 +219,7 @@ struct Prompt {
             for (int e = 0; e < 4; ++e) {
                 const uint32_t w = vr[i][e];
                 f = f || not_finite<DT>(w);
-                vr[i][e] = (not_finite<DT>(w & 0xFFFFu) ? 0 : w & 0xFFFFu) |
-                           (not_finite<DT>(w >> 16) ? 0 : w & 0xFFFF0000u);
+                vr[i][e] = finite_part<DT>(w);
             }
         if (f) sm.bad = 1;
     }
