@@ -53,6 +53,7 @@ struct PromptParams {
     float* lse;  // or null
     int32_t clear;  // 1: rows of no sequence get zeros and -inf
     int32_t tiles;  // workgroups per KV head
+    int32_t direct;  // 1: 32 rows of K and of V span less than 2^31 bytes
 };
 
 hipError_t launch_write(int dtype, int head_dim, int bits, const WriteParams& p, hipStream_t stream);

@@ -207,6 +207,7 @@ int vts_prompt_attention(const vts_prompts* a, int32_t causal, float scale, void
     p.lse = lse;
     p.clear = clear != 0;
     p.tiles = (int32_t)tiles;
+    p.direct = a->k_strides[0] < (1 << 24) && a->v_strides[0] < (1 << 24);
     return status(launch_prompt(a->dtype, a->head_dim, p, static_cast<hipStream_t>(stream)));
 }
 

@@ -264,10 +264,27 @@ struct Prompt {
                                                0.6931471805599453f);
     }
 
+    // A tile that every row sees, from memory to half `buf` without the way through
+    // registers (32 of them, which the products' operands take).  LDS gets a wave's chunks
+    // one after the other, so a lane reads the chunk that lies at its place.
+    __device__ __forceinline__ void load_direct(int32_t j0, int buf) {
+        const int r = tid / CH, c = tid % CH;  // (of 256 chunks; the next ones are as many rows on)
+        const uint32_t ko = 2 * (uint32_t)(r * p.k_token) + 16 * (c ^ (D == 128 ? r & 15 : (r >> 1) & 7));
+        const uint32_t vo = 2 * (uint32_t)(r * p.v_token) + 16 * (c ^ ((D == 128 ? r & 3 : (r >> 1) & 1) << 2));
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int64_t row = t.k0 + j0 + i * (PROMPT_NT / CH);
+            to_lds(&sm.k[buf][i * PROMPT_NT + wave * 64], (const char*)p.k + 2 * (row * p.k_token + kv * p.k_head), ko);
+            to_lds(&sm.v[buf][i * PROMPT_NT + wave * 64], (const char*)p.v + 2 * (row * p.v_token + kv * p.v_head), vo);
+        }
+    }
+    static __device__ __forceinline__ void to_lds(u32x4* to, const char* base, uint32_t offset) {
+        __builtin_amdgcn_global_load_lds((const VTS_GLOBAL void*)((const VTS_GLOBAL char*)base + offset),
+                                         (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+    }
     // the tile at j0 to LDS, and the next one on its way
-    template <bool MASKED>
     __device__ __forceinline__ void next(int32_t j0, int32_t end, int buf) {
-        if constexpr (MASKED) clear_not_finite();
+        clear_not_finite();
         // the other half may still be read; this one was done with before the last barrier
         stage(buf);
         if (j0 + PROMPT_KEYS < end) load(j0 + PROMPT_KEYS);
@@ -280,20 +297,27 @@ struct Prompt {
         const int32_t end = !p.causal ? t.lk : last_row / p.group + 1 + t.lk - t.lq;
         const int32_t all = !p.causal ? t.lk : t.row0 / p.group + 1 + t.lk - t.lq;
         if (end > 0) {
-            load(0);
             if (tid == 0) sm.bad = 0;
-            __syncthreads();
             int32_t j0 = 0;
             int buf = 0;
+            if (p.direct && all >= PROMPT_KEYS) {
+                load_direct(0, 0);
 #pragma unroll 1
-            for (; j0 + PROMPT_KEYS <= all; j0 += PROMPT_KEYS, buf ^= 1) {
-                next<false>(j0, end, buf);
-                tile<false>(j0, buf);
+                for (; j0 + PROMPT_KEYS <= all; j0 += PROMPT_KEYS, buf ^= 1) {
+                    // this wave's part of the tile is there, and after the barrier everyone's;
+                    // all have done with the other half
+                    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                    __syncthreads();
+                    if (j0 + 2 * PROMPT_KEYS <= all) load_direct(j0 + PROMPT_KEYS, buf ^ 1);
+                    tile<false>(j0, buf);
+                }
             }
             const int32_t first = j0;
+            if (j0 < end) load(j0);
+            __syncthreads();
 #pragma unroll 1
             for (; j0 < end; j0 += PROMPT_KEYS, buf ^= 1) {
-                next<true>(j0, end, buf);
+                next(j0, end, buf);
                 tile<true>(j0, buf);
             }
             __syncthreads();
