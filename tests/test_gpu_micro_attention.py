@@ -138,6 +138,24 @@ def test_slots(bits, heads, kv, dim, top_k, tree, draft):
 
 
 @pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("heads,kv,dim,top_k,tree,draft,batch,dtype", [
+    (16, 4, 128, 70, True, 3, 12, BF16), (16, 4, 64, 33, False, 2, 16, F16), (64, 4, 128, 100, True, 2, 16, F16),
+    (96, 4, 128, 40, True, 1, 32, BF16), (8, 8, 64, 300, True, 2, 8, BF16), (128, 4, 128, 65, True, 1, 32, BF16)])
+def test_many_slot_lists(bits, heads, kv, dim, top_k, tree, draft, batch, dtype):
+    """A KV head to each wave, 16 and 32 rows, lists shared by several workgroups, and more rows."""
+    gen = torch.Generator().manual_seed(68)
+    lens = [(61 * x) % 190 for x in range(batch)]
+    caches, scales, deep, table, n = make_cache(gen, lens, 16, kv, dim, bits)
+    total = caches[0].shape[0] * 16
+    slots = torch.randint(0, total, (batch, draft, top_k), generator=gen).int()
+    slots[torch.rand(slots.shape, generator=gen) < 0.2] = -1
+    slots[1, 0] = -1
+    q = (0.7 * torch.randn(batch, draft, heads, dim, generator=gen)).to(dtype).to(DEV)
+    mask = random_mask(gen, batch, draft) if tree else None
+    check(q, caches, scales, deep, table, n, mask, slots.to(DEV))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
 def test_pages_that_are_not_there(bits):
     gen = torch.Generator().manual_seed(61)
     caches, scales, deep, table, n = make_cache(gen, [200, 100, 50], 16, 2, 128, bits)
@@ -152,7 +170,7 @@ def test_pages_that_are_not_there(bits):
 
 
 @pytest.mark.parametrize("bits", [4, 8])
-@pytest.mark.parametrize("draft,heads,kv", [(3, 8, 2), (4, 16, 4), (16, 8, 2), (40, 8, 2)])
+@pytest.mark.parametrize("draft,heads,kv", [(3, 8, 2), (4, 16, 4), (16, 8, 2), (40, 8, 2), (6, 16, 4)])
 def test_nan_where_it_is_not_seen(bits, draft, heads, kv):
     """Blocks of NaN behind the length, on pages of nobody, and at drafted tokens that some rows do
     not see: those rows get what they would get without them, and the rows that see them NaN."""

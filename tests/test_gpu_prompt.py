@@ -249,3 +249,27 @@ def test_k_and_v_past_4_gib():
     out = torch.empty_like(big)
     vts.prompt_attention(big, big, big, cu([200], first=n - 200), out=out)
     assert torch.equal(out[-200:], want)
+
+
+@pytest.mark.parametrize("lens,keys,dim", [([5, 3, 9], [5000, 4200, 6000], 64), ([2, 40], [4096, 4500], 128),
+                                           ([1, 0, 2, 1], [9000, 0, 4096, 4096], 64)])
+def test_few_queries_behind_long_contexts(lens, keys, dim):
+    """Sequences taken in the order of their lengths, with ties and empty ones."""
+    gen = torch.Generator().manual_seed(80)
+    q = (1.5 * torch.randn(sum(lens), 4, dim, generator=gen)).bfloat16().to(DEV)
+    k, v = (torch.randn(sum(keys), 2, dim, generator=gen).bfloat16().to(DEV) for _ in "kv")
+    check(q, k, v, cu(lens), cu(keys))
+
+
+def test_rows_far_apart():
+    """Keys 2^25 bytes and more from each other."""
+    gen = torch.Generator().manual_seed(81)
+    n, step = 70, (1 << 24) + 8
+    room = torch.empty(n * step, dtype=BF16, device=DEV)
+    k, v = (room[at:at + n * step - 4096].as_strided((n, 2, 64), (step, 64, 1)) for at in (0, 2048))
+    x = torch.randn(n, 8, 64, generator=gen).bfloat16().to(DEV)
+    k.copy_(x[:, 4:6])
+    v.copy_(x[:, 6:])
+    want, _ = vts.prompt_attention(x[:, :4], x[:, 4:6], x[:, 6:], cu([n]))
+    got, _ = vts.prompt_attention(x[:, :4], k, v, cu([n]))
+    assert torch.equal(got, want)

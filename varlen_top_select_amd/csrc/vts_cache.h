@@ -53,6 +53,7 @@ struct PromptParams {
     float* lse;  // or null
     int32_t clear;  // 1: rows of no sequence get zeros and -inf
     int32_t tiles;  // workgroups per KV head
+    int32_t longest_first;  // 1: at most 64 sequences, the longest first
     int32_t direct;  // 1: 32 rows of K and of V span less than 2^31 bytes
 };
 

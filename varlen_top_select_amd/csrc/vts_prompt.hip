@@ -47,11 +47,27 @@ __device__ __forceinline__ PromptTile find_tile(const PromptParams& p, int32_t t
     int32_t base = 0;
     for (int32_t b0 = 0; b0 < p.batch; b0 += 64) {
         const int32_t b = b0 + lane;
-        int32_t q0 = 0, len = 0;
+        int32_t q0 = 0, len = 0, k0 = 0, keys = 0;
         if (b < p.batch) {
             q0 = cu_at(p.cu_q, b, p.total_q);
+            k0 = cu_at(p.cu_k, b, p.total_k);
             len = cu_at(p.cu_q, b + 1, p.total_q) - q0;
+            keys = cu_at(p.cu_k, b + 1, p.total_k) - k0;
             if (len < 0) len = 0;
+            if (keys < 0) keys = 0;
+        }
+        if (p.longest_first) {
+            // each sequence to the lane of its place in the order of falling lengths
+            int32_t place = 0;
+            for (int32_t i = 0; i < p.batch; ++i) {
+                const int32_t n = __builtin_amdgcn_readlane(keys, i);
+                place += n > keys || (n == keys && i < lane) ? 1 : 0;
+            }
+            place = lane < p.batch ? place : lane;
+            q0 = __builtin_amdgcn_ds_permute(place << 2, q0);
+            k0 = __builtin_amdgcn_ds_permute(place << 2, k0);
+            len = __builtin_amdgcn_ds_permute(place << 2, len);
+            keys = __builtin_amdgcn_ds_permute(place << 2, keys);
         }
         const int32_t mine = (len * p.group + PROMPT_ROWS - 1) / PROMPT_ROWS;
         int32_t inc = mine;
@@ -70,9 +86,8 @@ __device__ __forceinline__ PromptTile find_tile(const PromptParams& p, int32_t t
             const int32_t first = base + __builtin_amdgcn_readlane(inc, at) - tiles;
             // the sequence's last tile, which sees the most, comes first
             r.row0 = (tiles - 1 - (t - first)) * PROMPT_ROWS;
-            r.k0 = __builtin_amdgcn_readfirstlane(cu_at(p.cu_k, b0 + at, p.total_k));
-            r.lk = __builtin_amdgcn_readfirstlane(cu_at(p.cu_k, b0 + at + 1, p.total_k)) - r.k0;
-            if (r.lk < 0) r.lk = 0;
+            r.k0 = __builtin_amdgcn_readlane(k0, at);
+            r.lk = __builtin_amdgcn_readlane(keys, at);
             return r;
         }
         base += __builtin_amdgcn_readlane(inc, 63);
