@@ -253,11 +253,15 @@ struct Writer {
         }
     }
 
+    // The inputs are read once, and leave the caches alone: 16384 tokens of 64 and 8 heads
+    // into a 4-bit cache and back take 160 us for 169, and 156 with such stores of q_out too
+    // (4.8 TB/s, as fast as a copy).
     __device__ __forceinline__ u32x4 load(const void* base, int64_t token_stride, int64_t head_stride,
                                           int32_t head, int32_t heads) const {
         u32x4 x = {0, 0, 0, 0};
         if (head < heads)
-            x = gload((const u32x4*)((const char*)base + 2 * (token * token_stride + head * head_stride)) + c);
+            x = __builtin_nontemporal_load(
+                (const VTS_GLOBAL u32x4*)((const char*)base + 2 * (token * token_stride + head * head_stride)) + c);
         return x;
     }
 
@@ -306,8 +310,15 @@ struct Writer {
                 turn<float>(raw, p.q_norm != nullptr, own, partner, y);
                 u32x4 out = pack8<DT>(y);
                 if (!valid) out = u32x4{0, 0, 0, 0};
-                if (head < p.heads)
-                    gstore((u32x4*)((char*)p.q_out + 2 * ((int64_t)token * p.heads + head) * D) + c, out);
+                if (head < p.heads) {
+                    u32x4* at = (u32x4*)((char*)p.q_out + 2 * ((int64_t)token * p.heads + head) * D) + c;
+                    // (where there are many tokens; what reads the queries of a few finds them
+                    // in the caches)
+                    if (p.parts == 1)
+                        __builtin_nontemporal_store(out, (VTS_GLOBAL u32x4*)at);
+                    else
+                        gstore(at, out);
+                }
             }
         }
         if (it < q_end + each) {
