@@ -665,6 +665,9 @@ int vts_read_cache(const vts_paged_cache* cache, const vts_microscales* scales, 
  * out        device, dtype[total_q, heads, head_dim], 16-byte aligned; must not
  *            overlap the inputs.
  * lse        device float[total_q, heads] or NULL.
+ * workspace  device, 16-byte aligned, at least vts_prompt_attention_workspace_bytes(...)
+ *            bytes, of any contents (NULL where that is 0: only few queries behind long
+ *            contexts take any).
  *
  * total_q * heads, total_k and batch are below 2^31 - 1024, and kv_heads *
  * (total_q * (heads / kv_heads) / 128 + batch) is at most 2^24 - 64.
@@ -686,8 +689,10 @@ typedef struct {
     int32_t head_dim;
     int32_t dtype;
 } vts_prompts;
+size_t vts_prompt_attention_workspace_bytes(int64_t batch, int64_t total_q, int64_t total_k, int32_t heads,
+                                            int32_t kv_heads, int32_t head_dim);
 int vts_prompt_attention(const vts_prompts* prompts, int32_t causal, float scale, void* out, float* lse,
-                         int32_t clear, void* stream);
+                         int32_t clear, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Human-readable text of a vts_status. */
 const char* vts_status_string(int status);

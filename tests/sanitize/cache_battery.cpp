@@ -48,7 +48,8 @@ hipError_t launch_read(int, int head_dim, int, const ReadParams& p, hipStream_t)
 hipError_t launch_prompt(int, int, const PromptParams& p, hipStream_t) {
     ++launched;
     expect("tiles hold the rows", (int64_t)p.tiles * PROMPT_ROWS + PROMPT_ROWS > (int64_t)p.total_q * p.group, 1);
-    expect("a grid", (int64_t)p.tiles * p.kv_heads + 64 <= 1 << 24, 1);
+    expect("a grid", (int64_t)p.tiles * p.kv_heads * p.splits + 64 <= 1 << 24, 1);
+    expect("splits", p.splits == 1 || (p.splits <= 32 && (int64_t)p.tiles * p.kv_heads * p.splits <= 512), 1);
     expect("scale", p.scale_log2e > 0, 1);
     return hipSuccess;
 }
@@ -121,7 +122,9 @@ int main() {
                                 a.kv_heads = kv;
                                 a.head_dim = dim;
                                 a.dtype = VTS_BF16;
-                                const int st = vts_prompt_attention(&a, 1, -0.1f, B, 0, 1, 0);
+                                const size_t need =
+                                    vts_prompt_attention_workspace_bytes(batch, n, n, heads, kv, dim);
+                                const int st = vts_prompt_attention(&a, 1, -0.1f, B, 0, 1, A, need, 0);
                                 expect("prompt", st == VTS_OK || (st == VTS_ERR_UNSUPPORTED && n >= (1 << 20)), 1);
                             }
                         }

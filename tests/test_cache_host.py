@@ -103,7 +103,7 @@ def test_null_structures(lib):
     assert lib.vts_write_cache(None, None, tokens(), None) == INVALID
     assert lib.vts_write_cache(cache(), None, None, None) == INVALID
     assert lib.vts_read_cache(None, None, A, 10, A, 2 * A, None) == INVALID
-    assert lib.vts_prompt_attention(None, 1, 1.0, A, None, 0, None) == INVALID
+    assert lib.vts_prompt_attention(None, 1, 1.0, A, None, 0, None, 0, None) == INVALID
     assert micro(lib, None) == INVALID
 
 
@@ -164,20 +164,33 @@ def prompts(**kw):
     (dict(qs=(-8, 128)), {}, INVALID), (dict(ks=(8 * 128, 100)), {}, INVALID), (dict(cu_q=None), {}, INVALID),
     (dict(cu_k=None), {}, INVALID), ({}, dict(out=None), INVALID), ({}, dict(out=A + 8), INVALID),
     ({}, dict(lse=A + 2), INVALID), ({}, dict(out=A, lse=A + 256), INVALID), ({}, dict(scale=math.nan), INVALID),
+    (dict(tq=4, tk=9000, batch=1), {}, WORKSPACE), (dict(tq=4, tk=9000, batch=1), dict(ws=A, bytes=100), WORKSPACE),
+    (dict(tq=4, tk=9000, batch=1), dict(ws=A + 8, bytes=1 << 40), WORKSPACE),
     (dict(tq=0, q=None), dict(out=None), OK),
 ])
 def test_prompt_refuses(lib, kw, call, want):
-    a = dict(causal=1, scale=0.1, out=1 << 30, lse=None, clear=0)
+    a = dict(causal=1, scale=0.1, out=1 << 30, lse=None, clear=0, ws=None, bytes=0)
     a.update(call)
     assert lib.vts_prompt_attention(prompts(**kw), a["causal"], a["scale"], a["out"], a["lse"], a["clear"],
-                                    None) == want
+                                    a["ws"], a["bytes"], None) == want
+
+
+def test_prompt_workspace(lib):
+    """Only few queries behind long contexts take any; shapes that no call has take none."""
+    f = lib.vts_prompt_attention_workspace_bytes
+    assert f(1, 16384, 16384, 32, 8, 128) == 0 and f(1, 16, 1000, 32, 8, 128) == 0
+    assert 0 < f(1, 16, 16384, 32, 8, 128) < 1 << 27
+    assert f(1, 1, 1 << 30, 1, 1, 128) == f(1, 1, 1 << 20, 1, 1, 128) > 0
+    for bad in ((-1, 1, 9000, 8, 8, 128), (1, -1, 9000, 8, 8, 128), (1, 1, 9000, 9, 8, 128), (1, 1, 9000, 8, 0, 128),
+                (1, 1 << 62, 9000, 8, 8, 128), (1, 1, 9000, 1 << 30, 1, 128), (1, 1, 9000, 8, 8, 0)):
+        assert f(*bad) == 0
 
 
 def test_valid_calls_reach_the_device(lib):
     if NO_GPU:
         for got in (lib.vts_write_cache(cache(), None, tokens(), None),
                     lib.vts_read_cache(cache(4), scales(), A, 10, A, 1 << 30, None),
-                    lib.vts_prompt_attention(prompts(), 1, 0.1, 1 << 30, None, 1, None),
+                    lib.vts_prompt_attention(prompts(), 1, 0.1, 1 << 30, None, 1, None, 0, None),
                     micro(lib, scales())):
             assert got in (HIP, UNSUPPORTED)
 

@@ -226,6 +226,7 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     if scale is None:
         scale = 1.0 / math.sqrt(head_dim)
     lib = library()
+    need = lib.vts_prompt_attention_workspace_bytes(batch, total_q, total_k, heads, kv_heads, head_dim)
     packed = _PROMPTS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), *qs, *ks, *vs, cu_seqlens.data_ptr(),
                            cu_seqlens_k.data_ptr(), batch, total_q, total_k, heads, kv_heads, head_dim,
                            _DTYPE[dtype])
@@ -233,9 +234,11 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     def call(sp):
         o = q.new_empty((total_q, heads, head_dim)) if out is None else out
         lse = q.new_empty((total_q, heads), dtype=torch.float32) if return_lse else None
+        # (of any contents, so it is the call's own, also in a captured graph)
+        ws = q.new_empty(need, dtype=torch.uint8) if need else None
         _check("vts_prompt_attention", lib.vts_prompt_attention(
             packed, bool(causal), scale, o.data_ptr(), lse.data_ptr() if return_lse else None,
-            out is None, sp))
+            out is None, ws.data_ptr() if need else None, need, sp))
         return o, lse
 
     return _run(stream, index, call)
@@ -274,4 +277,6 @@ def declare(lib):
     lib.vts_read_cache.restype = ctypes.c_int
     lib.vts_read_cache.argtypes = [vp, vp, vp, i64, vp, vp, vp]
     lib.vts_prompt_attention.restype = ctypes.c_int
-    lib.vts_prompt_attention.argtypes = [vp, i32, f32, vp, vp, i32, vp]
+    lib.vts_prompt_attention.argtypes = [vp, i32, f32, vp, vp, i32, vp, ctypes.c_size_t, vp]
+    lib.vts_prompt_attention_workspace_bytes.restype = ctypes.c_size_t
+    lib.vts_prompt_attention_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, i32]

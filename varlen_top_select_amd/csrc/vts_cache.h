@@ -52,7 +52,10 @@ struct PromptParams {
     void* out;
     float* lse;  // or null
     int32_t clear;  // 1: rows of no sequence get zeros and -inf
-    int32_t tiles;  // workgroups per KV head
+    int32_t tiles;   // of 128 rows, per KV head, at most
+    int32_t splits;  // workgroups that share a tile's keys
+    // their parts: [tiles][kv_heads][splits][128] rows of head_dim outputs, and of maximum and sum
+    float *part_o, *part_ml;
     int32_t longest_first;  // 1: at most 64 sequences, the longest first
     int32_t direct;  // 1: 32 rows of K and of V span less than 2^31 bytes
 };

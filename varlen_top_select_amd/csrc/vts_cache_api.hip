@@ -32,6 +32,31 @@ int check_rows(const void* p, const int64_t* strides, int64_t n, int64_t heads) 
     return VTS_OK;
 }
 
+struct PromptPlan {
+    int64_t tiles;
+    int32_t splits;
+    size_t part_ml, total;
+};
+
+// Two workgroups to a compute unit fill the device: where there are half as many tiles or fewer,
+// and on average 1024 keys or more to a sequence, a tile's keys are shared, 512 or more to each
+// (one request's 16 queries of 32 heads behind 16400 keys: 60 us for 292; four of them behind
+// 2060 to 4100: 32 for 78; two of 128 behind 4100 and 8200: 53 for 152).
+PromptPlan prompt_plan(int64_t batch, int64_t total_q, int64_t total_k, int32_t heads, int32_t kv_heads,
+                       int32_t head_dim) {
+    PromptPlan plan;
+    plan.tiles = total_q * (heads / kv_heads) / PROMPT_ROWS + (batch < total_q ? batch : total_q);
+    const int64_t keys = batch > 0 ? total_k / batch : 0, work = plan.tiles * kv_heads;
+    int64_t n = work > 0 && keys >= 1024 ? 512 / work : 1;
+    if (n > keys / 512) n = keys / 512;
+    if (n > 32) n = 32;
+    plan.splits = n < 2 ? 1 : (int32_t)n;
+    const size_t rows = plan.splits > 1 ? (size_t)work * plan.splits * PROMPT_ROWS : 0;
+    plan.part_ml = align256(rows * head_dim * 4);
+    plan.total = plan.part_ml + align256(rows * 2 * 4);
+    return plan;
+}
+
 int status(hipError_t e) { return e == hipSuccess ? VTS_OK : VTS_ERR_HIP; }
 
 }  // namespace
@@ -153,8 +178,17 @@ int vts_read_cache(const vts_paged_cache* cache, const vts_microscales* scales, 
                               static_cast<hipStream_t>(stream)));
 }
 
+size_t vts_prompt_attention_workspace_bytes(int64_t batch, int64_t total_q, int64_t total_k, int32_t heads,
+                                            int32_t kv_heads, int32_t head_dim) {
+    if (batch < 0 || total_q < 0 || total_k < 0 || kv_heads < 1 || heads < kv_heads || heads > MAX_HEADS ||
+        heads % kv_heads != 0 || head_dim < 1 || head_dim > 1024 || batch > INT32_MAX || total_k > INT32_MAX ||
+        total_q > INT32_MAX / heads)
+        return 0;
+    return prompt_plan(batch, total_q, total_k, heads, kv_heads, head_dim).total;
+}
+
 int vts_prompt_attention(const vts_prompts* a, int32_t causal, float scale, void* out, float* lse,
-                         int32_t clear, void* stream) {
+                         int32_t clear, void* workspace, size_t workspace_bytes, void* stream) {
     PromptParams p;
     memset(&p, 0, sizeof(p));
     if (a == nullptr || isnan(scale)) return VTS_ERR_INVALID;
@@ -178,9 +212,11 @@ int vts_prompt_attention(const vts_prompts* a, int32_t causal, float scale, void
     if (out == nullptr || !aligned(out, 16)) return VTS_ERR_INVALID;
     if (lse && (!aligned(lse, 4) || overlap(out, rows * a->head_dim * 2, lse, rows * 4))) return VTS_ERR_INVALID;
     p.group = a->heads / a->kv_heads;
-    const int64_t tiles = a->total_q * p.group / PROMPT_ROWS + (a->batch < a->total_q ? a->batch : a->total_q);
+    const PromptPlan plan = prompt_plan(a->batch, a->total_q, a->total_k, a->heads, a->kv_heads, a->head_dim);
     // (a grid has below 2^32 threads)
-    if (tiles * a->kv_heads > (1 << 24) - 64) return VTS_ERR_UNSUPPORTED;
+    if (plan.tiles * a->kv_heads > (1 << 24) - 64) return VTS_ERR_UNSUPPORTED;
+    if (plan.total > 0 && (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < plan.total))
+        return VTS_ERR_WORKSPACE;
     st = check_device(stream);
     if (st != VTS_OK) return st;
     p.q = a->q;
@@ -206,7 +242,10 @@ int vts_prompt_attention(const vts_prompts* a, int32_t causal, float scale, void
     p.out = out;
     p.lse = lse;
     p.clear = clear != 0;
-    p.tiles = (int32_t)tiles;
+    p.tiles = (int32_t)plan.tiles;
+    p.splits = plan.splits;
+    p.part_o = static_cast<float*>(workspace);
+    p.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + (plan.total > 0 ? plan.part_ml : 0));
     // The last workgroups to start are then those of the shortest sequences (8 times 512
     // queries behind up to 16384 keys: 1608 us for 1635); finding the order takes a workgroup
     // half a microsecond, and is left where its work is a few.

@@ -13,6 +13,9 @@
 // at keys 8 * (e / 4) + 4 * (l / 32) + e % 4: its sixteen probabilities are already
 // its B operands of the second product, with V's keys taken in the same order by
 // transposing LDS loads.  m is raised only when a score passes it by a margin.
+//
+// Where there are few tiles and long contexts, several workgroups take parts of a tile's
+// keys, and a second kernel joins them.
 #include "vts_cache.h"
 #include "vts_paged.hpp"
 
@@ -258,6 +261,22 @@ struct Prompt {
         }
     }
 
+    // The row as a part of its keys gives it: outputs that are not divided, maximum and sum.
+    __device__ __forceinline__ void write_part(int64_t part) {
+        l += __shfl_xor(l, 32);
+        if (!valid) return;
+        const int64_t at = part * PROMPT_ROWS + wave * 32 + col;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+                gstore((f32x4*)(p.part_o + at * D + 32 * i + key_of(e) + 4 * half),
+                       f32x4{o[i][e], o[i][e + 1], o[i][e + 2], o[i][e + 3]});
+        if (half == 0) {
+            gstore(p.part_ml + 2 * at, m);
+            gstore(p.part_ml + 2 * at + 1, l);
+        }
+    }
     __device__ __forceinline__ void write() {
         l += __shfl_xor(l, 32);
         if (!valid) return;
@@ -305,18 +324,26 @@ struct Prompt {
         if (j0 + PROMPT_KEYS < end) load(j0 + PROMPT_KEYS);
         __syncthreads();
     }
-    __device__ __forceinline__ void run() {
+    // Part `split` of the keys.
+    __device__ __forceinline__ void run(int32_t split) {
         // the keys that the last token of the tile sees, and those that all rows see
         const int32_t rows = t.lq * p.group;
         const int32_t last_row = t.row0 + PROMPT_ROWS < rows ? t.row0 + PROMPT_ROWS - 1 : rows - 1;
-        const int32_t end = !p.causal ? t.lk : last_row / p.group + 1 + t.lk - t.lq;
-        const int32_t all = !p.causal ? t.lk : t.row0 / p.group + 1 + t.lk - t.lq;
-        if (end > 0) {
+        int32_t end = !p.causal ? t.lk : last_row / p.group + 1 + t.lk - t.lq;
+        int32_t all = !p.causal ? t.lk : t.row0 / p.group + 1 + t.lk - t.lq;
+        int32_t j0 = 0;
+        if (p.splits > 1 && end > 0) {
+            const int64_t tiles = (end + PROMPT_KEYS - 1) / PROMPT_KEYS;
+            j0 = (int32_t)(tiles * split / p.splits) * PROMPT_KEYS;
+            const int32_t to = (int32_t)(tiles * (split + 1) / p.splits) * PROMPT_KEYS;
+            if (to < end) end = to;
+            if (to < all) all = to;
+        }
+        if (j0 < end) {
             if (tid == 0) sm.bad = 0;
-            int32_t j0 = 0;
             int buf = 0;
-            if (p.direct && all >= PROMPT_KEYS) {
-                load_direct(0, 0);
+            if (p.direct && j0 + PROMPT_KEYS <= all) {
+                load_direct(j0, 0);
 #pragma unroll 1
                 for (; j0 + PROMPT_KEYS <= all; j0 += PROMPT_KEYS, buf ^= 1) {
                     // this wave's part of the tile is there, and after the barrier everyone's;
@@ -338,14 +365,13 @@ struct Prompt {
             __syncthreads();
             if (sm.bad) add_not_finite(first, end);
         }
-        write();
     }
 };
 
 template <int DT, int D>
 __global__ __launch_bounds__(PROMPT_NT, 2) void prompt_kernel(PromptParams p) {
     __shared__ PromptShared<D> sm;
-    const int32_t work = p.tiles * p.kv_heads;
+    const int32_t work = p.tiles * p.kv_heads * p.splits;
     if ((int32_t)blockIdx.x >= work) {
         // rows of no sequence, before the first and behind the last
         const int32_t a = p.batch > 0 ? cu_at(p.cu_q, 0, p.total_q) : 0;
@@ -359,17 +385,66 @@ __global__ __launch_bounds__(PROMPT_NT, 2) void prompt_kernel(PromptParams p) {
         }
         return;
     }
-    const int32_t kv = (int32_t)blockIdx.x % p.kv_heads;
-    const PromptTile t = find_tile(p, (int32_t)blockIdx.x / p.kv_heads);
+    const int32_t kv = (int32_t)blockIdx.x % p.kv_heads, x = (int32_t)blockIdx.x / p.kv_heads;
+    const int32_t n = x / p.splits, split = x - n * p.splits;
+    const PromptTile t = find_tile(p, n);
     if (!t.found) return;
     Prompt<DT, D> a(p, sm, t, kv);
-    a.run();
+    a.run(split);
+    if (p.splits > 1)
+        a.write_part(((int64_t)n * p.kv_heads + kv) * p.splits + split);
+    else
+        a.write();
+}
+
+// The parts of a tile's rows joined, in their order: 32 rows to a workgroup.
+constexpr int JOIN_ROWS = 32;
+template <int DT, int D>
+__global__ __launch_bounds__(PROMPT_NT) void prompt_join_kernel(PromptParams p) {
+    constexpr float SHIFT = DT == F16 ? 11 : 0;
+    constexpr int PER = PROMPT_ROWS / JOIN_ROWS;
+    const int32_t x = (int32_t)blockIdx.x / PER, first = (int32_t)blockIdx.x % PER * JOIN_ROWS;
+    const int32_t kv = x % p.kv_heads, n = x / p.kv_heads;
+    const PromptTile t = find_tile(p, n);
+    if (!t.found) return;
+    for (int32_t y = (int32_t)threadIdx.x * 4; y < JOIN_ROWS * D; y += PROMPT_NT * 4) {
+        const int32_t r = first + y / D, d = y % D, row = t.row0 + r, token = row / p.group;
+        if (token >= t.lq) continue;
+        const int64_t part = ((int64_t)n * p.kv_heads + kv) * p.splits;
+        float top = NEG_INF, sum = 0;
+        f32x4 o = {0, 0, 0, 0};
+        for (int32_t s = 0; s < p.splits; ++s) {
+            const int64_t at = (part + s) * PROMPT_ROWS + r;
+            const float m = gload(p.part_ml + 2 * at), l = gload(p.part_ml + 2 * at + 1);
+            const f32x4 v = gload((const f32x4*)(p.part_o + at * D + d));
+            const float up = fmaxf(top, m);
+            const float f = up == NEG_INF ? 1.0f : __builtin_amdgcn_exp2f(top - up);
+            const float g = up == NEG_INF ? 1.0f : __builtin_amdgcn_exp2f(m - up);
+            top = up;
+            sum = sum * f + l * g;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = o[e] * f + v[e] * g;
+        }
+        const bool none = sum == 0.0f;
+        const float inv = 1.0f / sum;
+        const int64_t out = (int64_t)(t.q0 + token) * p.heads + kv * p.group + (row - token * p.group);
+        u32x2 w;
+        w[0] = none ? 0 : pack2<DT>(o[0] * inv, o[1] * inv);
+        w[1] = none ? 0 : pack2<DT>(o[2] * inv, o[3] * inv);
+        gstore((u32x2*)((char*)p.out + 2 * (out * D + d)), w);
+        if (d == 0 && p.lse)
+            gstore(p.lse + out, none ? NEG_INF
+                                     : (top + SHIFT + log2f(sum * __builtin_exp2f(-SHIFT))) * 0.6931471805599453f);
+    }
 }
 
 template <int DT, int D>
 static hipError_t start(const PromptParams& p, hipStream_t stream) {
-    const uint32_t grid = (uint32_t)(p.tiles * p.kv_heads + (p.clear ? 64 : 0));
+    const uint32_t grid = (uint32_t)(p.tiles * p.kv_heads * p.splits + (p.clear ? 64 : 0));
     hipLaunchKernelGGL((prompt_kernel<DT, D>), dim3(grid), dim3(PROMPT_NT), 0, stream, p);
+    if (p.splits > 1)
+        hipLaunchKernelGGL((prompt_join_kernel<DT, D>), dim3(p.tiles * p.kv_heads * (PROMPT_ROWS / JOIN_ROWS)),
+                           dim3(PROMPT_NT), 0, stream, p);
     return hipGetLastError();
 }
 
