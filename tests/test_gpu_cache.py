@@ -65,6 +65,8 @@ CASES = [
     (2, 64, 8, 128, 96, False, True, 8, 32, None, F16),
     (5000, 2, 1, 128, 128, False, True, 4, 64, None, BF16),
     (300, 12, 12, 64, 16, True, True, 4, 16, None, BF16),
+    (9, 6, 3, 128, 0, False, True, 4, 16, None, BF16),   # norms alone
+    (9, 5, 2, 64, 0, False, True, 16, 16, None, F16),
 ]
 
 
@@ -321,3 +323,108 @@ def test_page_slots():
     table = torch.tensor([[3, 1, -1], [0, 2, 5]], dtype=torch.int32, device=DEV)
     pos = torch.tensor([[0, 17, 40, -1], [15, 16, 47, 48]], dtype=torch.int32, device=DEV)
     assert vts.page_slots(table, 16, pos).tolist() == [[48, 17, -1, -1], [15, 32, 95, -1]]
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+def test_one_of_the_norms(bits):
+    gen = torch.Generator().manual_seed(4)
+    q, k, v = make_tokens(gen, 21, 6, 2, 64, BF16)
+    (kc, vc), (ks, vs) = make_cache(gen, 3, 16, 2, 64, bits, BF16)
+    w = torch.randn(64, generator=gen).to(DEV)
+    slots = torch.arange(21, dtype=torch.int32, device=DEV)
+    for qn, kn in ((w, None), (None, w)):
+        got_q, got_k = vts.write_cache(q, k, v, slots, kc, vc, k_scales=ks, v_scales=vs, q_norm=qn, k_norm=kn,
+                                       return_k=True)
+        for got, x, n in ((got_q, q, qn), (got_k, k, kn)):
+            y, m = ref.ready(x, n, 1e-6, None, None, False)
+            assert ((got.cpu().double() - y).abs() <= ref.ready_bound(y, m, 64, BF16)).all()
+            if n is None:
+                assert torch.equal(got, x)
+
+
+def test_infinities_and_nan_in_rows():
+    """They stay in their row (and its pair), are kept by a 16-bit cache, and make a microscaled block
+    NaN."""
+    gen = torch.Generator().manual_seed(5)
+    q, k, v = make_tokens(gen, 6, 4, 2, 64, BF16)
+    q[1, 2, 40] = math.inf
+    k[2, 1, 3] = math.nan
+    v[3, 0, 33] = -math.inf
+    table, slots = vts.rotary_table(64, 32, device=DEV), torch.arange(6, dtype=torch.int32, device=DEV)
+    kw = dict(positions=slots, rotary=table, return_k=True)
+    (kc, vc), _ = make_cache(gen, 1, 16, 2, 64, 16, BF16)
+    got_q, got_k = vts.write_cache(q, k, v, slots, kc, vc, **kw)
+    assert got_q[1, 2, 40] == math.inf and int((~got_q.isfinite()).sum()) == 1  # (not turned)
+    bad = ~got_k.isfinite()
+    assert bad[2, 1, 3] and bad[2, 1, 19] and int(bad.sum()) == 2
+    assert torch.equal(at_slots(vc, slots).view(torch.int16), v.cpu().contiguous().view(torch.int16))
+    (kc, vc), (ks, vs) = make_cache(gen, 1, 16, 2, 64, 8, BF16)
+    vts.write_cache(q, k, v, slots, kc, vc, k_scales=ks, v_scales=vs, **kw)
+    kk, vv = vts.read_cache(kc, vc, slots, k_scales=ks, v_scales=vs)
+    assert kk[2, 1, :32].isnan().all() and int(kk.isnan().sum()) == 32
+    assert vv[3, 0, 32:].isnan().all() and int(vv.isnan().sum()) == 32
+
+
+def test_refusals():
+    gen = torch.Generator().manual_seed(6)
+    q, k, v = make_tokens(gen, 8, 4, 2, 64, BF16)
+    (kc, vc), (ks, vs) = make_cache(gen, 2, 16, 2, 64, 4, BF16)
+    (k16, v16), _ = make_cache(gen, 2, 16, 2, 64, 16, BF16)
+    slots = torch.arange(8, dtype=torch.int32, device=DEV)
+    table = vts.rotary_table(64, 32, device=DEV)
+    mx = dict(k_scales=ks, v_scales=vs)
+    own = torch.zeros(8, 4, 64, dtype=BF16, device=DEV)
+
+    def write(q=q, k=k, v=v, slots=slots, kc=kc, vc=vc, **kw):
+        vts.write_cache(q, k, v, slots, kc, vc, **{**mx, **kw})
+
+    write()
+    for match, kw in [
+        ("k must", dict(k=k[:7])), ("k must", dict(k=k.float())), ("v must", dict(v=v[:, :1])),
+        ("head_dim", dict(q=torch.zeros(8, 4, 128, dtype=BF16, device=DEV))), ("q rows", dict(q=q[..., :64:2])),
+        ("slots", dict(slots=slots.long())), ("slots", dict(slots=slots.cpu())), ("slots", dict(slots=slots[:7])),
+        ("together", dict(positions=slots)), ("together", dict(rotary=table)),
+        ("rotary", dict(positions=slots, rotary=table.double())),
+        ("rotary", dict(positions=slots, rotary=table[:, :24].contiguous())),
+        ("rotary", dict(positions=slots, rotary=torch.zeros(9, 128, device=DEV))),
+        ("positions", dict(positions=slots[:3], rotary=table)),
+        ("q_norm", dict(q_norm=torch.ones(64, device=DEV).half())), ("k_norm", dict(k_norm=torch.ones(32, device=DEV))),
+        ("eps", dict(eps=-1.0)), ("eps", dict(eps=math.nan)),
+        ("q_out", dict(q_out=own[:7])), ("q_out", dict(q_out=own.float())),
+        ("k_cache", dict(kc=k16)), ("shapes of K's|rows must be", dict(vc=vc[:, :, :1])),
+        ("k_cache", dict(kc=kc[..., ::2])), ("together", dict(v_scales=None)),
+        ("scales", dict(k_scales=ks[:1])), ("4-D uint8", dict(v_scales=vs.int())),
+    ]:
+        with pytest.raises(ValueError, match=match):
+            write(**kw)
+    with pytest.raises(ValueError, match="overlap"):
+        vts.write_cache(own, k, v, slots, kc, vc, q_out=own, **mx)
+    with pytest.raises(ValueError, match="own dtype"):
+        vts.write_cache(q.half(), k, v, slots, k16, v16)
+    with pytest.raises(ValueError, match="own dtype"):
+        vts.read_cache(k16, v16, slots, dtype=F16)
+    with pytest.raises(ValueError, match="bfloat16 or float16"):
+        vts.read_cache(kc, vc, slots, dtype=torch.float32, **mx)
+    for bad in (slots.long(), slots.cpu(), torch.arange(16, dtype=torch.int32, device=DEV)[::2], [1, 2]):
+        with pytest.raises(ValueError, match="slots"):
+            vts.read_cache(kc, vc, bad, **mx)
+    cu = torch.tensor([0, 8], dtype=torch.int32, device=DEV)
+    for match, args, kw in [
+        ("cu_seqlens", (q, k, v, cu.long()), {}), ("cu_seqlens", (q, k, v, cu.cpu()), {}),
+        ("cu_seqlens_k", (q, k, v, cu), dict(cu_seqlens_k=cu[:1])), ("dtype", (q.float(), k, v, cu), {}),
+        ("k must", (q, k.half(), v, cu), {}), ("v must", (q, k, v[:7], cu), {}),
+        ("multiple", (q[:, :3], k, v, cu), {}), ("out", (q, k, v, cu), dict(out=own[:7])),
+        ("overlap", (own, k, v, cu), dict(out=own)), ("head_dim", (q[..., :32], k[..., :32], v[..., :32], cu), {}),
+    ]:
+        with pytest.raises(ValueError, match=match):
+            vts.prompt_attention(*args, **kw)
+    lens, pages = torch.tensor([8], dtype=torch.int32, device=DEV), torch.zeros(1, 2, dtype=torch.int32, device=DEV)
+    q4 = own.view(1, 8, 4, 64)
+    for match, args, kw in [
+        ("q dtype", (q4.float(), kc, vc, pages, lens), mx), ("k_cache", (q4, k16, v16, pages, lens), mx),
+        ("k_cache dtype", (q4, kc, vc, pages, lens), {}), ("head_dim", (q4[..., :32], kc, vc, pages, lens), mx),
+        ("together", (q4, kc, vc, pages, lens), dict(k_scales=ks)),
+        ("overlap", (q4, kc, vc, pages, lens), dict(out=q4, **mx)),
+    ]:
+        with pytest.raises(ValueError, match=match):
+            vts.tree_attention(*args, **kw)

@@ -633,35 +633,34 @@ struct Attend {
     // Wide: the thread's chunks of a unit.  PAIRS of the same place and number of K and of V,
     // or, where the unit's K has fewer chunks than there are threads, one of K or of V.
     static constexpr int PAIRS = HALF >= T ? HALF / T : 0;
-    static constexpr bool RAGGED = 2 * HALF < T;  // (then only the first threads have one)
     __device__ __forceinline__ int place_of(int i) const { return (i * T + tid) % HALF / CHF; }
     __device__ __forceinline__ bool thread_v() const { return PAIRS == 0 && tid >= HALF; }
-    __device__ __forceinline__ void load_chunk(int to, const Spot& at, bool is_v, bool mine) {
+    __device__ __forceinline__ void load_chunk(int to, const Spot& at, bool is_v) {
         const CacheView& view = is_v ? p.c.v : p.c.k;
         const ScaleView& s = is_v ? p.v_scale : p.k_scale;
-        const int chunk = mine ? tid % CHF : 0;
-        here[to] = mine && at.there;
+        const int chunk = tid % CHF;
+        here[to] = at.there;
         k[to] = row_load<u32x4>(is_v ? vbase : kbase, spot_offset(at, view.page_stride, view.pos_stride), chunk * 16);
         sc_next[to] = ((const VTS_GLOBAL uint8_t*)s.base)
             [((uint64_t)spot_offset(at, s.page_stride, s.pos_stride) + (uint64_t)head_unit * s.head_stride) * BLOCKS +
              chunk * BLOCKS / CHF];
     }
-    static_assert(!BLOCK || (T % CHF == 0 && (PAIRS == 0 ? 2 * HALF <= T : HALF % T == 0)), "chunks of a thread");
+    static_assert(!BLOCK || (T % CHF == 0 && (PAIRS == 0 ? 2 * HALF == T : HALF % T == 0)), "chunks of a thread");
     static constexpr int LOOKUPS = PAIRS ? PAIRS : 1;  // places of a thread's chunks
     __device__ __forceinline__ void issue_wide(Lookup (&e)[LOOKUPS], int32_t u) const {
 #pragma unroll
         for (int i = 0; i < LOOKUPS; ++i)
-            e[i] = issue_lookup<SLOTS>(p.c, pl, !RAGGED || tid < 2 * HALF ? u * S::PLACES + place_of(i) : -1);
+            e[i] = issue_lookup<SLOTS>(p.c, pl, u * S::PLACES + place_of(i));
     }
     __device__ __forceinline__ void load_wide_micro(int to, const Lookup (&e)[LOOKUPS]) {
 #pragma unroll
         for (int i = 0; i < LOOKUPS; ++i) {
             const Spot at = resolve_lookup<SLOTS>(p.c, e[i]);
             if constexpr (PAIRS) {
-                load_chunk(to * LOADSF + 2 * i, at, false, true);
-                load_chunk(to * LOADSF + 2 * i + 1, at, true, true);
+                load_chunk(to * LOADSF + 2 * i, at, false);
+                load_chunk(to * LOADSF + 2 * i + 1, at, true);
             } else {
-                load_chunk(to, at, thread_v(), !RAGGED || tid < 2 * HALF);
+                load_chunk(to, at, thread_v());
             }
         }
     }
@@ -671,7 +670,6 @@ struct Attend {
         constexpr int OUT = CH / CHF;  // 16-byte chunks of operands from one
 #pragma unroll
         for (int i = 0; i < LOADSF; ++i) {
-            if (RAGGED && tid >= 2 * HALF) continue;
             const bool is_v = PAIRS ? i & 1 : thread_v();
             const int r = place_of(PAIRS ? i / 2 : 0), chunk = tid % CHF;
             const float scale = scale_of(sc_next[from * LOADSF + i]);
