@@ -49,10 +49,15 @@ __device__ __forceinline__ constexpr int key_of(int e) { return 8 * (e >> 2) + (
 
 // V rows in LDS, whole, for transposing loads: each takes 32 bytes of four rows for 16
 // lanes, so a row's chunks (16 bytes) are moved by 64 bytes from row to row and the four
-// lie in different banks.
+// lie in different banks; and by one chunk within them, so that a store of one chunk in
+// four to several rows meets in no bank either.
+template <int D>
+__device__ __forceinline__ int v_swizzle(int r) {
+    return D == 128 ? (r & 3) * 5 : ((r >> 1) & 1) << 2 | ((r >> 1) & 3);
+}
 template <int D>
 __device__ __forceinline__ int v_chunk(int r, int c) {
-    return r * (D / 8) + (c ^ ((D == 128 ? r & 3 : (r >> 1) & 1) << 2));
+    return r * (D / 8) + (c ^ v_swizzle<D>(r));
 }
 // The second product's A operand of places r0 + 16 .. and elements 32 * i ..: eight places
 // in the order of the lane's probabilities.

@@ -185,11 +185,11 @@ struct Prompt {
             for (int b = 0; b < 2; ++b)
                 s[b] = mfma32<DT>(sm.k[buf][k_at(32 * b + col, 2 * ks + half)], q[ks], s[b]);
         if constexpr (MASKED) {
+            const int32_t last = limit - j0 - 4 * half;
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    s[b][e] = j0 + 32 * b + key_of(e) + 4 * half <= limit ? s[b][e] : NEG_INF;
+                for (int e = 0; e < 16; ++e) s[b][e] = 32 * b + key_of(e) <= last ? s[b][e] : NEG_INF;
         }
         float top = s[0][0];
 #pragma unroll
@@ -304,7 +304,7 @@ struct Prompt {
     __device__ __forceinline__ void load_direct(int32_t j0, int buf) {
         const int r = tid / CH, c = tid % CH;  // (of 256 chunks; the next ones are as many rows on)
         const uint32_t ko = 2 * (uint32_t)(r * p.k_token) + 16 * (c ^ (D == 128 ? r & 15 : (r >> 1) & 7));
-        const uint32_t vo = 2 * (uint32_t)(r * p.v_token) + 16 * (c ^ ((D == 128 ? r & 3 : (r >> 1) & 1) << 2));
+        const uint32_t vo = 2 * (uint32_t)(r * p.v_token) + 16 * (c ^ v_swizzle<D>(r));
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
             const int64_t row = t.k0 + j0 + i * (PROMPT_NT / CH);
