@@ -239,6 +239,18 @@ def test_page_slots():
     assert vts.page_slots(table, 16, pos.int()).dtype == torch.int32
 
 
+def test_page_slots_at_the_ends():
+    """Entries whose slots pass 32 bits (2^28 + 3 pages of 16 came back as page 3), and tables
+    without columns."""
+    pos = torch.tensor([[5], [5], [15]])
+    table = torch.tensor([[2**28 + 3], [2**27], [2**27 - 1]], dtype=torch.int32)
+    assert vts.page_slots(table, 16, pos).tolist() == [[-1], [-1], [2**31 - 1]]
+    assert vts.page_slots(table[:, :0], 16, pos).tolist() == [[-1], [-1], [-1]]
+    assert vts.page_slots(table[:0], 16, pos[:0]).shape == (0, 1)
+    with pytest.raises(ValueError, match="page_size"):
+        vts.page_slots(table, 0, pos)
+
+
 @pytest.mark.parametrize("bits", [4, 8])
 def test_reference_formats(bits):
     """The oracle's numbers: every value is its own nearest, ties go to the even code, and the

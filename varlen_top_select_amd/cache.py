@@ -257,14 +257,19 @@ def rotary_table(max_position: int, rot: int, *, base: float = 10000.0, device=N
 
 def page_slots(page_table: torch.Tensor, page_size: int, positions: torch.Tensor) -> torch.Tensor:
     """int32 slots of ``positions`` [batch, n] in the requests' pages (page_table [batch, width]): -1
-    where a position is negative or past the table, or its entry is negative."""
+    where a position is negative or past the table, its entry is negative, or the slot no int32."""
     if page_table.dim() != 2 or positions.dim() != 2 or positions.shape[0] != page_table.shape[0]:
         raise ValueError("page_table and positions must be 2-D, with a row to each request")
+    if page_size < 1:
+        raise ValueError("page_size must be positive")
+    if page_table.shape[1] == 0:
+        return torch.full_like(positions, -1, dtype=torch.int32)
     pos = positions.long()
     page = torch.div(pos, page_size, rounding_mode="floor")
     known = (pos >= 0) & (page < page_table.shape[1])
     entry = page_table.long().gather(1, torch.where(known, page, 0))
-    return torch.where(known & (entry >= 0), entry * page_size + pos % page_size, -1).to(torch.int32)
+    slot = entry * page_size + pos % page_size
+    return torch.where(known & (entry >= 0) & (slot < 2**31), slot, -1).to(torch.int32)
 
 
 def declare(lib):
