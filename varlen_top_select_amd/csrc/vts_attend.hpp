@@ -488,8 +488,8 @@ struct Attend {
         }
     }
     // What was cleared of V in units [u0, u1), in the wave's tiles or (BLOCK) in all, from
-    // memory to the rows that see it: rare, and apart from the walk, whose registers it
-    // would take.
+    // memory to the rows that see it (all of them, where it is of the prefix or the list, whose
+    // end such a tile holds): rare, and apart from the walk, whose registers it would take.
     __device__ __forceinline__ void add_cleared(int32_t u0, int32_t u1) {
         fresh();
         constexpr int SPAN = BLOCK ? S::PLACES : 32;
@@ -500,7 +500,6 @@ struct Attend {
 #pragma unroll 1
             for (int kk = 0; kk < SPAN; ++kk) {
                 const int32_t i = j0 + kk - pl.first;
-                if (i < 0) continue;
                 const Spot at = resolve_lookup<SLOTS>(p.c, issue_lookup<SLOTS>(p.c, pl, j0 + kk));
                 if (!at.there) continue;
                 const uint32_t off = spot_offset(at, p.c.v.page_stride, p.c.v.pos_stride);
@@ -528,7 +527,7 @@ struct Attend {
                     const u32x4 x = widen(w[0], w[1], scale);
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
-                        const bool see = (bits[mt] >> (i & 63)) & 1;
+                        const bool see = i < 0 || ((bits[mt] >> (i & 63)) & 1);
 #pragma unroll
                         for (int n = 0; n < NTILE; ++n) {
                             const uint32_t half = (x[n >> 1] >> (16 * (n & 1))) & 0xFFFFu;
@@ -541,9 +540,10 @@ struct Attend {
             }
         }
     }
-    // The same of one place's row, to the lane's elements 32 i + 8 n + 4 half ..
+    // The same of one place's row (place < 0: of the prefix or the list), to the lane's elements
+    // 32 i + 8 n + 4 half ..
     __device__ __forceinline__ void add_to_block(const uint8_t* codes, const VTS_GLOBAL char* row, int32_t place) {
-        const bool see = (bits[0] >> (place & 63)) & 1;
+        const bool see = place < 0 || ((bits[0] >> (place & 63)) & 1);
 #pragma unroll
         for (int i = 0; i < OB; ++i) {
             const float scale = scale_of(gload(codes + i));
