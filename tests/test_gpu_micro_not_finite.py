@@ -109,3 +109,22 @@ def test_values_of_listed_slots(draft, heads, kv, batch, top_k, tree, bits):
     assert got[0, :, :, 32:64].isnan().all() and got[1, :, :, 96:].isnan().all()
     got[0, :, :, 32:64], got[1, :, :, 96:] = clean[0, :, :, 32:64], clean[1, :, :, 96:]
     assert torch.equal(got, clean)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("heads", [2, 6])
+def test_infinities_of_places_that_part_of_a_workgroup_sees(heads, bits):
+    """Rows that see drafted tokens 32 and more alone, of which one is infinite: the waves of the first
+    32 places see nothing of those rows."""
+    draft = 40
+    gen = torch.Generator().manual_seed(911)
+    caches, scales, deep, table, n = make_cache(gen, [draft, draft], PAGE, 2, 128, bits)
+    q = (0.2 * torch.randn(2, draft, heads, 128, generator=gen)).half().to(DEV)
+    mask = torch.tensor([1 << t | (1 << 33 if t >= 32 else 0) for t in range(draft)]).expand(2, -1).contiguous().to(DEV)
+    clean, clean_lse = run(q, caches, scales, table, n, mask)
+    infinite(caches, scales, bits, 1, place(table, 1, 33), 2)
+    got, lse = run(q, caches, scales, table, n, mask)
+    assert torch.equal(lse, clean_lse)
+    assert (got[1, 32:, :, 64:96] == math.inf).all()
+    got[1, 32:, :, 64:96] = clean[1, 32:, :, 64:96]
+    assert torch.equal(got, clean)

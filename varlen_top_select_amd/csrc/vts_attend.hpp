@@ -487,16 +487,19 @@ struct Attend {
             }
         }
     }
-    // What was cleared of V in units [u0, u1), in the wave's tiles or (BLOCK) in all, from
-    // memory to the rows that see it (all of them, where it is of the prefix or the list, whose
-    // end such a tile holds): rare, and apart from the walk, whose registers it would take.
+    // What was cleared of V in the wave's tiles of units [u0, u1), from memory to the rows that
+    // see it (all of them, where it is of the prefix or the list, whose end such a tile holds):
+    // rare, and apart from the walk, whose registers it would take.  Each wave adds what its
+    // own places hold, for in the join its outputs meet those of waves that saw more or less
+    // of a row (0 * inf).
     __device__ __forceinline__ void add_cleared(int32_t u0, int32_t u1) {
         fresh();
-        constexpr int SPAN = BLOCK ? S::PLACES : 32;
+        constexpr int SPAN = BLOCK ? PB * 32 : 32;
 #pragma unroll 1
         for (int32_t u = u0; u < u1; ++u) {
-            const int32_t j0 = BLOCK ? u * SPAN : first_place(u);
-            if (j0 + SPAN - 1 < pl.first) continue;
+            const int32_t j0 = first_place(u);
+            // (a wide unit is cleared as a whole)
+            if ((BLOCK ? u * S::PLACES + S::PLACES : j0 + SPAN) <= pl.first) continue;
 #pragma unroll 1
             for (int kk = 0; kk < SPAN; ++kk) {
                 const int32_t i = j0 + kk - pl.first;
@@ -1037,8 +1040,7 @@ struct Attend {
             __syncthreads();
             if (cleared) sm.last = 1;
             __syncthreads();
-            // (the groups' outputs are added up: one of them does it)
-            if (sm.last && kg == 0) add_cleared(u0, u1);
+            if (sm.last) add_cleared(u0, u1);
             __syncthreads();
         }
     }
