@@ -108,6 +108,7 @@ struct Attend {
     // same time (8 trees of 16 up to 65536: 280 us for 433).
     static constexpr bool BLOCK = MICRO && S::WIDE;
     static constexpr int KB = D / 16, OB = D / 32;  // steps and tiles of its products
+    static constexpr int PB = BLOCK ? S::PLACES / 32 / S::KG : 1;  // 32 places of a wave in a unit
     static constexpr bool HEAD = MODE == HEADS, WIDE = S::WIDE;
     static constexpr int T = S::NW * 64;    // threads
     // whether a cache row is read once by the whole call, as far as it is known
@@ -169,6 +170,9 @@ struct Attend {
     const char* sbase;
     uint32_t scale_page, scale_pos;
     bool cleared;  // something that is not finite was taken out of a tile's V
+    // Which of the lane's probabilities are 0 or NaN, of the last tiles that hold drafted
+    // tokens, eight bits to a tile and the last one's low (three hold 64 tokens)
+    uint32_t none[MT];
 
     __device__ Attend(const AttendParams& p_, AttendShared<D, MT, MODE, F>& s_, int32_t mb_)
         : p(p_), sm(s_), mb(mb_) {
@@ -487,14 +491,44 @@ struct Attend {
             }
         }
     }
+    // Whether a probability as the products take it (0 or more) is 0 or NaN.
+    static __device__ __forceinline__ uint32_t weightless(uint32_t half) {
+        return half - 1u >= (DT == BF16 ? 0x7F80u : 0x7C00u) ? 1 : 0;
+    }
+    // the same of a tile's eight, as bits
+    static __device__ __forceinline__ uint32_t weightless_of(u32x4 pv) {
+        uint32_t x = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x |= weightless(e & 1 ? pv[e / 2] >> 16 : pv[e / 2] & 0xFFFFu) << e;
+        return x;
+    }
+    // (BLOCK) The same of 32 places of a unit, sixteen bits, their scores computed again: the K
+    // rows of the walk's last two units, which hold all drafted tokens, are still in LDS.
+    __device__ __forceinline__ uint32_t weightless_block(int32_t u, int b) const {
+        f32x16 s;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[e] = 0;
+        const int r = (kg + b) * 32 + bcol;
+#pragma unroll
+        for (int ks = 0; ks < KB; ++ks)
+            s = mfma32<DT>(sm.w.k[u & 1][r * CH + ((2 * ks + half) ^ swizzled<D>(r))], q[ks], s);
+        const float base = m[0] == NEG_INF ? 0.0f : m[0];
+        uint32_t x = 0;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            x |= weightless(pack2<DT>(__builtin_amdgcn_exp2f(fmaf(s[e], p.scale_log2e, -base)), 0.0f) & 0xFFFFu) << e;
+        return x;
+    }
     // What was cleared of V in the wave's tiles of units [u0, u1), from memory to the rows that
     // see it (all of them, where it is of the prefix or the list, whose end such a tile holds):
     // rare, and apart from the walk, whose registers it would take.  Each wave adds what its
     // own places hold, for in the join its outputs meet those of waves that saw more or less
-    // of a row (0 * inf).
+    // of a row (0 * inf).  An infinity of any weight is the infinity; of none (a score of
+    // -inf) it is NaN, as the products of other tiles give it.
     __device__ __forceinline__ void add_cleared(int32_t u0, int32_t u1) {
         fresh();
         constexpr int SPAN = BLOCK ? PB * 32 : 32;
+        uint32_t of_block = 0;
 #pragma unroll 1
         for (int32_t u = u0; u < u1; ++u) {
             const int32_t j0 = first_place(u);
@@ -502,6 +536,8 @@ struct Attend {
             if ((BLOCK ? u * S::PLACES + S::PLACES : j0 + SPAN) <= pl.first) continue;
 #pragma unroll 1
             for (int kk = 0; kk < SPAN; ++kk) {
+                if constexpr (BLOCK)
+                    if ((kk & 31) == 0) of_block = weightless_block(u, kk >> 5);
                 const int32_t i = j0 + kk - pl.first;
                 const Spot at = resolve_lookup<SLOTS>(p.c, issue_lookup<SLOTS>(p.c, pl, j0 + kk));
                 if (!at.there) continue;
@@ -511,9 +547,14 @@ struct Attend {
                 const uint8_t* codes = p.v_scale.base + ((uint64_t)soff + (uint64_t)h * p.v_scale.head_stride) * BLOCKS;
                 const VTS_GLOBAL char* row = (const VTS_GLOBAL char*)vbase + ((uint64_t)off << 4);
                 if constexpr (BLOCK) {
-                    add_to_block(codes, row, i);
+                    const uint32_t n = from_lane(of_block, (kk >> 2 & 1) * 32 + bcol);
+                    add_to_block(codes, row, i, n >> ((kk >> 3 & 3) * 4 + (kk & 3)) & 1);
                     continue;
                 }
+                const int src = ((kk & 15) >> 2) * 16 + col, bit = 8 * (u1 - 1 - u) + (kk >> 4) * 4 + (kk & 3);
+                uint32_t weighs_nothing[MT];
+#pragma unroll
+                for (int mt = 0; mt < (BLOCK ? 0 : MT); ++mt) weighs_nothing[mt] = from_lane(none[mt], src) >> bit & 1;
 #pragma unroll
                 for (int e4 = 0; e4 < (BLOCK ? 0 : 4); ++e4) {
                     constexpr int B = RB / 16;
@@ -534,7 +575,7 @@ struct Attend {
 #pragma unroll
                         for (int n = 0; n < NTILE; ++n) {
                             const uint32_t half = (x[n >> 1] >> (16 * (n & 1))) & 0xFFFFu;
-                            const float y = o[mt][n][e4] + to_float<DT>(half);
+                            const float y = o[mt][n][e4] + (weighs_nothing[mt] ? NOT_A_NUMBER : to_float<DT>(half));
                             o[mt][n][e4] = see && not_finite<DT>(half) ? y : o[mt][n][e4];
                         }
                     }
@@ -545,7 +586,8 @@ struct Attend {
     }
     // The same of one place's row (place < 0: of the prefix or the list), to the lane's elements
     // 32 i + 8 n + 4 half ..
-    __device__ __forceinline__ void add_to_block(const uint8_t* codes, const VTS_GLOBAL char* row, int32_t place) {
+    __device__ __forceinline__ void add_to_block(const uint8_t* codes, const VTS_GLOBAL char* row, int32_t place,
+                                                 bool weighs_nothing) {
         const bool see = place < 0 || ((bits[0] >> (place & 63)) & 1);
 #pragma unroll
         for (int i = 0; i < OB; ++i) {
@@ -561,7 +603,7 @@ struct Attend {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const uint32_t one = (x[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
-                    const float y = ob[i][4 * n + e] + to_float<DT>(one);
+                    const float y = ob[i][4 * n + e] + (weighs_nothing ? NOT_A_NUMBER : to_float<DT>(one));
                     ob[i][4 * n + e] = see && not_finite<DT>(one) ? y : ob[i][4 * n + e];
                 }
                 __builtin_amdgcn_sched_barrier(0);
@@ -570,7 +612,6 @@ struct Attend {
     }
 
     // A wave's 32 rows and its places of a unit, 32 or all 64: as tile(), in blocks.
-    static constexpr int PB = BLOCK ? S::PLACES / 32 / S::KG : 1;
     __device__ __forceinline__ void tile_block(const uint32_t (&have)[PB], bool masked, int32_t j0, int buf) {
         const float c = p.scale_log2e;
         f32x16 s[PB];
@@ -902,6 +943,10 @@ struct Attend {
             for (int j = 0; j < 8; ++j) v[j] = wide_v(buf, v_place(j), col);
         uint32_t bad = 0;
         if constexpr (PERMUTED) {
+            if (drafted) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) none[mt] = none[mt] << 8 | weightless_of(pv[mt]);
+            }
             micro_product(have, masked, drafted, pv);
         } else if (masked) {
             int g = grp;
@@ -973,6 +1018,8 @@ struct Attend {
     // The same over a microscaled cache, AHEAD tiles on their way.
     __device__ __forceinline__ void walk_micro(int32_t u0, int32_t u1) {
         cleared = false;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) none[mt] = 0;
         scale_page = lane < 32 ? p.k_scale.page_stride : p.v_scale.page_stride;
         scale_pos = lane < 32 ? p.k_scale.pos_stride : p.v_scale.pos_stride;
         const auto look = [&](int32_t u) { return issue_lookup<SLOTS>(p.c, pl, first_place(u) + (lane & 31)); };
@@ -1534,9 +1581,12 @@ __global__ __launch_bounds__(threads_of(MODE, F), MODE >= WIDE2 || F != 16 ? 2 :
         if (x == g0 && x1 == g1) {
             a.finish_whole();
         } else {
-            const int32_t w0 = share_of(sh.total, sh.workers, g0);
-            const int32_t w1 = share_of(sh.total, sh.workers, g1 - 1);
-            const bool whole_start = share_start(sh.total, sh.workers, w0) == g0;
+            // (opaque: its reciprocal is not kept in a register from the shares above to here)
+            int32_t workers = sh.workers;
+            if constexpr (F != 16) asm volatile("" : "+s"(workers));
+            const int32_t w0 = share_of(sh.total, workers, g0);
+            const int32_t w1 = share_of(sh.total, workers, g1 - 1);
+            const bool whole_start = share_start(sh.total, workers, w0) == g0;
             a.finish_part(a.part(w, w0, whole_start), w0, w1, whole_start);
         }
         x = x1;
