@@ -491,15 +491,11 @@ struct Attend {
             }
         }
     }
-    // Whether a probability as the products take it (0 or more) is 0 or NaN.
-    static __device__ __forceinline__ uint32_t weightless(uint32_t half) {
-        return half - 1u >= (DT == BF16 ? 0x7F80u : 0x7C00u) ? 1 : 0;
-    }
-    // the same of a tile's eight, as bits
+    // weightless of a tile's eight, as bits
     static __device__ __forceinline__ uint32_t weightless_of(u32x4 pv) {
         uint32_t x = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x |= weightless(e & 1 ? pv[e / 2] >> 16 : pv[e / 2] & 0xFFFFu) << e;
+        for (int e = 0; e < 8; ++e) x |= weightless<DT>(e & 1 ? pv[e / 2] >> 16 : pv[e / 2] & 0xFFFFu) << e;
         return x;
     }
     // (BLOCK) The same of 32 places of a unit, sixteen bits, their scores computed again: the K
@@ -516,7 +512,7 @@ struct Attend {
         uint32_t x = 0;
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-            x |= weightless(pack2<DT>(__builtin_amdgcn_exp2f(fmaf(s[e], p.scale_log2e, -base)), 0.0f) & 0xFFFFu) << e;
+            x |= weightless<DT>(pack2<DT>(__builtin_amdgcn_exp2f(fmaf(s[e], p.scale_log2e, -base)), 0.0f) & 0xFFFFu) << e;
         return x;
     }
     // What was cleared of V in the wave's tiles of units [u0, u1), from memory to the rows that

@@ -137,6 +137,12 @@ __device__ __forceinline__ uint32_t finite_part(uint32_t pair) {
            (not_finite<DT>(pair >> 16) ? 0 : pair & 0xFFFF0000u);
 }
 
+// Whether a probability as the products take it (0 or more) is 0 or NaN.
+template <int DT>
+__device__ __forceinline__ uint32_t weightless(uint32_t half) {
+    return half - 1u >= (DT == BF16 ? 0x7F80u : 0x7C00u) ? 1 : 0;
+}
+
 // One request's (or, with slot lists, one row's) positions: a list of `count`
 // places, those from `first` on being the drafted tokens.
 struct Places {

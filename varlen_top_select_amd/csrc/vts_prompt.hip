@@ -28,7 +28,7 @@ constexpr int PROMPT_KEYS = 64;  // of a tile
 template <int D>
 struct PromptShared {
     u32x4 k[2][PROMPT_KEYS * (D / 8)], v[2][PROMPT_KEYS * (D / 8)];
-    uint32_t bad;  // a masked tile's V holds something that is not finite
+    int32_t bad[2];  // 1 + the first key of the last tile there whose V held something not finite
 };
 
 // A workgroup's tile: its sequence, the first of its rows, and the lengths.
@@ -227,9 +227,9 @@ struct Prompt {
 
     // Where not every row sees every key, an infinity or NaN in V would reach rows that
     // do not see it (0 * inf).  Such a tile's are cleared on the way to LDS, and what rows
-    // see of them is added at the end, from memory: rare, and kept apart from the loops,
-    // whose registers it would take (45 spilled).
-    __device__ __forceinline__ void clear_not_finite() {
+    // see of them is added after the tile's products, from memory: rare, and kept apart from
+    // the tile on its way, whose registers it would take (45 spilled): that is loaded again.
+    __device__ __forceinline__ void clear_not_finite(int32_t j0, int buf) {
         bool f = false;
 #pragma unroll
         for (int i = 0; i < LOADS; ++i)
@@ -239,13 +239,36 @@ struct Prompt {
                 f = f || not_finite<DT>(w);
                 vr[i][e] = finite_part<DT>(w);
             }
-        if (f) sm.bad = 1;
+        if (f) sm.bad[buf] = j0 + 1;
     }
-    __device__ __forceinline__ void add_not_finite(int32_t j0, int32_t end) {
+    // Which of the lane's probabilities of 32 keys in half `buf` are 0 or NaN: sixteen bits, their
+    // scores computed again.
+    __device__ __forceinline__ uint32_t weightless_block(int buf, int b) const {
+        f32x16 s;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[e] = 0;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+            s = mfma32<DT>(sm.k[buf][k_at(32 * b + col, 2 * ks + half)], q[ks], s);
+        const float base = m == NEG_INF ? 0.0f : m;
+        uint32_t x = 0;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            x |= weightless<DT>(pack2<DT>(__builtin_amdgcn_exp2f(fmaf(s[e], p.scale_log2e, -base)), 0.0f) & 0xFFFFu) << e;
+        return x;
+    }
+    // An infinity of any weight is the infinity; of none (a score of -inf) it is NaN, as the
+    // products of other tiles give it.
+    __device__ __forceinline__ void add_not_finite(int32_t j0, int32_t end, int buf) {
+        uint32_t none = 0;
 #pragma unroll 1
         for (int32_t j = j0; j < end; ++j) {
+            const int kk = j - j0;
+            if ((kk & 31) == 0) none = weightless_block(buf, kk >> 5);
             const char* at = (const char*)p.v + 2 * ((int64_t)(t.k0 + j) * p.v_token + kv * p.v_head);
             const bool see = j <= limit;
+            const int bit = (kk >> 3 & 3) * 4 + (kk & 3);
+            const bool weighs_nothing = from_lane(none, (kk >> 2 & 1) * 32 + col) >> bit & 1;
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -254,7 +277,7 @@ struct Prompt {
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         const uint32_t raw = (four[x >> 1] >> (16 * (x & 1))) & 0xFFFFu;
-                        const float y = o[i][e + x] + to_float<DT>(raw);
+                        const float y = o[i][e + x] + (weighs_nothing ? NOT_A_NUMBER : to_float<DT>(raw));
                         o[i][e + x] = see && not_finite<DT>(raw) ? y : o[i][e + x];
                     }
                 }
@@ -318,7 +341,7 @@ struct Prompt {
     }
     // the tile at j0 to LDS, and the next one on its way
     __device__ __forceinline__ void next(int32_t j0, int32_t end, int buf) {
-        clear_not_finite();
+        clear_not_finite(j0, buf);
         // the other half may still be read; this one was done with before the last barrier
         stage(buf);
         if (j0 + PROMPT_KEYS < end) load(j0 + PROMPT_KEYS);
@@ -340,7 +363,7 @@ struct Prompt {
             if (to < all) all = to;
         }
         if (j0 < end) {
-            if (tid == 0) sm.bad = 0;
+            if (tid < 2) sm.bad[tid] = 0;
             int buf = 0;
             if (p.direct && j0 + PROMPT_KEYS <= all) {
                 load_direct(j0, 0);
@@ -354,22 +377,24 @@ struct Prompt {
                     tile<false>(j0, buf);
                 }
             }
-            const int32_t first = j0;
             if (j0 < end) load(j0);
             __syncthreads();
 #pragma unroll 1
             for (; j0 < end; j0 += PROMPT_KEYS, buf ^= 1) {
                 next(j0, end, buf);
                 tile<true>(j0, buf);
+                if (sm.bad[buf] == j0 + 1) {
+                    add_not_finite(j0, j0 + PROMPT_KEYS < end ? j0 + PROMPT_KEYS : end, buf);
+                    if (j0 + PROMPT_KEYS < end) load(j0 + PROMPT_KEYS);
+                }
             }
-            __syncthreads();
-            if (sm.bad) add_not_finite(first, end);
         }
     }
 };
 
+// (Heads of 64: three workgroups to a compute unit, packed prompts 342 us for 375 with two.)
 template <int DT, int D>
-__global__ __launch_bounds__(PROMPT_NT, 2) void prompt_kernel(PromptParams p) {
+__global__ __launch_bounds__(PROMPT_NT, D == 64 ? 3 : 2) void prompt_kernel(PromptParams p) {
     __shared__ PromptShared<D> sm;
     const int32_t work = p.tiles * p.kv_heads * p.splits;
     if ((int32_t)blockIdx.x >= work) {
