@@ -217,6 +217,7 @@ int vts_prompt_attention(const vts_prompts* a, int32_t causal, float scale, void
     if (plan.tiles * a->kv_heads > (1 << 24) - 64) return VTS_ERR_UNSUPPORTED;
     if (plan.total > 0 && (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < plan.total))
         return VTS_ERR_WORKSPACE;
+    if (a->batch == 0 && !clear) return VTS_OK;  // (a grid may not be empty)
     st = check_device(stream);
     if (st != VTS_OK) return st;
     p.q = a->q;
