@@ -670,7 +670,7 @@ int vts_read_cache(const vts_paged_cache* cache, const vts_microscales* scales, 
  *            contexts take any).
  *
  * total_q * heads, total_k and batch are below 2^31 - 1024, and kv_heads *
- * (total_q * (heads / kv_heads) / 128 + batch) is at most 2^24 - 64.
+ * (total_q * (heads / kv_heads) / 128 + batch) below 2^24 - 64.
  */
 typedef struct {
     const void* q;

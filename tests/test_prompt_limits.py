@@ -13,3 +13,16 @@ def call(lib, clear, **kw):  # noqa: F811
 def test_no_sequence(lib, kw):  # noqa: F811
     """A batch of none leaves all rows as they are: nothing is started, be there a tile's rows or fewer."""
     assert call(lib, 0, batch=0, **kw) == OK
+
+
+@pytest.mark.skipif(not NO_GPU, reason="pointers to nothing")
+@pytest.mark.parametrize("over", [0, 1])
+def test_the_largest_grid(lib, over):  # noqa: F811
+    """tiles * kv_heads below 2^24 - 64: with the 64 workgroups for rows of no sequence a grid of 256
+    threads each stays below 2^32."""
+    batch = 2 ** 23 - 65 + over  # and 2^23 full tiles of 128 rows
+    got = call(lib, 1, heads=1, kv=1, qs=(128, 128), ks=(128, 128), vs=(128, 128), tq=2 ** 30, tk=100, batch=batch)
+    if over:
+        assert got == UNSUPPORTED
+    else:  # (as far as the device, which is not there)
+        assert got == HIP

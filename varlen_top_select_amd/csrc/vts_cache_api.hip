@@ -213,8 +213,8 @@ int vts_prompt_attention(const vts_prompts* a, int32_t causal, float scale, void
     if (lse && (!aligned(lse, 4) || overlap(out, rows * a->head_dim * 2, lse, rows * 4))) return VTS_ERR_INVALID;
     p.group = a->heads / a->kv_heads;
     const PromptPlan plan = prompt_plan(a->batch, a->total_q, a->total_k, a->heads, a->kv_heads, a->head_dim);
-    // (a grid has below 2^32 threads)
-    if (plan.tiles * a->kv_heads > (1 << 24) - 64) return VTS_ERR_UNSUPPORTED;
+    // (a grid has below 2^32 threads, and with `clear` 64 workgroups more)
+    if (plan.tiles * a->kv_heads >= (1 << 24) - 64) return VTS_ERR_UNSUPPORTED;
     if (plan.total > 0 && (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < plan.total))
         return VTS_ERR_WORKSPACE;
     if (a->batch == 0 && !clear) return VTS_OK;  // (a grid may not be empty)
