@@ -233,7 +233,10 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
 
     def call(sp):
         o = q.new_empty((total_q, heads, head_dim)) if out is None else out
-        lse = q.new_empty((total_q, heads), dtype=torch.float32) if return_lse else None
+        lse = None
+        if return_lse:  # (beside outputs that are left as they were, rows of no sequence are not written)
+            lse = (q.new_empty((total_q, heads), dtype=torch.float32) if out is None
+                   else q.new_full((total_q, heads), -math.inf, dtype=torch.float32))
         # (of any contents, so it is the call's own, also in a captured graph)
         ws = q.new_empty(need, dtype=torch.uint8) if need else None
         _check("vts_prompt_attention", lib.vts_prompt_attention(
