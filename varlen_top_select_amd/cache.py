@@ -271,8 +271,10 @@ def page_slots(page_table: torch.Tensor, page_size: int, positions: torch.Tensor
     page = torch.div(pos, page_size, rounding_mode="floor")
     known = (pos >= 0) & (page < page_table.shape[1])
     entry = page_table.long().gather(1, torch.where(known, page, 0))
+    # (an entry whose slots all pass 32 bits may wrap in the product)
+    known = known & (entry >= 0) & (entry <= (2**31 - 1) // page_size)
     slot = entry * page_size + pos % page_size
-    return torch.where(known & (entry >= 0) & (slot < 2**31), slot, -1).to(torch.int32)
+    return torch.where(known & (slot < 2**31), slot, -1).to(torch.int32)
 
 
 def declare(lib):
