@@ -33,10 +33,10 @@ FLAGS = [
 # unit (every row of a 1024-row batch resident at once) and must not spill:
 # the compiler's resource remarks are checked on every build.
 MIN_WAVES_PER_SIMD = 4
-# The decode-step kernels must not spill either: a spill's load waits for every
+# The others must not spill either: a spill's load waits for every
 # cache row on its way.
-NO_SCRATCH = ("topk_kernel", "attend_kernel", "weigh_kernel", "evict_", "verify_", "write_kernel",
-              "read_kernel", "prompt_kernel")
+NO_SCRATCH = ("topk_kernel", "row_batch_kernel", "zero_kernel", "attend_kernel", "weigh_kernel", "evict_",
+              "verify_", "write_kernel", "read_kernel", "prompt_kernel", "prompt_join_kernel")
 
 
 def _check_resources(remarks: str, out: str) -> None:
