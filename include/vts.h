@@ -584,8 +584,8 @@ int vts_tree_attention_microscaled(const vts_paged_cache* cache, const vts_micro
  * A slot outside the cache (-1 for padding) is not written; the token's q_out and
  * k_out are.  A token whose position is outside [0, max_position) gets zeros in q_out
  * and k_out and is not written.  The slots inside the cache have to be distinct: the
- * entry of one named twice holds parts of either token.  Nothing else of the cache
- * changes.  page_table, seq_lens and batch of `cache` are not looked at.
+ * entry of one named twice holds parts of either token.  So do rows of the caches, and
+ * of their scales, that overlap each other.  Nothing else of the cache changes.  page_table, seq_lens and batch of `cache` are not looked at.
  *
  * q, k, v    device, the cache's dtype, 16-byte aligned rows of head_dim elements;
  *            strides: elements between tokens and heads, multiples of 8.

@@ -91,6 +91,19 @@ def _apart(name, out, *others):
         raise ValueError(f"{name} must not overlap the inputs or the caches")
 
 
+def _own_rows(*pairs):
+    """That the rows written of each pair of caches (or scales) are apart, as far as their addresses and
+    steps of 0 tell: two threads would write one of them in any order."""
+    for k, v in pairs:
+        if k is None:
+            continue
+        if k.numel() and k.data_ptr() == v.data_ptr():
+            raise ValueError("k_cache and v_cache, or their scales, must not overlap where they are written")
+        for t in (k, v):
+            if 0 in t.stride() and any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
+                raise ValueError("k_cache, v_cache and their scales must not overlap themselves where they are written")
+
+
 def write_cache(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
                 k_cache: torch.Tensor, v_cache: torch.Tensor, *, k_scales: torch.Tensor | None = None,
                 v_scales: torch.Tensor | None = None, positions: torch.Tensor | None = None,
@@ -101,13 +114,14 @@ def write_cache(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slots: torch.
     (``q_norm``, ``k_norm``: weights [head_dim], either or none), turns them by the angles of
     ``positions`` (int32 [tokens]) in ``rotary`` (float32 [max_position, rot], cosines then
     sines; pairs (i, i + rot / 2), or neighbours if ``interleaved``), and writes k and v to the
-    ``slots`` (int32 [tokens]) of the caches (vts_write_cache in include/vts.h).  A slot outside the
-    cache is not written; the others must be distinct.  A token whose position is outside the
+    ``slots`` (int32 [tokens]) of the caches (vts_write_cache in include/vts.h), whose rows must not
+    overlap each other's.  A slot outside the cache is not written; the others must be distinct.  A token whose position is outside the
     table is not written and gets zeros.  Returns the queries, in ``q_out`` if given, and with
     ``return_k`` the keys as they are before they are cut to the cache's bits, else None."""
     if not isinstance(q, torch.Tensor):
         raise ValueError("q must be a 3-D tensor [tokens, heads, head_dim]")
     cache, scales, index, dtype, kv_heads, head_dim = _slot_cache(k_cache, v_cache, k_scales, v_scales, q.dtype)
+    _own_rows((k_cache, v_cache), (k_scales, v_scales))
     (tokens, heads, dim), qs = _heads("q", q, dtype, index)
     if dim != head_dim:
         raise ValueError("q must have the cache's head_dim")
