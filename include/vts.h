@@ -407,7 +407,8 @@ typedef struct {
  * cache, such as the -1 of unused entries, are skipped) and, if tree_mask is
  * given, the drafted tokens it names.  A row that sees nothing, or nothing of
  * weight, gets zeros and an lse of -inf.  Values in places that a row does not
- * see never reach it, infinities and NaN among them.
+ * see never reach it, infinities and NaN among them; in those that it sees they
+ * count as the weight says, so that with a score of -inf they give NaN.
  *
  * q          device, the cache's dtype, 16-byte aligned; q_strides: elements
  *            between requests, drafted tokens and heads, multiples of 8.
@@ -536,7 +537,10 @@ int vts_verify_draft(const void* target_probs, int32_t dtype, int64_t target_bat
  * mantissa; 0x7F and 0xFF are NaN) or E2M1 (bits 4: 0, 0.5, 1, 1.5, 2, 3, 4, 6 with a
  * sign, the first of two in a byte's low half).  A scale is one byte, E8M0: 2^(x - 127), NaN
  * for 255.  Values are rounded to the queries' dtype where they are used: bf16 holds
- * every number of the format down to 2^-133, fp16 those of its own range.
+ * every number of the format from 2^-133 to its own largest, fp16 those of its own
+ * range, and what lies past it is an infinity.  So are values next to the dtype's
+ * largest that the format rounds up to the next power of two: written with 4 bits from
+ * 1.75 times its largest power of two on (57344 in fp16), with 8 from 1.9375 (63488).
  *
  * k, v       device: head_dim / 32 bytes per row, aligned to that.
  * k_strides, v_strides  bytes between pages, positions of a page, and heads,
@@ -552,7 +556,7 @@ typedef struct {
 
 /*
  * vts_tree_attention_microscaled -- vts_tree_attention over a microscaled cache,
- * with the same arguments, masks and guarantees; the workspace serves caches of
+ * with the same arguments, masks, sums and guarantees; the workspace serves caches of
  * 8 and of 4 bits.
  */
 size_t vts_tree_attention_microscaled_workspace_bytes(int32_t batch, int32_t draft, int32_t heads,
@@ -651,12 +655,16 @@ int vts_read_cache(const vts_paged_cache* cache, const vts_microscales* scales, 
  * its keys, so of nq queries and nk keys query i sees the keys j <= i + nk - nq; else
  * all.  A row that sees nothing, or nothing of weight, gets zeros and an lse of
  * -inf.  Values of keys that a row does not see never reach it, infinities and NaN
- * among them.  Rows of no sequence (before cu_q[0], from cu_q[batch] on) are left as
+ * among them; of keys that it sees they count as the weight says, so that with a score
+ * of -inf they give NaN (0 times infinity).  Rows of no sequence (before cu_q[0], from cu_q[batch] on) are left as
  * they were, or with `clear` get zeros and -inf.
  *
  * Entries of cu_q and cu_k are clamped to the rows there are; one below its
  * predecessor makes an empty sequence, after which what later sequences' rows get is
  * not defined (nothing outside the outputs is touched).
+ *
+ * Scores, maxima, sums and outputs are 32-bit; the probabilities are rounded to dtype
+ * for the product with V, as in vts_tree_attention, and the sum takes them unrounded.
  *
  * q, k, v    device, dtype (VTS_BF16 or VTS_F16), 16-byte aligned rows of head_dim
  *            (64 or 128) elements, total_q of heads, total_k of kv_heads; strides:

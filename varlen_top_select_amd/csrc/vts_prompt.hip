@@ -12,7 +12,10 @@
 // as A and query rows as B of the 32x32x16 product, lane l gets scores of row l % 32
 // at keys 8 * (e / 4) + 4 * (l / 32) + e % 4: its sixteen probabilities are already
 // its B operands of the second product, with V's keys taken in the same order by
-// transposing LDS loads.  m is raised only when a score passes it by a margin.
+// transposing LDS loads.  m is raised only when a score passes it by a margin, and p is
+// rounded to the type of V for the second product, whose operands it takes (at most half
+// a step, 2^-8 of a bf16 p and 2^-11 of an fp16 one, which average out over the keys; the
+// margins are those of vts_attend.hpp); l sums the unrounded p, and all else is 32-bit.
 //
 // Where there are few tiles and long contexts, several workgroups take parts of a tile's
 // keys, and a second kernel joins them.
