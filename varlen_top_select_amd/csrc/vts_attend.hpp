@@ -1577,9 +1577,10 @@ __global__ __launch_bounds__(threads_of(MODE, F), MODE >= WIDE2 || F != 16 ? 2 :
         if (x == g0 && x1 == g1) {
             a.finish_whole();
         } else {
-            // (opaque: its reciprocal is not kept in a register from the shares above to here)
+            // (opaque: its reciprocal is not kept from the shares above to here, in the one form that
+            // has no register left for it; dividing anew takes 1.7 us)
             int32_t workers = sh.workers;
-            if constexpr (F != 16) asm volatile("" : "+s"(workers));
+            if constexpr (F != 16 && SLOTS && MODE == WIDE4) asm volatile("" : "+s"(workers));
             const int32_t w0 = share_of(sh.total, workers, g0);
             const int32_t w1 = share_of(sh.total, workers, g1 - 1);
             const bool whole_start = share_start(sh.total, workers, w0) == g0;
