@@ -408,7 +408,8 @@ typedef struct {
  * given, the drafted tokens it names.  A row that sees nothing, or nothing of
  * weight, gets zeros and an lse of -inf.  Values in places that a row does not
  * see never reach it, infinities and NaN among them; in those that it sees they
- * count as the weight says, so that with a score of -inf they give NaN.
+ * count as the weight says, so that with a score of -inf they give NaN.  A row with
+ * a score that is NaN or +inf gets NaN, its lse too.
  *
  * q          device, the cache's dtype, 16-byte aligned; q_strides: elements
  *            between requests, drafted tokens and heads, multiples of 8.
@@ -656,7 +657,8 @@ int vts_read_cache(const vts_paged_cache* cache, const vts_microscales* scales, 
  * all.  A row that sees nothing, or nothing of weight, gets zeros and an lse of
  * -inf.  Values of keys that a row does not see never reach it, infinities and NaN
  * among them; of keys that it sees they count as the weight says, so that with a score
- * of -inf they give NaN (0 times infinity).  Rows of no sequence (before cu_q[0], from cu_q[batch] on) are left as
+ * of -inf they give NaN (0 times infinity).  A row with a score that is NaN or +inf gets
+ * NaN, its lse too.  Rows of no sequence (before cu_q[0], from cu_q[batch] on) are left as
  * they were, or with `clear` get zeros and -inf.
  *
  * Entries of cu_q and cu_k are clamped to the rows there are; one below its

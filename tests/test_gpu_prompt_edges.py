@@ -50,3 +50,21 @@ def test_new_lse_beside_given_outputs():
         assert torch.equal(lse, want_lse)
         assert torch.equal(got[10:80], want[10:80] if len(cu) > 1 else torch.full_like(want[10:80], 3.0))
         assert (got[:10] == 3).all() and (got[80:] == 3).all()
+
+
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+@pytest.mark.parametrize("front", [0, 3000])
+def test_scores_that_are_not_finite(bad, front):
+    """A row that sees a score of +inf or NaN gets NaN, its lse too; the rows before it do not."""
+    gen = torch.Generator().manual_seed(932)
+    n = 100 if front == 0 else 8
+    q = torch.randn(n, 2, 64, generator=gen).bfloat16()
+    q[..., 3] = q[..., 3].abs() + 0.01
+    k, v = (torch.randn(front + n, 2, 64, generator=gen).bfloat16() for _ in "kv")
+    at = n - 4
+    k[front + at, 0, 3] = bad
+    cu = [torch.tensor([0, x], dtype=torch.int32, device=DEV) for x in (n, front + n)]
+    out, lse = vts.prompt_attention(q.to(DEV), k.to(DEV), v.to(DEV), cu[0], cu_seqlens_k=cu[1], return_lse=True)
+    assert out[at:, 0].isnan().all() and lse[at:, 0].isnan().all()
+    assert out[:at].isfinite().all() and lse[:at].isfinite().all()
+    assert out[:, 1].isfinite().all() and lse[:, 1].isfinite().all()
